@@ -19,6 +19,14 @@
  *   5. main-KV entry build: m=2 per-channel softmax of two tokens (m=1:
  *      weight 1), RMSNorm, RoPE on the last 64 dims, FP4  -> csa2_compress_m2
  *
+ * and what a step takes as its inputs (no counterpart in the pages):
+ *
+ *   6. hidden states or weights to e4m3 codes with a scale per 128 -> csa2_quant_fp8
+ *   7. projections on those codes: C and Z, the indexer query (codes and
+ *      scales), the attention query (with RoPE)             -> csa2_fp8_linear
+ *   8. rows, page table, entry and SWA slots of a batch, from the lengths of
+ *      its sequences                                        -> csa2_batch_plan
+ *
  * Conventions shared by every call
  *   - All pointers in the argument structs are DEVICE pointers to
  *     caller-owned memory (except the struct itself, which lives on the host
@@ -361,6 +369,121 @@ typedef struct {
   uint16_t* out;               /* [T, 512] bf16 */
 } csa2_kv_project_args;
 CSA2_API int csa2_kv_project(const csa2_kv_project_args* args, void* stream);
+
+/* ---- 6. e4m3 codes with a scale per 128 --------------------------------------
+ * The format of the indexer query: a fp32 scale for each block of 128 columns
+ * of a row (block_rows = 1: activations), or for each tile of 128 rows x 128
+ * columns (block_rows = 128: weights).  The last block of a row, and the last
+ * rows of a matrix, may be short.
+ *   y = x, or with gamma (block_rows = 1 only) x / sqrt(mean(x^2) + eps) * gamma
+ *   a = the largest |y| of the block's finite values, raised to 448 * 2^-120
+ *   scale = a / 448 (1 for a block without a finite value other than 0)
+ *   code  = e4m3 round-to-nearest-even of y * (448 / a), saturating at 448;
+ *           an infinity or NaN becomes the NaN code 0x7F (its own element only)
+ * The row's sum of squares is held in fp32.  K is a multiple of 16, at most
+ * 16384.  Alignment: x, codes, gamma 16 B; ld_x a multiple of 8 and ld_codes of
+ * 16.  codes must not overlap x.  No workspace. */
+typedef struct {
+  const uint16_t* x; int64_t ld_x;             /* [T, K] bf16, row stride ld_x >= K */
+  int32_t T, K;
+  int32_t block_rows;                          /* 1 or 128 */
+  const float* gamma; float eps;               /* optional [K] */
+  uint8_t* codes; int64_t ld_codes;            /* [T, K], row stride ld_codes >= K */
+  float* scale; int64_t ld_scale;              /* [ceil(T / block_rows), ceil(K / 128)] */
+} csa2_quant_fp8_args;
+CSA2_API int csa2_quant_fp8(const csa2_quant_fp8_args* args, void* stream);
+
+/* ---- 7. projection on e4m3 codes with a scale per block of 128 ---------------
+ *   y[t][n] = sum_b x_scale[t][b] * w_scale[n / 128][b] * sum_{k in block b} x[t][k] * w[n][k]
+ * x and its scales as csa2_quant_fp8 writes them with block_rows = 1, w (row =
+ * output column) and its scales with block_rows = 128; products and sums are
+ * held in fp32 and rounded once, to the output's type.
+ * RoPE (rope_head != 0): the columns form heads of rope_head columns (a
+ * multiple of 128 that divides N); the last 64 of each head are turned in
+ * interleaved pairs (D-64+2p, D-63+2p) by row_pos[t] * rope_theta^(-2p/64), the
+ * rotation of the keys (csa2_compress_m2), before the rounding.
+ * Output: fp32, bf16, or (CSA2_OUT_FP8, N a multiple of 128) e4m3 codes with a
+ * scale for each 128 columns by the rule of csa2_quant_fp8: with N = 32 * 128
+ * the query that csa2_index_score and csa2_reindex take.
+ * Rows t < T and columns n < N are written and nothing else.  K is a multiple
+ * of 16, at most 65536.  Alignment: x, w, out 16 B; ld_x and ld_w multiples of
+ * 16; row_pos, scales 4 B; for CSA2_OUT_FP8 ld_out a multiple of 16.  out must
+ * not overlap an input.  No workspace; results do not depend on the launch's
+ * timing (no atomics). */
+enum { CSA2_OUT_F32 = 0, CSA2_OUT_BF16 = 1, CSA2_OUT_FP8 = 2 };
+typedef struct {
+  const uint8_t* x; int64_t ld_x;              /* [T, K] e4m3 codes, row stride ld_x >= K */
+  const float* x_scale; int64_t ld_x_scale;    /* [T, ceil(K / 128)] */
+  const uint8_t* w; int64_t ld_w;              /* [N, K] e4m3 codes, row stride ld_w >= K */
+  const float* w_scale; int64_t ld_w_scale;    /* [ceil(N / 128), ceil(K / 128)] */
+  int32_t T, N, K;
+  int32_t out_format;                          /* CSA2_OUT_F32, CSA2_OUT_BF16 or CSA2_OUT_FP8 */
+  void* out; int64_t ld_out;                   /* [T, N], row stride ld_out >= N elements */
+  float* out_scale; int64_t ld_out_scale;      /* [T, N / 128] with CSA2_OUT_FP8 */
+  const int32_t* row_pos;                      /* [T] positions, with rope_head */
+  int32_t rope_head; float rope_theta;         /* 0: no RoPE; rope_theta == 0 selects 10000 */
+  /* 1: w and w_scale were written at least two launches before this call on
+   * the stream (weights), so they may be read before the previous launch
+   * completes; the two launches before the call must be ordinary launches or
+   * kernels that signal their dependents only after their own dependency wait
+   * (as every kernel of this library does).  0: everything is read after it. */
+  int32_t w_ready;
+} csa2_fp8_linear_args;
+CSA2_API int csa2_fp8_linear(const csa2_fp8_linear_args* args, void* stream);
+
+/* ---- 8. the batch's rows, pages and slots from its sequences' lengths --------
+ * Sequence b holds ctx_len[b] tokens and gets new_len[b] more in this step
+ * (0: it rests).  With E0 = ctx_len / ratio_m and E1 = (ctx_len + new_len) /
+ * ratio_m its cache grows from E0 to E1 entries.  Every output is optional:
+ *   row_start[b]   rows of the sequences before b ([B + 1]; the last: all rows)
+ *   n_visible[b]   E1
+ *   entry_start[b] new entries of the sequences before b ([B + 1])
+ *   page_table     with free_pages: the logical pages [ceil(E0 / 64), ceil(E1 /
+ *                  64)) of b get the next pages of free_pages, in sequence
+ *                  order, from free_head[0] on (NULL: 0); other places stay.
+ *                  free_head_out[0]: the next page's place after the call
+ *                  (not the same word as free_head).
+ *   per row t (a new token; sequence order): row_seq[t], row_pos[t] (its
+ *     position), swa_new[t] (the ring slot of its own SWA record), swa_slot[t][j]
+ *     (the slot of position row_pos - n_swa + 1 + j, -1 before the sequence's
+ *     start).  The ring of sequence b is the swa_ring slots from ring_id[b] *
+ *     swa_ring on (ring_id NULL: b); position p is in its slot p % swa_ring.  A
+ *     ring of n_swa - 1 + new_len slots keeps every key that the step reads.
+ *   per new entry i (sequence order): entry_slot[i], entry_pos[i] = e * ratio_m,
+ *     entry_row[i] = the row of its last token.
+ * row_seq, row_pos, n_visible are what the csa2_rows of the other calls take,
+ * entry_slot and entry_pos what csa2_compress_m2 takes, swa_slot what
+ * csa2_sparse_attn takes.  Places behind the last row and the last entry are
+ * left as they were, or with pad = 1 set to -1 (0 in entry_pos), which every
+ * call above reads as "nothing here" except csa2_compress_m2, which reports an
+ * entry_slot of -1.
+ * What does not fit is -1 (or not written, past max_rows, max_entries or
+ * pt_stride) and recorded in the device error word (CSA2_ERR_DEVICE_BOUNDS): a
+ * negative length (read as 0), a sequence past pt_stride pages or INT32_MAX
+ * tokens, an empty free list, a page that the table lacks, a ring shorter than
+ * the above (the keys and records that this step overwrites become -1), a slot
+ * past INT32_MAX.  B <= 8192.  No workspace. */
+typedef struct {
+  int32_t B;
+  const int32_t* ctx_len;                      /* [B] */
+  const int32_t* new_len;                      /* [B] */
+  int32_t ratio_m;                             /* 1 or 2 */
+  int32_t* page_table; int32_t pt_stride;      /* [B, pt_stride], for entry_slot and free_pages */
+  const int32_t* free_pages; int32_t n_free;   /* optional [n_free] */
+  const int32_t* free_head; int32_t* free_head_out; /* optional [1] each */
+  int32_t* row_start;                          /* [B + 1] */
+  int32_t* n_visible;                          /* [B] */
+  int32_t* entry_start;                        /* [B + 1] */
+  int32_t max_rows;
+  int32_t* row_seq; int32_t* row_pos;          /* [max_rows] */
+  int32_t max_entries;
+  int32_t* entry_slot; int32_t* entry_pos; int32_t* entry_row; /* [max_entries] */
+  int32_t swa_ring; const int32_t* ring_id;    /* ring_id optional [B] */
+  int32_t* swa_new;                            /* [max_rows] */
+  int32_t* swa_slot; int32_t n_swa; int64_t ld_swa; /* [max_rows, ld_swa], n_swa in 1..128 */
+  int32_t pad;
+} csa2_batch_plan_args;
+CSA2_API int csa2_batch_plan(const csa2_batch_plan_args* args, void* stream);
 
 /* ---- workspace, device errors ------------------------------------------------ */
 enum { CSA2_CALL_INDEX_SCORE = 1, CSA2_CALL_TOPK = 2, CSA2_CALL_REINDEX = 3, CSA2_CALL_SPARSE_ATTN = 4 };

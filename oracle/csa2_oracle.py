@@ -569,3 +569,120 @@ def index_key_fp4_bytes(k: np.ndarray):
     u = fp4_scale_exponent(np.abs(g).max(axis=2))
     codes = fp4_codes(g / np.exp2(u - 127)[..., None]).reshape(n, IDX_DIM)
     return (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8), u.astype(np.uint8)
+
+
+# ---------------------------------------------------------------------------
+# The step's inputs (no counterpart in the pages): e4m3 codes with a scale per
+# 128, projections on them, and the batch's rows, pages and slots
+# ---------------------------------------------------------------------------
+
+E4M3_AMAX_FLOOR = 448.0 * 2.0 ** -120
+
+
+def rms_norm_rows(x: np.ndarray, gamma: np.ndarray, eps: float) -> np.ndarray:
+    """x / sqrt(mean(x^2) + eps) * gamma, row by row."""
+    x = np.asarray(x, dtype=np.float64)
+    return x / np.sqrt((x * x).mean(axis=1, keepdims=True) + eps) * gamma
+
+
+def e4m3_block_scales(y: np.ndarray, block_rows: int):
+    """(scale, code multiplier) of each block of block_rows x 128 of y [T,K]:
+    a = largest finite |y|, raised to 448 * 2^-120; a / 448 and 448 / a; scale 1
+    where every finite value is 0."""
+    T, K = y.shape
+    rb, cb = -(-T // block_rows), -(-K // 128)
+    scale, mult = np.empty((rb, cb)), np.empty((rb, cb))
+    for i in range(rb):
+        for j in range(cb):
+            blk = y[i * block_rows:(i + 1) * block_rows, j * 128:(j + 1) * 128]
+            fin = np.abs(blk[np.isfinite(blk)])
+            top = fin.max() if fin.size else 0.0
+            a = max(top, E4M3_AMAX_FLOOR)
+            scale[i, j] = a / 448.0 if top > 0 else 1.0
+            mult[i, j] = 448.0 / a
+    return scale, mult
+
+
+def expand_blocks(s: np.ndarray, block_rows: int, T: int, K: int) -> np.ndarray:
+    """Per-block values [rows / block_rows, K / 128] at every element of [T,K]."""
+    return np.repeat(np.repeat(s, block_rows, axis=0)[:T], 128, axis=1)[:, :K]
+
+
+def fp8_linear(x: np.ndarray, x_scale: np.ndarray, w: np.ndarray, w_scale: np.ndarray) -> np.ndarray:
+    """y[t][n] = sum_k x[t][k] x_scale[t][k / 128] w[n][k] w_scale[n / 128][k / 128]
+    of decoded codes x [T,K] and w [N,K]."""
+    T, K = x.shape
+    xd = x * expand_blocks(x_scale, 1, T, K)
+    wd = w * expand_blocks(w_scale, 128, w.shape[0], K)
+    return xd @ wd.T
+
+
+def rope_heads(y: np.ndarray, positions: np.ndarray, head: int, theta: float) -> np.ndarray:
+    """The last 64 columns of every head of `head` columns, in interleaved pairs,
+    turned by position * theta^(-2p/64) (the rotation of the keys)."""
+    y = np.array(y, dtype=np.float64)
+    for p in range(32):
+        ang = np.asarray(positions, dtype=np.float64) * theta ** (-2.0 * p / 64.0)
+        c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+        a, b = y[:, head - 64 + 2 * p::head].copy(), y[:, head - 63 + 2 * p::head].copy()
+        y[:, head - 64 + 2 * p::head] = a * c - b * s
+        y[:, head - 63 + 2 * p::head] = a * s + b * c
+    return y
+
+
+def batch_plan(ctx_len, new_len, ratio_m, page_table=None, free_pages=None, free_head=0, ring=0, ring_id=None, n_swa=0):
+    """The batch's arrays, one sequence, token and entry after the other.
+    Returns (dict of lists, page table, whether something did not fit)."""
+    B = len(ctx_len)
+    out = {k: [] for k in ("row_start", "row_seq", "row_pos", "n_visible", "entry_start", "entry_slot", "entry_pos",
+                           "entry_row", "swa_new", "swa_slot")}
+    table = None if page_table is None else np.array(page_table)
+    bad = False
+    for b in range(B):
+        c, n = int(ctx_len[b]), int(new_len[b])
+        if c < 0 or n < 0 or c + n > 2 ** 31 - 1:
+            bad, c, n = True, max(c, 0), 0
+        out["row_start"].append(len(out["row_seq"]))
+        out["entry_start"].append(len(out["entry_pos"]))
+        e0, e1 = c // ratio_m, (c + n) // ratio_m
+        out["n_visible"].append(e1)
+        p0, p1 = -(-e0 // PAGE), -(-e1 // PAGE)
+        if table is not None and p1 > table.shape[1]:
+            bad = True
+        fresh = {}
+        if free_pages is not None:
+            for lp in range(p0, p1):
+                page = int(free_pages[free_head]) if 0 <= free_head < len(free_pages) else -1
+                free_head += 1
+                bad = bad or page < 0
+                fresh[lp] = max(page, -1)
+                if lp < table.shape[1]:
+                    table[b, lp] = fresh[lp]
+        first_row = len(out["row_seq"])
+        rid = b if ring_id is None else int(ring_id[b])
+        has_ring = ring > 0 and rid >= 0 and rid * ring + ring - 1 <= 2 ** 31 - 1
+        kept = max(c + n - ring, 0)     # first position whose slot the step leaves in place
+        if ring > 0 and n > 0 and (not has_ring or kept > (max(c - n_swa + 1, 0) if n_swa else c)):
+            bad = True
+
+        def slot(p):
+            return rid * ring + p % ring if has_ring and p >= kept else -1
+
+        for pos in range(c, c + n):
+            out["row_seq"].append(b)
+            out["row_pos"].append(pos)
+            if ring > 0:
+                out["swa_new"].append(slot(pos))
+                out["swa_slot"].append([slot(pos - n_swa + 1 + j) for j in range(n_swa)])
+        for e in range(e0, e1):
+            out["entry_pos"].append(e * ratio_m)
+            out["entry_row"].append(first_row + e * ratio_m + ratio_m - 1 - c)
+            if table is not None:
+                lp = e // PAGE
+                page = -1 if lp >= table.shape[1] else int(table[b, lp])
+                bad = bad or page < 0
+                out["entry_slot"].append(page * PAGE + e % PAGE if page >= 0 else -1)
+    out["row_start"].append(len(out["row_seq"]))
+    out["entry_start"].append(len(out["entry_pos"]))
+    out["free_head_out"] = [free_head]
+    return out, table, bad

@@ -70,11 +70,32 @@ class KvProjectArgs(C.Structure):
     _fields_ = [("hidden", _P), ("w", _P), ("T", _I32), ("hidden_dim", _I32), ("out", _P)]
 
 
+class QuantFp8Args(C.Structure):
+    _fields_ = [("x", _P), ("ld_x", _I64), ("T", _I32), ("K", _I32), ("block_rows", _I32), ("gamma", _P),
+                ("eps", C.c_float), ("codes", _P), ("ld_codes", _I64), ("scale", _P), ("ld_scale", _I64)]
+
+
+class Fp8LinearArgs(C.Structure):
+    _fields_ = [("x", _P), ("ld_x", _I64), ("x_scale", _P), ("ld_x_scale", _I64), ("w", _P), ("ld_w", _I64),
+                ("w_scale", _P), ("ld_w_scale", _I64), ("T", _I32), ("N", _I32), ("K", _I32), ("out_format", _I32),
+                ("out", _P), ("ld_out", _I64), ("out_scale", _P), ("ld_out_scale", _I64), ("row_pos", _P),
+                ("rope_head", _I32), ("rope_theta", C.c_float), ("w_ready", _I32)]
+
+
+class BatchPlanArgs(C.Structure):
+    _fields_ = [("B", _I32), ("ctx_len", _P), ("new_len", _P), ("ratio_m", _I32), ("page_table", _P),
+                ("pt_stride", _I32), ("free_pages", _P), ("n_free", _I32), ("free_head", _P), ("free_head_out", _P),
+                ("row_start", _P), ("n_visible", _P), ("entry_start", _P), ("max_rows", _I32), ("row_seq", _P),
+                ("row_pos", _P), ("max_entries", _I32), ("entry_slot", _P), ("entry_pos", _P), ("entry_row", _P),
+                ("swa_ring", _I32), ("ring_id", _P), ("swa_new", _P), ("swa_slot", _P), ("n_swa", _I32),
+                ("ld_swa", _I64), ("pad", _I32)]
+
+
 CALL_INDEX_SCORE, CALL_TOPK, CALL_REINDEX, CALL_SPARSE_ATTN = 1, 2, 3, 4
 EXPORTED = ("csa2_status_string", "csa2_last_error_detail", "csa2_index_score", "csa2_topk_with_candidates",
             "csa2_reindex", "csa2_sparse_attn", "csa2_compress_m2", "csa2_workspace_size",
             "csa2_check_device_error", "csa2_version", "csa2_topk_with_candidates_noalloc",
-            "csa2_debug_bounded_wait", "csa2_kv_project")
+            "csa2_debug_bounded_wait", "csa2_kv_project", "csa2_quant_fp8", "csa2_fp8_linear", "csa2_batch_plan")
 
 _lib = None
 
@@ -113,6 +134,11 @@ def load(build_if_missing: bool = False) -> C.CDLL:
     lib.csa2_check_device_error.argtypes = [_P]
     lib.csa2_kv_project.restype = C.c_int
     lib.csa2_kv_project.argtypes = [C.POINTER(KvProjectArgs), _P]
+    for name, st in (("csa2_quant_fp8", QuantFp8Args), ("csa2_fp8_linear", Fp8LinearArgs),
+                     ("csa2_batch_plan", BatchPlanArgs)):
+        f = getattr(lib, name)
+        f.restype = C.c_int
+        f.argtypes = [C.POINTER(st), _P]
     lib.csa2_debug_bounded_wait.restype = C.c_int
     lib.csa2_debug_bounded_wait.argtypes = [C.c_uint32, _P]
     _lib = lib
@@ -275,6 +301,144 @@ def kv_project(hidden, w, out, stream=None):
     lib = load()
     a = KvProjectArgs(_ptr(hidden), _ptr(w), hidden.shape[0], hidden.shape[1], _ptr(out))
     _check(lib.csa2_kv_project(C.byref(a), _stream(stream)), "csa2_kv_project")
+
+
+_EMPTY = 16  # stands for a given tensor without elements (its data_ptr is 0); the length 0 goes along
+
+
+def _mat(t, name: str, dtype, rows: int | None = None, cols: int | None = None):
+    """(pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous (the rows may be apart)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: CSA2 calls take CUDA tensors (no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name}: expected a 2-D tensor with contiguous rows")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name}: expected shape [{rows}, {cols}], got {list(t.shape)}")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"{name}: its rows overlap (row stride {ld})")
+    return t.data_ptr() or _EMPTY, ld
+
+
+def _vec(t, name: str, dtype, n: int | None = None) -> int | None:
+    """Pointer of a contiguous 1-D CUDA tensor of n elements (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: CSA2 calls take CUDA tensors (no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous 1-D tensor")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.shape[0]}")
+    return t.data_ptr() or _EMPTY
+
+
+def _call(fn, args, where: str, stream, *tensors):
+    """Issues a call on the tensors' device: all of them on one, its current
+    stream unless one is given."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.get_device()
+            elif t.get_device() != dev:
+                raise ValueError(f"{where}: its tensors are on different devices")
+    if dev == torch.cuda.current_device():
+        rc = fn(C.byref(args), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(C.byref(args), _stream(stream))
+    if rc != 0:
+        _check(rc, where)
+
+
+def quant_fp8(x, codes, scale, gamma=None, eps=1e-6, block_rows=1, stream=None):
+    """e4m3 codes of x [T,K] bf16 with a fp32 scale per 128 columns of a row (block_rows=1;
+    with gamma [K] of the row's RMSNorm) or per 128 x 128 tile (block_rows=128, weights):
+    codes uint8 [T,K], scale [ceil(T/block_rows), ceil(K/128)] (csa2_quant_fp8)."""
+    lib = load()
+    px, ldx = _mat(x, "x", torch.bfloat16)
+    T, K = x.shape
+    pc, ldc = _mat(codes, "codes", torch.uint8, T, K)
+    ps, lds = _mat(scale, "scale", torch.float32, T if block_rows == 1 else (T + 127) // 128, (K + 127) // 128)
+    a = QuantFp8Args(px, ldx, T, K, block_rows, _vec(gamma, "gamma", torch.float32, K), eps, pc, ldc, ps, lds)
+    _call(lib.csa2_quant_fp8, a, "csa2_quant_fp8", stream, x, codes, scale, gamma)
+
+
+OUT_F32, OUT_BF16, OUT_FP8 = 0, 1, 2
+_OUT_FORMAT = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.uint8: OUT_FP8}
+
+
+def fp8_linear(x, x_scale, w, w_scale, out, out_scale=None, row_pos=None, rope_head=0, rope_theta=0.0, w_ready=False,
+               stream=None):
+    """out [T,N] = x [T,K] @ w [N,K]^T on e4m3 codes (uint8) with their scales: x_scale
+    [T,ceil(K/128)], w_scale [ceil(N/128),ceil(K/128)].  out fp32, bf16, or uint8 codes with
+    out_scale [T,N/128]; rope_head turns the last 64 columns of every head of that many
+    columns by row_pos [T] (csa2_fp8_linear)."""
+    lib = load()
+    px, ldx = _mat(x, "x", torch.uint8)
+    T, K = x.shape
+    pw, ldw = _mat(w, "w", torch.uint8, None, K)
+    N = w.shape[0]
+    nb = (K + 127) // 128
+    pxs, ldxs = _mat(x_scale, "x_scale", torch.float32, T, nb)
+    pws, ldws = _mat(w_scale, "w_scale", torch.float32, (N + 127) // 128, nb)
+    fmt = _OUT_FORMAT.get(out.dtype)
+    if fmt is None:
+        raise TypeError(f"out: expected float32, bfloat16 or uint8, got {out.dtype}")
+    po, ldo = _mat(out, "out", out.dtype, T, N)
+    pos, ldos = (None, 0) if out_scale is None else _mat(out_scale, "out_scale", torch.float32, T, N // 128)
+    a = Fp8LinearArgs(px, ldx, pxs, ldxs, pw, ldw, pws, ldws, T, N, K, fmt, po, ldo, pos, ldos,
+                      _vec(row_pos, "row_pos", torch.int32, T), rope_head, rope_theta, 1 if w_ready else 0)
+    _call(lib.csa2_fp8_linear, a, "csa2_fp8_linear", stream, x, x_scale, w, w_scale, out, out_scale, row_pos)
+
+
+def _cap(**arrays) -> int:
+    """The one length of the given arrays (0 when none is given)."""
+    sizes = {k: t.shape[0] for k, t in arrays.items() if t is not None}
+    if len(set(sizes.values())) > 1:
+        raise ValueError(f"these arrays must have one length: {sizes}")
+    return next(iter(sizes.values()), 0)
+
+
+def batch_plan(ctx_len, new_len, ratio_m=1, page_table=None, free_pages=None, free_head=None, free_head_out=None,
+               row_start=None, n_visible=None, entry_start=None, row_seq=None, row_pos=None, entry_slot=None,
+               entry_pos=None, entry_row=None, swa_ring=0, ring_id=None, swa_new=None, swa_slot=None, pad=False,
+               stream=None):
+    """Rows, pages and slots of a step whose sequences hold ctx_len [B] tokens and get
+    new_len [B] more (csa2_batch_plan).  Every output is optional, int32, and written in
+    place; row arrays share one length (rows the step may have), entry arrays another;
+    page_table [B, pages] is extended from free_pages when that is given."""
+    lib = load()
+    i32 = torch.int32
+    B = ctx_len.shape[0]
+    pt, ldp = (None, 0) if page_table is None else _mat(page_table, "page_table", i32, B)
+    if page_table is not None and ldp != page_table.shape[1]:
+        raise ValueError("page_table: expected a contiguous tensor")
+    ss, lds = (None, 0) if swa_slot is None else _mat(swa_slot, "swa_slot", i32)
+    a = BatchPlanArgs(
+        B, _vec(ctx_len, "ctx_len", i32), _vec(new_len, "new_len", i32, B), ratio_m, pt, ldp,
+        _vec(free_pages, "free_pages", i32), 0 if free_pages is None else free_pages.shape[0],
+        _vec(free_head, "free_head", i32, 1), _vec(free_head_out, "free_head_out", i32, 1),
+        _vec(row_start, "row_start", i32, B + 1), _vec(n_visible, "n_visible", i32, B),
+        _vec(entry_start, "entry_start", i32, B + 1),
+        _cap(row_seq=row_seq, row_pos=row_pos, swa_new=swa_new, swa_slot=swa_slot),
+        _vec(row_seq, "row_seq", i32), _vec(row_pos, "row_pos", i32),
+        _cap(entry_slot=entry_slot, entry_pos=entry_pos, entry_row=entry_row),
+        _vec(entry_slot, "entry_slot", i32), _vec(entry_pos, "entry_pos", i32), _vec(entry_row, "entry_row", i32),
+        swa_ring, _vec(ring_id, "ring_id", i32, B), _vec(swa_new, "swa_new", i32), ss,
+        0 if swa_slot is None else swa_slot.shape[1], lds, 1 if pad else 0)
+    _call(lib.csa2_batch_plan, a, "csa2_batch_plan", stream, ctx_len, new_len, page_table, free_pages, free_head,
+          free_head_out, row_start, n_visible, entry_start, row_seq, row_pos, entry_slot, entry_pos, entry_row, ring_id,
+          swa_new, swa_slot)
 
 
 def check_device_error(stream=None) -> int:

@@ -47,6 +47,8 @@ int cuda_fail(cudaError_t e, const char* what) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 constexpr int kMaxDevices = 64;
 std::mutex g_ctx_mu;
 csa2::DeviceCtx g_ctx[kMaxDevices];
@@ -495,6 +497,107 @@ int csa2_kv_project(const csa2_kv_project_args* a, void* stream) {
   cudaError_t e = csa2::launch_kv_project(a->hidden, a->w, a->T, a->hidden_dim, a->out,
                                           static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "csa2_kv_project: launch");
+  return CSA2_OK;
+}
+
+int csa2_quant_fp8(const csa2_quant_fp8_args* a, void* stream) {
+  if (!a) return fail(CSA2_ERR_NULL, "csa2_quant_fp8: args is NULL");
+  if (!a->x || !a->codes || !a->scale) return fail(CSA2_ERR_NULL, "csa2_quant_fp8: x/codes/scale is NULL");
+  if (a->T < 1) return fail(CSA2_ERR_SHAPE, "csa2_quant_fp8: T must be >= 1");
+  if (a->K < 16 || a->K > 16384 || (a->K & 15))
+    return fail(CSA2_ERR_SHAPE, "csa2_quant_fp8: K=%d must be a multiple of 16 in 16..16384", a->K);
+  if (a->block_rows != 1 && a->block_rows != 128)
+    return fail(CSA2_ERR_UNSUPPORTED, "csa2_quant_fp8: block_rows=%d must be 1 or 128", a->block_rows);
+  if (a->gamma && a->block_rows != 1)
+    return fail(CSA2_ERR_UNSUPPORTED, "csa2_quant_fp8: gamma needs block_rows = 1");
+  if (!(a->eps >= 0.f) || !isfinite(a->eps)) return fail(CSA2_ERR_SHAPE, "csa2_quant_fp8: eps must be finite and >= 0");
+  if (a->ld_x < a->K || a->ld_codes < a->K || a->ld_scale < (a->K + 127) / 128)
+    return fail(CSA2_ERR_SHAPE, "csa2_quant_fp8: a row stride is smaller than its row");
+  if (!aligned16(a->x) || !aligned16(a->codes) || (a->gamma && !aligned16(a->gamma)) || (a->ld_x & 7) || (a->ld_codes & 15))
+    return fail(CSA2_ERR_ALIGN, "csa2_quant_fp8: x, codes, gamma must be 16-B aligned, ld_x a multiple of 8, ld_codes of 16");
+  if (!aligned4(a->scale)) return fail(CSA2_ERR_ALIGN, "csa2_quant_fp8: scale must be 4-B aligned");
+  // one thread block per 8 runs of 512 columns, per row or per tile
+  if (static_cast<long long>(a->T) * ((a->K + 511) / 512) / 8 > 0x7FFFFFFELL)
+    return fail(CSA2_ERR_SHAPE, "csa2_quant_fp8: T=%d rows of %d are too many for one call", a->T, a->K);
+  cudaError_t e = csa2::launch_quant_fp8(*a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_quant_fp8: launch");
+  return CSA2_OK;
+}
+
+int csa2_fp8_linear(const csa2_fp8_linear_args* a, void* stream) {
+  if (!a) return fail(CSA2_ERR_NULL, "csa2_fp8_linear: args is NULL");
+  if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->out)
+    return fail(CSA2_ERR_NULL, "csa2_fp8_linear: x/x_scale/w/w_scale/out is NULL");
+  if (a->T < 1 || a->N < 1) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: T=%d and N=%d must be >= 1", a->T, a->N);
+  if (a->K < 16 || a->K > 65536 || (a->K & 15))
+    return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: K=%d must be a multiple of 16 in 16..65536", a->K);
+  const int nb = (a->K + 127) / 128;
+  if (a->ld_x < a->K || a->ld_w < a->K || a->ld_out < a->N || a->ld_x_scale < nb || a->ld_w_scale < nb)
+    return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: a row stride is smaller than its row");
+  if (a->ld_x >= (1LL << 39) || a->ld_w >= (1LL << 39))
+    return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: ld_x and ld_w must be below 2^39");
+  if (a->out_format != CSA2_OUT_F32 && a->out_format != CSA2_OUT_BF16 && a->out_format != CSA2_OUT_FP8)
+    return fail(CSA2_ERR_UNSUPPORTED, "csa2_fp8_linear: out_format=%d is not fp32 (0), bf16 (1) or e4m3 (2)", a->out_format);
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->out) || (a->ld_x & 15) || (a->ld_w & 15))
+    return fail(CSA2_ERR_ALIGN, "csa2_fp8_linear: x, w, out must be 16-B aligned, ld_x and ld_w multiples of 16");
+  if (!aligned4(a->x_scale) || !aligned4(a->w_scale) || !aligned4(a->row_pos) || !aligned4(a->out_scale))
+    return fail(CSA2_ERR_ALIGN, "csa2_fp8_linear: scales and row_pos must be 4-B aligned");
+  if (a->out_format == CSA2_OUT_FP8) {
+    if (!a->out_scale) return fail(CSA2_ERR_NULL, "csa2_fp8_linear: e4m3 output needs out_scale");
+    if (a->N & 127) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: e4m3 output needs N=%d to be a multiple of 128", a->N);
+    if (a->ld_out_scale < a->N / 128) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: ld_out_scale < N / 128");
+    if (a->ld_out & 15) return fail(CSA2_ERR_ALIGN, "csa2_fp8_linear: e4m3 output needs ld_out to be a multiple of 16");
+  }
+  if (a->rope_head) {
+    if (!a->row_pos) return fail(CSA2_ERR_NULL, "csa2_fp8_linear: rope_head needs row_pos");
+    if (a->rope_head < 128 || (a->rope_head & 127) || a->N % a->rope_head)
+      return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: rope_head=%d must be a multiple of 128 that divides N=%d",
+                  a->rope_head, a->N);
+    if (!(a->rope_theta >= 0.f) || !isfinite(a->rope_theta))
+      return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: rope_theta must be finite and >= 0");
+  }
+  if (a->w_ready != 0 && a->w_ready != 1) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: w_ready=%d must be 0 or 1", a->w_ready);
+  DeviceCtx ctx;
+  cudaError_t e = csa2::device_ctx(&ctx);
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_fp8_linear: device");
+  const char* why = "csa2_fp8_linear: launch";
+  e = csa2::launch_fp8_linear(*a, ctx, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return cuda_fail(e, why);
+  return CSA2_OK;
+}
+
+int csa2_batch_plan(const csa2_batch_plan_args* a, void* stream) {
+  if (!a) return fail(CSA2_ERR_NULL, "csa2_batch_plan: args is NULL");
+  if (!a->ctx_len || !a->new_len) return fail(CSA2_ERR_NULL, "csa2_batch_plan: ctx_len/new_len is NULL");
+  if (a->B < 1 || a->B > csa2::kPlanMaxSeqs)
+    return fail(CSA2_ERR_SHAPE, "csa2_batch_plan: B=%d not in 1..%d", a->B, csa2::kPlanMaxSeqs);
+  if (a->ratio_m != 1 && a->ratio_m != 2) return fail(CSA2_ERR_UNSUPPORTED, "csa2_batch_plan: ratio_m=%d must be 1 or 2", a->ratio_m);
+  if (a->page_table && a->pt_stride < 1) return fail(CSA2_ERR_SHAPE, "csa2_batch_plan: pt_stride must be >= 1");
+  if ((a->entry_slot || a->free_pages) && !a->page_table)
+    return fail(CSA2_ERR_NULL, "csa2_batch_plan: entry_slot and free_pages need page_table");
+  if (a->free_pages && a->n_free < 0) return fail(CSA2_ERR_SHAPE, "csa2_batch_plan: n_free < 0");
+  if ((a->free_head || a->free_head_out) && !a->free_pages)
+    return fail(CSA2_ERR_NULL, "csa2_batch_plan: free_head and free_head_out need free_pages");
+  if (a->free_head && a->free_head == a->free_head_out)
+    return fail(CSA2_ERR_UNSUPPORTED, "csa2_batch_plan: free_head_out must not be the word of free_head");
+  if (a->max_rows < 0 || a->max_entries < 0) return fail(CSA2_ERR_SHAPE, "csa2_batch_plan: max_rows or max_entries < 0");
+  if (a->swa_new || a->swa_slot) {
+    if (a->swa_ring < 1) return fail(CSA2_ERR_SHAPE, "csa2_batch_plan: swa_ring must be >= 1");
+    if (a->swa_slot && (a->n_swa < 1 || a->n_swa > CSA2_MAX_SWA))
+      return fail(CSA2_ERR_SHAPE, "csa2_batch_plan: n_swa=%d not in 1..128", a->n_swa);
+    if (a->swa_slot && a->ld_swa < a->n_swa) return fail(CSA2_ERR_SHAPE, "csa2_batch_plan: ld_swa < n_swa");
+  }
+  if (a->pad != 0 && a->pad != 1) return fail(CSA2_ERR_SHAPE, "csa2_batch_plan: pad=%d must be 0 or 1", a->pad);
+  const void* words[] = {a->ctx_len, a->new_len, a->page_table, a->free_pages, a->free_head, a->free_head_out,
+                         a->row_start, a->n_visible, a->entry_start, a->row_seq, a->row_pos, a->entry_slot,
+                         a->entry_pos, a->entry_row, a->ring_id, a->swa_new, a->swa_slot};
+  for (const void* w : words)
+    if (!aligned4(w)) return fail(CSA2_ERR_ALIGN, "csa2_batch_plan: arrays must be 4-B aligned");
+  DeviceCtx ctx;
+  cudaError_t e = csa2::device_ctx(&ctx);
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_batch_plan: device");
+  e = csa2::launch_batch_plan(*a, ctx, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_batch_plan: launch");
   return CSA2_OK;
 }
 

@@ -158,6 +158,14 @@ cudaError_t launch_compress(const CompressLaunch& a, const DeviceCtx& ctx, cudaS
 cudaError_t launch_kv_project(const uint16_t* H, const uint16_t* W, int T, int hidden, uint16_t* out,
                               cudaStream_t st);
 
+// e4m3 codes with a scale per 128 columns (or per 128 x 128 tile).
+cudaError_t launch_quant_fp8(const csa2_quant_fp8_args& a, cudaStream_t st);
+// Projection on e4m3 codes with block scales.
+cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ctx, cudaStream_t st, const char** why);
+// Rows, pages and slots of a batch from its sequences' lengths.
+constexpr int kPlanMaxSeqs = 8192;
+cudaError_t launch_batch_plan(const csa2_batch_plan_args& a, const DeviceCtx& ctx, cudaStream_t st);
+
 // Shared by the top-k entry points: argument checks + launch description;
 // `who` names the entry point in the error detail.
 int topk_prepare(const csa2_topk_args* a, SelectLaunch* S, const char* who);
