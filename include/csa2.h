@@ -406,7 +406,7 @@ CSA2_API int csa2_quant_fp8(const csa2_quant_fp8_args* args, void* stream);
  * scale for each 128 columns by the rule of csa2_quant_fp8: with N = 32 * 128
  * the query that csa2_index_score and csa2_reindex take.
  * Rows t < T and columns n < N are written and nothing else.  K is a multiple
- * of 16, at most 65536.  Alignment: x, w, out 16 B; ld_x and ld_w multiples of
+ * of 16, at most 65536; N at most 2^28.  Alignment: x, w, out 16 B; ld_x and ld_w multiples of
  * 16; row_pos, scales 4 B; for CSA2_OUT_FP8 ld_out a multiple of 16.  out must
  * not overlap an input.  No workspace; results do not depend on the launch's
  * timing (no atomics). */

@@ -124,7 +124,7 @@ CUresult encode_tmap_2d_fp4(CUtensorMap* map, const void* base, uint64_t rows, u
 }
 
 CUresult encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows,
-                           uint64_t row_stride, uint32_t box_inner, uint32_t box_rows) {
+                           uint64_t row_stride, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_encoder();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
   const cuuint64_t dims[2] = {inner_bytes, rows};
@@ -132,7 +132,7 @@ CUresult encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner_by
   const cuuint32_t box[2] = {box_inner, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
@@ -531,6 +531,7 @@ int csa2_fp8_linear(const csa2_fp8_linear_args* a, void* stream) {
   if (a->T < 1 || a->N < 1) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: T=%d and N=%d must be >= 1", a->T, a->N);
   if (a->K < 16 || a->K > 65536 || (a->K & 15))
     return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: K=%d must be a multiple of 16 in 16..65536", a->K);
+  if (a->N > (1 << 28)) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: N=%d is above 2^28", a->N);
   const int nb = (a->K + 127) / 128;
   if (a->ld_x < a->K || a->ld_w < a->K || a->ld_out < a->N || a->ld_x_scale < nb || a->ld_w_scale < nb)
     return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: a row stride is smaller than its row");

@@ -195,6 +195,7 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // box_rows rows; base must be 32-byte aligned.
 CUresult encode_tmap_2d_fp4(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
 CUresult encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows,
-                           uint64_t row_stride, uint32_t box_inner, uint32_t box_rows);
+                           uint64_t row_stride, uint32_t box_inner, uint32_t box_rows,
+                           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 }  // namespace csa2

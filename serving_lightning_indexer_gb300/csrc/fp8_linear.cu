@@ -20,7 +20,7 @@ namespace {
 constexpr int kTileM = 128;   // rows of x a tile
 constexpr int kBlockK = 128;  // input dims of a scale block: one swizzled 128-B row of codes
 constexpr int kAccWarps = 8;
-constexpr int kThreads = (kAccWarps + 2) * 32;
+constexpr int kThreads = (kAccWarps + 4) * 32;  // three warpgroups: the last holds the producer and the MMA issuer
 
 struct LinearParams {
   const float* x_scale;
@@ -31,7 +31,8 @@ struct LinearParams {
   long long ld_xs, ld_ws, ld_out, ld_os;
   int T, N, K;
   int rope_head;
-  int vec;      // output rows are 16-B aligned
+  int vec;         // output rows are 16-B aligned
+  int vec_scales;  // scale rows are 16-B aligned
   int w_ready;
   uint32_t* err;
   uint64_t turn[32];  // RoPE turn rates of the 32 pairs
@@ -39,64 +40,214 @@ struct LinearParams {
 
 template <int BN>
 struct WideCfg {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStages = 4;
   static constexpr int kStageBytes = (kTileM + BN) * kBlockK;
   static constexpr int kAccs = 512 / BN;          // TMEM ring: 512 columns
   static constexpr int kCols = BN / 2;            // columns of a tile an accumulation warp holds
-  static constexpr int kOffBars = kStages * kStageBytes;
-  static constexpr int kOffMax = kOffBars + 256;  // block maxima of the two column halves
-  static constexpr int kSmem = 1024 + kOffMax + 2 * kTileM * 4;
+  static constexpr int kOffOut = kStages * kStageBytes;  // 32 rows x 64 B of output per accumulation warp
+  static constexpr int kScaleSlots = 4;                  // ring of the scales of four blocks: 128 rows, 2 column halves
+  static constexpr int kScaleBytes = 4 * (kTileM + 2) * 4;  // per block: the rows', the halves'
+  static constexpr int kOffScales = kOffOut + kAccWarps * 2048;
+  static constexpr int kOffBars = kOffScales + kScaleSlots * kScaleBytes;
+  static constexpr int kSmem = 1024 + kOffBars + 256;
 };
 
-// Writes NV consecutive values of one row from column c on; only columns < N.
-template <int OUT, int NV>
-__device__ __forceinline__ void store_row(const LinearParams& p, long long row, int c, const float (&y)[NV]) {
-  if (OUT == CSA2_OUT_F32) {
-    float* o = static_cast<float*>(p.out) + row * p.ld_out + c;
-    if (p.vec && c + NV <= p.N) {
+// Registers move from the producer's warpgroup to the two accumulation
+// warpgroups: 384 threads start with 168 each; 2 * 128 * 224 + 128 * 56 = 384 * 168.
+__device__ __forceinline__ void regs_accumulate() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+__device__ __forceinline__ void regs_produce() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
+
+// Four consecutive scales of a row, of which n (<= 0: none) exist; 0 for the others.
+__device__ __forceinline__ float4 load_scales(const float* s, int n, bool vec) {
+  if (vec && n >= 4) return __ldg(reinterpret_cast<const float4*>(s));
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (n > 0) v.x = __ldg(s);
+  if (n > 1) v.y = __ldg(s + 1);
+  if (n > 2) v.z = __ldg(s + 2);
+  if (n > 3) v.w = __ldg(s + 3);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The 16-byte piece i of a row's output values y (f: the factor to e4m3 codes).
+template <int OUT, int C>
+__device__ __forceinline__ uint4 out_piece(const float (&y)[C], int i, float f) {
+  if (OUT == CSA2_OUT_F32)
+    return make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
+                      __float_as_uint(y[4 * i + 3]));
+  if (OUT == CSA2_OUT_BF16)
+    return make_uint4(bf16x2(y[8 * i], y[8 * i + 1]), bf16x2(y[8 * i + 2], y[8 * i + 3]), bf16x2(y[8 * i + 4], y[8 * i + 5]),
+                      bf16x2(y[8 * i + 6], y[8 * i + 7]));
+  return make_uint4(e4m3x4(y[16 * i] * f, y[16 * i + 1] * f, y[16 * i + 2] * f, y[16 * i + 3] * f),
+                    e4m3x4(y[16 * i + 4] * f, y[16 * i + 5] * f, y[16 * i + 6] * f, y[16 * i + 7] * f),
+                    e4m3x4(y[16 * i + 8] * f, y[16 * i + 9] * f, y[16 * i + 10] * f, y[16 * i + 11] * f),
+                    e4m3x4(y[16 * i + 12] * f, y[16 * i + 13] * f, y[16 * i + 14] * f, y[16 * i + 15] * f));
+}
+__host__ __device__ constexpr int out_size(int format) {
+  return format == CSA2_OUT_F32 ? 4 : (format == CSA2_OUT_BF16 ? 2 : 1);
+}
+
+// The accumulation warps' part: sums each tile in registers and writes it.
+// False when a wait gave up (the same in a warp's lanes).
+template <int BN, int OUT>
+__device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out, const LinearParams& p, uint8_t* smem,
+                                                     uint32_t tmem, uint64_t* tfull, uint64_t* tempty, uint64_t* empty,
+                                                     uint64_t* sfull, uint64_t* sempty, volatile int* s_abort) {
+  using Cfg = WideCfg<BN>;
+  constexpr int S = Cfg::kStages, NA = Cfg::kAccs, C = Cfg::kCols, SS = Cfg::kScaleSlots;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = warp >> 2;            // columns half * C .. of the tile
+  const int r = (warp & 3) * 32 + lane;  // row of the tile: TMEM lane
+  const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * C;
+  uint8_t* s_out = smem + Cfg::kOffOut + warp * 2048;
+  const int m_tiles = (p.T + kTileM - 1) / kTileM, n_tiles = (p.N + BN - 1) / BN;
+  const int blocks = (p.K + kBlockK - 1) / kBlockK;
+  const long long tiles = static_cast<long long>(m_tiles) * n_tiles;
+  // A wait on a completed barrier still costs its round trip (some 100 cycles),
+  // so the next block's accumulator and scales are asked for under this block's
+  // last sums.
+  uint32_t a = 0, a_phase = 0, st = 0;      // accumulator ring, stage ring
+  uint32_t sl = 0, sl_phase = 0, in4 = 0;   // scale ring, block within its group
+  const float* sc = reinterpret_cast<const float*>(smem + Cfg::kOffScales);
+  bool ready = false;
+  float s = 0.f;
+  if (blockIdx.x < tiles) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&sfull[0], 0, s_abort))) return false;
+    s = sc[r] * sc[kTileM + half];
+  }
+  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int n0 = static_cast<int>(tile / m_tiles) * BN + half * C, t0 = static_cast<int>(tile % m_tiles) * kTileM;
+    const int row = t0 + r;
+    const bool last_tile = tile + gridDim.x >= tiles;
+    uint64_t acc[C / 2];  // this row's sums, in pairs of columns
 #pragma unroll
-      for (int i = 0; i < NV; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-    } else {
+    for (int i = 0; i < C / 2; ++i) acc[i] = 0;
+#pragma unroll 1
+    for (int b = blocks; b > 0; --b) {
+      if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, mbar_wait(&tfull[a], a_phase, s_abort))) return false;
+      tc_fence_after();
+      // the products have read the stage: one commit a block serves both rings
+      // (a second one costs the tensor pipe some 60 cycles)
+      if (warp == 0 && lane == 0) mbar_arrive(&empty[st]);
+      const uint64_t s2 = pack_f32x2(s, s);
+      uint32_t v[2][32];
+      tmem_ld32x32(taddr + a * BN, v[0]);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (c + i < p.N) o[i] = y[i];
-    }
-  } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + c;
-    if (p.vec && c + NV <= p.N) {
-#pragma unroll
-      for (int i = 0; i < NV; i += 8) {
-        uint32_t r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(y[i + 2 * j], y[i + 2 * j + 1]);
-          r[j] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int c = 0; c < C / 32; ++c) {
+        tmem_wait_ld(v[c & 1]);
+        if (c + 1 < C / 32) {
+          tmem_ld32x32(taddr + a * BN + (c + 1) * 32, v[(c + 1) & 1]);
+        } else {  // all of it is in registers: the next product may have the accumulator
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[a]);
+          if (++a == NA) {
+            a = 0;
+            a_phase ^= 1;
+          }
+          if (++st == S) st = 0;
+          ready = mbar_test(&tfull[a], a_phase);
+          if (++in4 == 4 || b == 1) {
+            if (lane == 0) mbar_arrive(&sempty[sl]);
+            in4 = 0;
+            if (++sl == SS) {
+              sl = 0;
+              sl_phase ^= 1;
+            }
+            if (!(last_tile && b == 1) && !__all_sync(0xffffffffu, mbar_wait(&sfull[sl], sl_phase, s_abort))) return false;
+          }
+          const float* sn = sc + sl * (Cfg::kScaleBytes / 4) + in4 * (kTileM + 2);
+          s = sn[r] * sn[kTileM + half];
         }
-        *reinterpret_cast<uint4*>(o + i) = make_uint4(r[0], r[1], r[2], r[3]);
-      }
-    } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (c + i < p.N) o[i] = __float2bfloat16_rn(y[i]);
+        for (int i = 0; i < 16; ++i)
+          acc[c * 16 + i] = fma_f32x2(pack_f32x2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2,
+                                      acc[c * 16 + i]);
+      }
+    }
+    if (n0 >= p.N || t0 + (warp & 3) * 32 >= p.T) continue;
+    float y[C];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      const float2 f = unpack_f32x2(acc[i]);
+      y[2 * i] = f.x;
+      y[2 * i + 1] = f.y;
+    }
+    if (p.rope_head && (n0 + C) % p.rope_head == 0) {  // the 64 columns below a head's end
+      const int pos = __ldg(p.row_pos + min(row, p.T - 1));
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float sn, cs;
+        rope_angle(pos, p.turn[i], &sn, &cs);
+        const float u = y[C - 64 + 2 * i], v = y[C - 63 + 2 * i];
+        y[C - 64 + 2 * i] = u * cs - v * sn;
+        y[C - 63 + 2 * i] = u * sn + v * cs;
+      }
+    }
+    float f = 0.f;
+    if (OUT == CSA2_OUT_FP8) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        y[i] = finite_or_nan(y[i]);
+        m = fmaxf(m, fabsf(y[i]));
+      }
+      const float sc = e4m3_block(m, &f);
+      if (row < p.T) p.out_scale[static_cast<long long>(row) * p.ld_os + (n0 >> 7)] = sc;
+    }
+    constexpr int kSize = out_size(OUT), kPieces = C * kSize / 16;
+    if (p.vec) {
+      // 32 rows x 64 B at a time through shared memory (swizzled, so that the
+      // lanes' 16-byte stores do not collide) and out by a tensor store
+#pragma unroll
+      for (int c = 0; c < kPieces; c += 4) {
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(s_out + lane * 64 + ((i ^ ((lane >> 1) & 3)) * 16)) = out_piece<OUT, C>(y, c + i, f);
+        fence_proxy_async_smem();
+        __syncwarp();
+        const int x = n0 * kSize + c * 16;
+        if (lane == 0 && x < p.N * kSize) {
+          tma_store_2d(&map_out, s_out, x, t0 + (warp & 3) * 32);
+          bulk_commit();
+        }
+      }
+    } else if (row < p.T) {  // rows that are not 16-byte aligned (never e4m3)
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        if (n0 + i >= p.N) continue;
+        const long long at = static_cast<long long>(row) * p.ld_out + n0 + i;
+        if (OUT == CSA2_OUT_F32) static_cast<float*>(p.out)[at] = y[i];
+        else if (OUT == CSA2_OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y[i]);
+      }
     }
   }
+  if (lane == 0) bulk_wait_all();
+  return true;
 }
 
 template <int BN, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_linear_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                           const __grid_constant__ LinearParams p) {
+                           const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p) {
   using Cfg = WideCfg<BN>;
-  constexpr int S = Cfg::kStages, NA = Cfg::kAccs, C = Cfg::kCols;
+  constexpr int S = Cfg::kStages, NA = Cfg::kAccs, C = Cfg::kCols, SS = Cfg::kScaleSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBars);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
   uint64_t* tempty = tfull + NA;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + NA);
+  uint64_t* sfull = tempty + NA;
+  uint64_t* sempty = sfull + SS;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sempty + SS);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  float* s_max = reinterpret_cast<float*>(smem + Cfg::kOffMax);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -108,6 +259,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < NA; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], kAccWarps);
+    }
+    for (int i = 0; i < SS; ++i) {
+      mbar_init(&sfull[i], 2);
+      mbar_init(&sempty[i], kAccWarps);
     }
     fence_mbar_init();
     prefetch_tmap(&map_x);
@@ -127,7 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int blocks = (p.K + kBlockK - 1) / kBlockK;
   const long long tiles = static_cast<long long>(m_tiles) * n_tiles;
 
-  if (warp == kAccWarps) {
+  if (warp >= kAccWarps) {
+   regs_produce();
+   if (warp == kAccWarps) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t keep = l2_policy_evict_last();
@@ -152,25 +309,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long i = (it > S ? it - S : 0); i < it; ++i)
         mbar_wait(&full[i % S], static_cast<uint32_t>((i / S) & 1), nullptr);
     }
-  } else if (warp == kAccWarps + 1) {
+   } else if (warp == kAccWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(kTileM, BN);
-      long long it = 0;
+      constexpr uint64_t kStageDesc = Cfg::kStageBytes >> 4;
+      const uint64_t x_desc = smem_desc_sw128(smem), w_desc = smem_desc_sw128(smem + kTileM * kBlockK);
+      const long long mine = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * blocks;  // blocks of this CTA's tiles
+      uint32_t s = 0, phase = 0, a = 0, a_phase = 1;
       bool ok = true;
-      for (long long tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        for (int b = 0; b < blocks; ++b, ++it) {
-          const int s = static_cast<int>(it % S), a = static_cast<int>(it % NA);
-          if (!(ok = mbar_wait(&full[s], static_cast<uint32_t>((it / S) & 1), s_abort))) break;
-          if (!(ok = mbar_wait(&tempty[a], static_cast<uint32_t>((it / NA) & 1) ^ 1u, s_abort))) break;
-          tc_fence_after();
-          const uint64_t ad = smem_desc_sw128(smem + s * Cfg::kStageBytes);
-          const uint64_t bd = smem_desc_sw128(smem + s * Cfg::kStageBytes + kTileM * kBlockK);
+      for (long long i = 0; i < mine; ++i) {
+        if (!(ok = mbar_wait(&full[s], phase, s_abort))) break;
+        const uint64_t ad = x_desc + s * kStageDesc, bd = w_desc + s * kStageDesc;
+        const uint32_t d = tmem + a * BN;
+        if (!(ok = mbar_wait(&tempty[a], a_phase, s_abort))) break;
+        tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 32 B of the swizzled rows a step
-            mma_e4m3(tmem + a * BN, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
-          mma_commit(&empty[s]);
-          mma_commit(&tfull[a]);
+        for (int k = 0; k < 4; ++k)  // 32 B of the swizzled rows a step
+          mma_e4m3(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+        mma_commit(&tfull[a]);
+        if (++s == S) {
+          s = 0;
+          phase ^= 1;
+        }
+        if (++a == NA) {
+          a = 0;
+          a_phase ^= 1;
         }
       }
       if (!ok) {
@@ -178,96 +342,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_error(p.err, kErrTimeout);
       }
     }
-  } else {
-    // ------------------------------------------------------------ accumulation and output
-    const int half = warp >> 2;                       // columns half * C .. of the tile
-    const int r = (warp & 3) * 32 + lane;             // row of the tile: TMEM lane
-    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * C;
-    long long it = 0;
-    bool ok = true;  // the same in a warp's lanes; a warp that gave up still takes part in the barriers below
-    for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      const int n0 = static_cast<int>(tile / m_tiles) * BN + half * C, t0 = static_cast<int>(tile % m_tiles) * kTileM;
-      const int row = t0 + r;
-      const float* xs = p.x_scale + static_cast<long long>(min(row, p.T - 1)) * p.ld_xs;
-      const float* ws = p.w_scale + static_cast<long long>(min(n0, p.N - 1) >> 7) * p.ld_ws;
-      uint64_t acc[C / 2];
-#pragma unroll
-      for (int i = 0; i < C / 2; ++i) acc[i] = 0;
-      float sx = __ldg(xs), sw = __ldg(ws);
-      for (int b = 0; b < blocks && ok; ++b, ++it) {
-        const float s = sx * sw;
-        if (b + 1 < blocks) {  // the next block's scales, under this block's product
-          sx = __ldg(xs + b + 1);
-          sw = __ldg(ws + b + 1);
-        }
-        const uint64_t s2 = pack_f32x2(s, s);
-        const int a = static_cast<int>(it % NA);
-        ok = __all_sync(0xffffffffu, mbar_wait(&tfull[a], static_cast<uint32_t>((it / NA) & 1), s_abort));
+   } else {
+    // ------------------------------------------------------------ scales
+    // Two warps bring the scales of four blocks at a time into shared memory: a
+    // load in flight in an accumulation warp would be waited for at its next
+    // barrier arrival (570 against 400 ns a block).
+    const int r0 = (warp - kAccWarps - 2) * 32 + lane;
+    long long g = 0;
+    bool ok = true;
+    for (long long tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      const int n0 = static_cast<int>(tile / m_tiles) * BN, t0 = static_cast<int>(tile % m_tiles) * kTileM;
+      const float* xs0 = p.x_scale + static_cast<long long>(min(t0 + r0, p.T - 1)) * p.ld_xs;
+      const float* xs1 = p.x_scale + static_cast<long long>(min(t0 + r0 + 64, p.T - 1)) * p.ld_xs;
+      const int nw = n0 + (warp - kAccWarps - 2) * C;  // lane 0: this column half's weight scales
+      const float* ws = p.w_scale + static_cast<long long>(min(nw, p.N - 1) >> 7) * p.ld_ws;
+      for (int b = 0; b < blocks; b += 4, ++g) {
+        const int s = static_cast<int>(g % SS);
+        ok = __all_sync(0xffffffffu, mbar_wait(&sempty[s], static_cast<uint32_t>((g / SS) & 1) ^ 1u, s_abort));
         if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < C; c += 16) {
-          uint32_t v[16];
-          tmem_ld32x16_async(taddr + a * BN + c, v);
-          tmem_wait_ld16(v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc[c / 2 + i] = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[c / 2 + i]);
-        }
-        tc_fence_before();
+        float* dst = reinterpret_cast<float*>(smem + Cfg::kOffScales + s * Cfg::kScaleBytes);
+        auto put = [&](int i, const float4& v) {
+          dst[i] = v.x;
+          dst[i + kTileM + 2] = v.y;
+          dst[i + 2 * (kTileM + 2)] = v.z;
+          dst[i + 3 * (kTileM + 2)] = v.w;
+        };
+        const float4 v0 = load_scales(xs0 + b, blocks - b, p.vec_scales), v1 = load_scales(xs1 + b, blocks - b, p.vec_scales);
+        if (lane == 0) put(kTileM + warp - kAccWarps - 2, load_scales(ws + b, blocks - b, p.vec_scales));
+        put(r0, v0);
+        put(r0 + 64, v1);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[a]);
-      }
-      // RoPE: the 64 columns below a head's end
-      float y[C];
-#pragma unroll
-      for (int i = 0; i < C / 2; ++i) {
-        const float2 f = unpack_f32x2(acc[i]);
-        y[2 * i] = f.x;
-        y[2 * i + 1] = f.y;
-      }
-      if (p.rope_head && (n0 + C) % p.rope_head == 0 && n0 < p.N) {
-        const int pos = __ldg(p.row_pos + min(row, p.T - 1));
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float sn, cs;
-          rope_angle(pos, p.turn[i], &sn, &cs);
-          const float u = y[C - 64 + 2 * i], v = y[C - 63 + 2 * i];
-          y[C - 64 + 2 * i] = u * cs - v * sn;
-          y[C - 63 + 2 * i] = u * sn + v * cs;
-        }
-      }
-      if (OUT == CSA2_OUT_FP8) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-          y[i] = finite_or_nan(y[i]);
-          m = fmaxf(m, fabsf(y[i]));
-        }
-        if (C == 64) {  // a block's two halves are in two warps
-          s_max[half * kTileM + r] = m;
-          named_bar_sync(1, kAccWarps * 32);
-          m = fmaxf(m, s_max[(half ^ 1) * kTileM + r]);
-          named_bar_sync(1, kAccWarps * 32);  // read before the next tile writes
-        }
-        float f;
-        const float sc = e4m3_block(m, &f);
-        if (ok && row < p.T && n0 < p.N) {
-          uint8_t* o = static_cast<uint8_t*>(p.out) + static_cast<long long>(row) * p.ld_out + n0;
-#pragma unroll
-          for (int i = 0; i < C; i += 16)
-            *reinterpret_cast<uint4*>(o + i) =
-                make_uint4(e4m3x4(y[i] * f, y[i + 1] * f, y[i + 2] * f, y[i + 3] * f),
-                           e4m3x4(y[i + 4] * f, y[i + 5] * f, y[i + 6] * f, y[i + 7] * f),
-                           e4m3x4(y[i + 8] * f, y[i + 9] * f, y[i + 10] * f, y[i + 11] * f),
-                           e4m3x4(y[i + 12] * f, y[i + 13] * f, y[i + 14] * f, y[i + 15] * f));
-          if (C == 128 || half == 0) p.out_scale[static_cast<long long>(row) * p.ld_os + (n0 >> 7)] = sc;
-        }
-      } else if (ok && row < p.T && n0 < p.N) {
-        store_row<OUT, C>(p, row, n0, y);
+        if (lane == 0) mbar_arrive(&sfull[s]);
       }
     }
     if (!ok) {
+      *s_abort = 1;
+      set_error(p.err, kErrTimeout);
+    }
+   }
+  } else {
+    regs_accumulate();
+    if (!accumulate_and_store<BN, OUT>(map_out, p, smem, tmem, tfull, tempty, empty, sfull, sempty, s_abort)) {
       *s_abort = 1;
       set_error(p.err, kErrTimeout);
     }
@@ -283,9 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int BN, int OUT>
 cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, const DeviceCtx& ctx, cudaStream_t st,
                         const char** why) {
-  CUtensorMap map_x, map_w;
+  CUtensorMap map_x, map_w, map_out = {};
   if (encode_tmap_2d_u8(&map_x, a.x, a.K, a.T, a.ld_x, kBlockK, kTileM) != CUDA_SUCCESS ||
-      encode_tmap_2d_u8(&map_w, a.w, a.K, a.N, a.ld_w, kBlockK, BN) != CUDA_SUCCESS) {
+      encode_tmap_2d_u8(&map_w, a.w, a.K, a.N, a.ld_w, kBlockK, BN) != CUDA_SUCCESS ||
+      (p.vec && encode_tmap_2d_u8(&map_out, a.out, static_cast<uint64_t>(a.N) * out_size(OUT), a.T,
+                                  a.ld_out * out_size(OUT), 64, 32, CU_TENSOR_MAP_SWIZZLE_64B) != CUDA_SUCCESS)) {
     *why = "csa2_fp8_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
   }
@@ -294,7 +411,7 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
   if (e != cudaSuccess) return e;
   const long long tiles = ((static_cast<long long>(a.T) + kTileM - 1) / kTileM) * ((static_cast<long long>(a.N) + BN - 1) / BN);
   const unsigned grid = static_cast<unsigned>(tiles < ctx.num_sms ? tiles : ctx.num_sms);
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), WideCfg<BN>::kSmem, st, map_x, map_w, p);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), WideCfg<BN>::kSmem, st, map_x, map_w, map_out, p);
 }
 
 }  // namespace
@@ -314,8 +431,9 @@ cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ct
   p.N = a.N;
   p.K = a.K;
   p.rope_head = a.rope_head;
-  const int size = a.out_format == CSA2_OUT_F32 ? 4 : (a.out_format == CSA2_OUT_BF16 ? 2 : 1);
-  p.vec = (a.ld_out * size) % 16 == 0;
+  p.vec = (a.ld_out * out_size(a.out_format)) % 16 == 0;
+  p.vec_scales = (reinterpret_cast<uintptr_t>(a.x_scale) | reinterpret_cast<uintptr_t>(a.w_scale)) % 16 == 0 &&
+                 a.ld_x_scale % 4 == 0 && a.ld_w_scale % 4 == 0;
   p.w_ready = a.w_ready;
   p.err = ctx.err;
   if (a.rope_head) {
@@ -323,9 +441,9 @@ cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ct
     for (int i = 0; i < 32; ++i) p.turn[i] = rope_turn_rate(theta, i);
   }
   switch (a.out_format) {
-    case CSA2_OUT_F32: return launch_wide<128, CSA2_OUT_F32>(a, p, ctx, st, why);
-    case CSA2_OUT_BF16: return launch_wide<128, CSA2_OUT_BF16>(a, p, ctx, st, why);
-    default: return launch_wide<128, CSA2_OUT_FP8>(a, p, ctx, st, why);
+    case CSA2_OUT_F32: return launch_wide<256, CSA2_OUT_F32>(a, p, ctx, st, why);
+    case CSA2_OUT_BF16: return launch_wide<256, CSA2_OUT_BF16>(a, p, ctx, st, why);
+    default: return launch_wide<256, CSA2_OUT_FP8>(a, p, ctx, st, why);
   }
 }
 

@@ -73,6 +73,7 @@ def _linear(**kw):
 @pytest.mark.parametrize("kw,code,word", [
     ({"x": None}, 1, b"NULL"), ({"x_scale": None}, 1, b"NULL"), ({"w": None}, 1, b"NULL"), ({"w_scale": None}, 1, b"NULL"),
     ({"out": None}, 1, b"NULL"), ({"T": 0}, 2, b"T=0"), ({"N": 0}, 2, b"N=0"), ({"N": -5}, 2, b"N=-5"),
+    ({"N": (1 << 28) + 1, "ld_out": 1 << 29}, 2, b"2^28"),
     ({"K": 8}, 2, b"K=8"), ({"K": 264}, 2, b"K=264"), ({"K": 65552, "ld_x": 65552, "ld_w": 65552}, 2, b"K=65552"),
     ({"ld_x": 240}, 2, b"stride"), ({"ld_w": 240}, 2, b"stride"), ({"ld_out": 511}, 2, b"stride"),
     ({"ld_x_scale": 1}, 2, b"stride"), ({"ld_w_scale": 1}, 2, b"stride"), ({"ld_x": 1 << 39}, 2, b"2^39"),
