@@ -9,6 +9,8 @@
 // output tiles of 128 rows x BN columns (persistent grid).
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "csa2_device.cuh"
 #include "csa2_e4m3.cuh"
 #include "csa2_internal.h"
@@ -200,31 +202,38 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
       if (row < p.T) p.out_scale[static_cast<long long>(row) * p.ld_os + (n0 >> 7)] = sc;
     }
     constexpr int kSize = out_size(OUT), kPieces = C * kSize / 16;
-    if (p.vec) {
-      // 32 rows x 64 B at a time through shared memory (swizzled, so that the
-      // lanes' 16-byte stores do not collide) and out by a tensor store
+    // 32 rows x 64 B at a time through shared memory (swizzled, so that the lanes'
+    // 16-byte stores do not collide) and out by a tensor store; rows that are not
+    // 16-byte aligned (never e4m3) element by element, a row's 64 B by one half warp or
+    // warp
 #pragma unroll
-      for (int c = 0; c < kPieces; c += 4) {
-        if (lane == 0) bulk_wait_read();
-        __syncwarp();
+    for (int c = 0; c < kPieces; c += 4) {
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(s_out + lane * 64 + ((i ^ ((lane >> 1) & 3)) * 16)) = out_piece<OUT, C>(y, c + i, f);
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(s_out + lane * 64 + ((i ^ ((lane >> 1) & 3)) * 16)) = out_piece<OUT, C>(y, c + i, f);
+      const int x = n0 * kSize + c * 16;  // byte of the output row
+      if (p.vec) {
         fence_proxy_async_smem();
         __syncwarp();
-        const int x = n0 * kSize + c * 16;
         if (lane == 0 && x < p.N * kSize) {
           tma_store_2d(&map_out, s_out, x, t0 + (warp & 3) * 32);
           bulk_commit();
         }
-      }
-    } else if (row < p.T) {  // rows that are not 16-byte aligned (never e4m3)
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        if (n0 + i >= p.N) continue;
-        const long long at = static_cast<long long>(row) * p.ld_out + n0 + i;
-        if (OUT == CSA2_OUT_F32) static_cast<float*>(p.out)[at] = y[i];
-        else if (OUT == CSA2_OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y[i]);
+      } else if (OUT != CSA2_OUT_FP8) {
+        __syncwarp();
+        constexpr int kEl = 64 / kSize;  // elements of a row here
+        const int e = lane % kEl, n = x / kSize + e;
+#pragma unroll 4
+        for (int q = lane / kEl; q < 32; q += 32 / kEl) {
+          const uint8_t* src = s_out + q * 64 + (((e * kSize / 16) ^ ((q >> 1) & 3)) * 16) + e * kSize % 16;
+          const long long at = static_cast<long long>(t0 + (warp & 3) * 32 + q) * p.ld_out + n;
+          if (t0 + (warp & 3) * 32 + q < p.T && n < p.N) {
+            if (OUT == CSA2_OUT_F32) static_cast<float*>(p.out)[at] = *reinterpret_cast<const float*>(src);
+            else static_cast<uint16_t*>(p.out)[at] = *reinterpret_cast<const uint16_t*>(src);
+          }
+        }
       }
     }
   }
@@ -414,6 +423,341 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
   return launch_pdl(kern, dim3(grid), dim3(kThreads), WideCfg<BN>::kSmem, st, map_x, map_w, map_out, p);
 }
 
+// ---------------------------------------------------------------- few rows
+// Up to a few hundred rows the weights are what is read, so they take the M side
+// of the product: a CTA has 128 output columns (one block of weight scales) by
+// NT rows of x, and a cluster of CTAs splits the input dims and adds its parts
+// through distributed shared memory, in rank order.  Warps: 0 TMA producer, 1
+// MMA issuer, 2..9 accumulation (a lane is an output column; two groups of four
+// take the blocks in turn), all of them the output (a warp is a row of x).
+constexpr int kNarrowThreads = 320;
+constexpr int kScaleSeg = 32;  // blocks whose scales are staged at a time
+
+template <int NT>
+struct NarrowCfg {
+  static constexpr int kStages = 4;
+  static constexpr int kStageBytes = (128 + NT) * kBlockK;
+  static constexpr int kAccs = 4;
+  static constexpr int kCols = kAccs * NT < 32 ? 32 : kAccs * NT;
+  static constexpr int kOffScales = kStages * kStageBytes;  // the parts [NT][128] reuse the stages
+  static constexpr int kOffBars = kOffScales + kScaleSeg * NT * 4;
+  static constexpr int kSmem = 1024 + kOffBars + 256;
+  static_assert(NT * 128 * 4 <= kOffScales, "the parts fit the stages");
+};
+
+template <int NT, int OUT>
+__global__ void __launch_bounds__(kNarrowThreads)
+    fp8_linear_narrow_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                             const __grid_constant__ LinearParams p) {
+  using Cfg = NarrowCfg<NT>;
+  constexpr int S = Cfg::kStages, NA = Cfg::kAccs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBars);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + NA;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + NA);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * 128, t0 = blockIdx.y * NT;
+  const int splits = gridDim.z, rank = blockIdx.z;
+  const int all = (p.K + kBlockK - 1) / kBlockK;
+  const int b0 = all * rank / splits, blocks = all * (rank + 1) / splits - b0;
+  const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+
+  if (threadIdx.x == 0) {
+    *s_abort = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < NA; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 4);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&map_x);
+    prefetch_tmap(&map_w);
+    if (p.w_ready) {  // the first weights do not wait for the previous launch
+      for (int b = 0; b < min(S, blocks); ++b) {
+        mbar_arrive_expect_tx(&full[b], Cfg::kStageBytes);
+        tma_load_2d(smem + b * Cfg::kStageBytes, &map_w, (b0 + b) * kBlockK, n0, &full[b], pol_w);
+      }
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, Cfg::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();  // every CTA holds its TMEM
+  const uint32_t tmem = *s_tmem;
+
+  bool ok = true;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int b = 0;
+      for (; b < blocks; ++b) {
+        const int s = b % S;
+        if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
+        uint8_t* dst = smem + s * Cfg::kStageBytes;
+        if (b >= S || !p.w_ready) {
+          mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+          tma_load_2d(dst, &map_w, (b0 + b) * kBlockK, n0, &full[s], pol_w);
+        }
+        tma_load_2d(dst + 128 * kBlockK, &map_x, (b0 + b) * kBlockK, t0, &full[s], pol_x);
+      }
+      if (!ok) {
+        *s_abort = 1;
+        set_error(p.err, kErrTimeout);
+      }
+      // the copies must land before shared memory is reused
+      for (int i = (b > S ? b - S : 0); i < b; ++i) mbar_wait(&full[i % S], static_cast<uint32_t>(i / S) & 1u, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(128, NT);
+      for (int b = 0; b < blocks; ++b) {
+        const int s = b % S, a = b % NA;
+        if (!(ok = mbar_wait(&full[s], static_cast<uint32_t>(b / S) & 1u, s_abort))) break;
+        if (b >= NA && !(ok = mbar_wait(&tempty[a], static_cast<uint32_t>(b / NA - 1) & 1u, s_abort))) break;
+        tc_fence_after();
+        const uint64_t wd = smem_desc_sw128(smem + s * Cfg::kStageBytes);
+        const uint64_t xd = smem_desc_sw128(smem + s * Cfg::kStageBytes + 128 * kBlockK);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_e4m3(tmem + a * NT, wd + 2 * k, xd + 2 * k, idesc, k > 0 ? 1u : 0u);
+        mma_commit(&tfull[a]);
+      }
+      if (!ok) {
+        *s_abort = 1;
+        set_error(p.err, kErrTimeout);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ accumulation
+    const int quad = warp & 3, group = (warp - 2) >> 2;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    float* s_scale = reinterpret_cast<float*>(smem + Cfg::kOffScales);  // [block][NT]: both scales
+    const float* ws = p.w_scale + static_cast<long long>(n0 >> 7) * p.ld_ws + b0;
+    const int tid = threadIdx.x - 64;
+    uint64_t acc[NT / 2];
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) acc[i] = 0;
+    for (int seg = 0; seg < blocks; seg += kScaleSeg) {
+      const int n = min(kScaleSeg, blocks - seg);
+      if (seg > 0) named_bar_sync(1, 256);  // the last segment has been used
+      for (int i = tid; i < n * NT; i += 256) {
+        const int t = i / n, b = i - t * n;
+        s_scale[b * NT + t] = t0 + t < p.T ? __ldg(p.x_scale + (t0 + t) * p.ld_xs + b0 + seg + b) * __ldg(ws + seg + b) : 0.f;
+      }
+      named_bar_sync(1, 256);
+      for (int j = group; j < n && ok; j += 2) {  // kScaleSeg is even: a group keeps its blocks' parity
+        const int b = seg + j, a = b % NA;
+        ok = __all_sync(0xffffffffu, mbar_wait(&tfull[a], static_cast<uint32_t>(b / NA) & 1u, s_abort));
+        if (!ok) break;
+        tc_fence_after();
+        if (quad == 0 && lane == 0) mbar_arrive(&empty[b % S]);  // the products have read the stage
+        uint32_t v[NT / 16][16];
+#pragma unroll
+        for (int c = 0; c < NT / 16; ++c) tmem_ld32x16_async(taddr + a * NT + c * 16, v[c]);
+#pragma unroll
+        for (int c = 0; c < NT / 16; ++c) tmem_wait_ld16(v[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[a]);
+        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s_scale + j * NT);
+#pragma unroll
+        for (int i = 0; i < NT / 4; ++i) {
+          const ulonglong2 m = sc[i];
+          const uint32_t* q = &v[i / 4][(i % 4) * 4];
+          acc[2 * i] = fma_f32x2(pack_f32x2(__uint_as_float(q[0]), __uint_as_float(q[1])), m.x, acc[2 * i]);
+          acc[2 * i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(q[2]), __uint_as_float(q[3])), m.y, acc[2 * i + 1]);
+        }
+      }
+    }
+    if (!ok) {
+      *s_abort = 1;
+      set_error(p.err, kErrTimeout);
+    }
+    // every product is complete (or given up), so the stages hold the parts now
+    float* part = reinterpret_cast<float*>(smem) + quad * 32 + lane;
+    named_bar_sync(1, 256);
+    if (ok && group == 0) {
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i) {
+        const float2 f = unpack_f32x2(acc[i]);
+        part[(2 * i) * 128] = f.x;
+        part[(2 * i + 1) * 128] = f.y;
+      }
+    }
+    named_bar_sync(1, 256);
+    if (ok && group == 1) {
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i) {
+        const float2 f = unpack_f32x2(acc[i]);
+        part[(2 * i) * 128] += f.x;
+        part[(2 * i + 1) * 128] += f.y;
+      }
+    }
+  }
+  __syncthreads();
+  if (splits > 1) cluster_sync();
+  // ------------------------------------------------------------ output: a warp takes a row
+  if (!*s_abort) {
+    for (int t = rank + splits * warp; t < NT && t0 + t < p.T; t += splits * (kNarrowThreads / 32)) {
+      const uint32_t at = smem_u32(reinterpret_cast<float*>(smem) + t * 128 + lane * 4);
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < splits; ++r) {
+        float4 v;
+        if (splits > 1) {
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                       : "r"(map_rank(at, static_cast<uint32_t>(r))));
+        } else {
+          v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + t * 128 + lane * 4);
+        }
+        y[0] += v.x;
+        y[1] += v.y;
+        y[2] += v.z;
+        y[3] += v.w;
+      }
+      const long long row = t0 + t;
+      if (p.rope_head && (n0 + 128) % p.rope_head == 0 && lane >= 16) {
+        const int pos = __ldg(p.row_pos + row);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float sn, cs;
+          rope_angle(pos, p.turn[(lane - 16) * 2 + h], &sn, &cs);
+          const float u = y[2 * h], w = y[2 * h + 1];
+          y[2 * h] = u * cs - w * sn;
+          y[2 * h + 1] = u * sn + w * cs;
+        }
+      }
+      const int n = n0 + lane * 4;
+      if (OUT == CSA2_OUT_FP8) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[i] = finite_or_nan(y[i]);
+          m = fmaxf(m, fabsf(y[i]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float f;
+        const float sc = e4m3_block(m, &f);
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row * p.ld_out + n) =
+            e4m3x4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+        if (lane == 0) p.out_scale[row * p.ld_os + (n0 >> 7)] = sc;
+      } else if (OUT == CSA2_OUT_F32) {
+        float* o = static_cast<float*>(p.out) + row * p.ld_out + n;
+        if (p.vec && n + 4 <= p.N) {
+          *reinterpret_cast<float4*>(o) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) o[i] = y[i];
+        }
+      } else {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + n;
+        if (p.vec && n + 4 <= p.N) {
+          *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) o[i] = __float2bfloat16_rn(y[i]);
+        }
+      }
+    }
+  }
+  if (splits > 1) cluster_sync();  // no CTA leaves while its part may still be read
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kCols);
+  }
+}
+
+// Clusters of `splits` CTAs that run at once on the device (asked of the runtime
+// once a device, kernel and size).
+template <int NT, int OUT>
+int narrow_clusters(const cudaLaunchConfig_t& cfg, int splits, int device) {
+  static std::atomic<int> known[64][5];
+  int i = 0;
+  while ((1 << i) < splits) ++i;
+  int n = known[device][i].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_linear_narrow_kernel<NT, OUT>, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      n = -1;
+    }
+    if (n == 0) n = -1;
+    known[device][i].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Launches the few-rows kernel, or sets *taken to false where its CTAs would not
+// all run at once and the rows are enough for 128 x 256 tiles.
+template <int NT, int OUT>
+cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, const DeviceCtx& ctx, cudaStream_t st,
+                          const char** why, bool* taken) {
+  auto kern = fp8_linear_narrow_kernel<NT, OUT>;
+  const long long n_tiles = (static_cast<long long>(a.N) + 127) / 128;
+  const int t_tiles = (a.T + NT - 1) / NT, blocks = (a.K + 127) / 128;
+  *taken = NT < 64 || n_tiles * t_tiles <= ctx.num_sms;
+  if (!*taken) return cudaSuccess;
+  cudaError_t e = prefer_max_smem(kern, NarrowCfg<NT>::kSmem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kNarrowThreads);
+  cfg.dynamicSmemBytes = NarrowCfg<NT>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  // The largest split whose clusters all run at once and whose CTAs keep two
+  // blocks each.
+  int splits = 16;
+  for (; splits > 1; splits >>= 1) {
+    cfg.gridDim = dim3(static_cast<unsigned>(n_tiles), t_tiles, splits);
+    attr[1].val.clusterDim.z = splits;
+    if (2 * splits <= blocks && n_tiles * t_tiles <= narrow_clusters<NT, OUT>(cfg, splits, ctx.device)) break;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(n_tiles), t_tiles, splits);
+  attr[1].val.clusterDim.z = splits;
+  CUtensorMap map_x, map_w;
+  if (encode_tmap_2d_u8(&map_x, a.x, a.K, a.T, a.ld_x, kBlockK, NT) != CUDA_SUCCESS ||
+      encode_tmap_2d_u8(&map_w, a.w, a.K, a.N, a.ld_w, kBlockK, 128) != CUDA_SUCCESS) {
+    *why = "csa2_fp8_linear: a tensor map could not be encoded";
+    return cudaErrorInvalidValue;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, p);
+}
+
+template <int OUT>
+cudaError_t launch_out(const csa2_fp8_linear_args& a, const LinearParams& p, const DeviceCtx& ctx, cudaStream_t st,
+                       const char** why) {
+  bool taken = false;
+  cudaError_t e = a.T <= 16   ? launch_narrow<16, OUT>(a, p, ctx, st, why, &taken)
+                  : a.T <= 32 ? launch_narrow<32, OUT>(a, p, ctx, st, why, &taken)
+                              : launch_narrow<64, OUT>(a, p, ctx, st, why, &taken);
+  if (e != cudaSuccess || taken) return e;
+  return launch_wide<256, OUT>(a, p, ctx, st, why);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ctx, cudaStream_t st, const char** why) {
@@ -441,9 +785,9 @@ cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ct
     for (int i = 0; i < 32; ++i) p.turn[i] = rope_turn_rate(theta, i);
   }
   switch (a.out_format) {
-    case CSA2_OUT_F32: return launch_wide<256, CSA2_OUT_F32>(a, p, ctx, st, why);
-    case CSA2_OUT_BF16: return launch_wide<256, CSA2_OUT_BF16>(a, p, ctx, st, why);
-    default: return launch_wide<256, CSA2_OUT_FP8>(a, p, ctx, st, why);
+    case CSA2_OUT_F32: return launch_out<CSA2_OUT_F32>(a, p, ctx, st, why);
+    case CSA2_OUT_BF16: return launch_out<CSA2_OUT_BF16>(a, p, ctx, st, why);
+    default: return launch_out<CSA2_OUT_FP8>(a, p, ctx, st, why);
   }
 }
 
