@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -134,11 +135,10 @@ def load(build_if_missing: bool = False) -> C.CDLL:
     lib.csa2_check_device_error.argtypes = [_P]
     lib.csa2_kv_project.restype = C.c_int
     lib.csa2_kv_project.argtypes = [C.POINTER(KvProjectArgs), _P]
-    for name, st in (("csa2_quant_fp8", QuantFp8Args), ("csa2_fp8_linear", Fp8LinearArgs),
-                     ("csa2_batch_plan", BatchPlanArgs)):
+    for name in ("csa2_quant_fp8", "csa2_fp8_linear", "csa2_batch_plan"):
         f = getattr(lib, name)
         f.restype = C.c_int
-        f.argtypes = [C.POINTER(st), _P]
+        f.argtypes = [_P, _P]   # the packed struct or a pointer to one
     lib.csa2_debug_bounded_wait.restype = C.c_int
     lib.csa2_debug_bounded_wait.argtypes = [C.c_uint32, _P]
     _lib = lib
@@ -304,58 +304,81 @@ def kv_project(hidden, w, out, stream=None):
 
 
 _EMPTY = 16  # stands for a given tensor without elements (its data_ptr is 0); the length 0 goes along
+_Tensor = torch.Tensor
+_BF16, _F32, _U8, _INT32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
-def _mat(t, name: str, dtype, rows: int | None = None, cols: int | None = None):
-    """(pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous (the rows may be apart)."""
-    if not isinstance(t, torch.Tensor):
+def _packer(st):
+    """Packs a struct's fields in order into bytes (a fifth of the time of filling the ctypes struct)."""
+    code = {_P: "P", _I32: "i", _I64: "q", C.c_float: "f"}
+    fmt = "@" + "".join(code[f[1]] for f in st._fields_)
+    pad = C.sizeof(st) - struct.calcsize(fmt)
+    return struct.Struct(fmt + "x" * pad).pack
+
+
+_pack_quant, _pack_linear, _pack_plan = _packer(QuantFp8Args), _packer(Fp8LinearArgs), _packer(BatchPlanArgs)
+
+
+def _device(t, name: str) -> int:
+    """Device of a call's first tensor."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name}: CSA2 calls take CUDA tensors (no CPU path)")
+    return dev
+
+
+def _check_tensor(t, name: str, dtype, dev: int):
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
-        raise ValueError(f"{name}: expected a 2-D tensor with contiguous rows")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name}: expected shape [{rows}, {cols}], got {list(t.shape)}")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if ld < t.shape[1]:
-        raise ValueError(f"{name}: its rows overlap (row stride {ld})")
+    if t.get_device() < 0:
+        raise ValueError(f"{name}: CSA2 calls take CUDA tensors (no CPU path)")
+    raise ValueError(f"{name}: on cuda:{t.get_device()}, the call's first tensor on cuda:{dev}")
+
+
+def _mat(t, name: str, dtype, dev: int, rows, cols):
+    """(pointer, row stride) of a 2-D tensor [rows, cols] whose rows are contiguous (the
+    rows may be apart); rows or cols None: any."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _check_tensor(t, name, dtype, dev)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got {list(shape)}")
+    n, m = shape
+    if (rows is not None and n != rows) or (cols is not None and m != cols):
+        raise ValueError(f"{name}: expected shape [{rows}, {cols}], got {[n, m]}")
+    ld, step = t.stride()
+    if n <= 1:
+        ld = m
+    if (step != 1 and m > 1) or ld < m:
+        raise ValueError(f"{name}: expected contiguous rows that do not overlap, got strides {t.stride()}")
     return t.data_ptr() or _EMPTY, ld
 
 
-def _vec(t, name: str, dtype, n: int | None = None) -> int | None:
-    """Pointer of a contiguous 1-D CUDA tensor of n elements (None stays None)."""
+def _vec(t, name: str, dtype, dev: int, n=None) -> int:
+    """Pointer of a contiguous 1-D tensor of n elements (0 for None)."""
     if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: CSA2 calls take CUDA tensors (no CPU path)")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 1 or not t.is_contiguous():
+        return 0
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _check_tensor(t, name, dtype, dev)
+    shape = t.shape
+    if len(shape) != 1 or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous 1-D tensor")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name}: expected {n} elements, got {t.shape[0]}")
+    if n is not None and shape[0] != n:
+        raise ValueError(f"{name}: expected {n} elements, got {shape[0]}")
     return t.data_ptr() or _EMPTY
 
 
-def _call(fn, args, where: str, stream, *tensors):
-    """Issues a call on the tensors' device: all of them on one, its current
-    stream unless one is given."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.get_device()
-            elif t.get_device() != dev:
-                raise ValueError(f"{where}: its tensors are on different devices")
-    if dev == torch.cuda.current_device():
-        rc = fn(C.byref(args), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+def _issue(fn, packed: bytes, where: str, dev: int, stream):
+    """Issues a call on its tensors' device: the device's current stream unless one is given."""
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(packed, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
-            rc = fn(C.byref(args), _stream(stream))
+            rc = fn(packed, _stream(stream))
     if rc != 0:
         _check(rc, where)
 
@@ -364,17 +387,17 @@ def quant_fp8(x, codes, scale, gamma=None, eps=1e-6, block_rows=1, stream=None):
     """e4m3 codes of x [T,K] bf16 with a fp32 scale per 128 columns of a row (block_rows=1;
     with gamma [K] of the row's RMSNorm) or per 128 x 128 tile (block_rows=128, weights):
     codes uint8 [T,K], scale [ceil(T/block_rows), ceil(K/128)] (csa2_quant_fp8)."""
-    lib = load()
-    px, ldx = _mat(x, "x", torch.bfloat16)
+    dev = _device(x, "x")
+    px, ldx = _mat(x, "x", _BF16, dev, None, None)
     T, K = x.shape
-    pc, ldc = _mat(codes, "codes", torch.uint8, T, K)
-    ps, lds = _mat(scale, "scale", torch.float32, T if block_rows == 1 else (T + 127) // 128, (K + 127) // 128)
-    a = QuantFp8Args(px, ldx, T, K, block_rows, _vec(gamma, "gamma", torch.float32, K), eps, pc, ldc, ps, lds)
-    _call(lib.csa2_quant_fp8, a, "csa2_quant_fp8", stream, x, codes, scale, gamma)
+    pc, ldc = _mat(codes, "codes", _U8, dev, T, K)
+    ps, lds = _mat(scale, "scale", _F32, dev, T if block_rows == 1 else (T + 127) // 128, (K + 127) // 128)
+    _issue(load().csa2_quant_fp8, _pack_quant(px, ldx, T, K, block_rows, _vec(gamma, "gamma", _F32, dev, K), eps, pc, ldc,
+                                              ps, lds), "csa2_quant_fp8", dev, stream)
 
 
 OUT_F32, OUT_BF16, OUT_FP8 = 0, 1, 2
-_OUT_FORMAT = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.uint8: OUT_FP8}
+_OUT_FORMAT = {_F32: OUT_F32, _BF16: OUT_BF16, _U8: OUT_FP8}
 
 
 def fp8_linear(x, x_scale, w, w_scale, out, out_scale=None, row_pos=None, rope_head=0, rope_theta=0.0, w_ready=False,
@@ -383,30 +406,36 @@ def fp8_linear(x, x_scale, w, w_scale, out, out_scale=None, row_pos=None, rope_h
     [T,ceil(K/128)], w_scale [ceil(N/128),ceil(K/128)].  out fp32, bf16, or uint8 codes with
     out_scale [T,N/128]; rope_head turns the last 64 columns of every head of that many
     columns by row_pos [T] (csa2_fp8_linear)."""
-    lib = load()
-    px, ldx = _mat(x, "x", torch.uint8)
+    dev = _device(x, "x")
+    px, ldx = _mat(x, "x", _U8, dev, None, None)
     T, K = x.shape
-    pw, ldw = _mat(w, "w", torch.uint8, None, K)
+    pw, ldw = _mat(w, "w", _U8, dev, None, K)
     N = w.shape[0]
     nb = (K + 127) // 128
-    pxs, ldxs = _mat(x_scale, "x_scale", torch.float32, T, nb)
-    pws, ldws = _mat(w_scale, "w_scale", torch.float32, (N + 127) // 128, nb)
-    fmt = _OUT_FORMAT.get(out.dtype)
+    pxs, ldxs = _mat(x_scale, "x_scale", _F32, dev, T, nb)
+    pws, ldws = _mat(w_scale, "w_scale", _F32, dev, (N + 127) // 128, nb)
+    kind = out.dtype
+    fmt = _OUT_FORMAT.get(kind)
     if fmt is None:
-        raise TypeError(f"out: expected float32, bfloat16 or uint8, got {out.dtype}")
-    po, ldo = _mat(out, "out", out.dtype, T, N)
-    pos, ldos = (None, 0) if out_scale is None else _mat(out_scale, "out_scale", torch.float32, T, N // 128)
-    a = Fp8LinearArgs(px, ldx, pxs, ldxs, pw, ldw, pws, ldws, T, N, K, fmt, po, ldo, pos, ldos,
-                      _vec(row_pos, "row_pos", torch.int32, T), rope_head, rope_theta, 1 if w_ready else 0)
-    _call(lib.csa2_fp8_linear, a, "csa2_fp8_linear", stream, x, x_scale, w, w_scale, out, out_scale, row_pos)
+        raise TypeError(f"out: expected float32, bfloat16 or uint8, got {kind}")
+    po, ldo = _mat(out, "out", kind, dev, T, N)
+    pos, ldos = (0, 0) if out_scale is None else _mat(out_scale, "out_scale", _F32, dev, T, N // 128)
+    _issue(load().csa2_fp8_linear,
+           _pack_linear(px, ldx, pxs, ldxs, pw, ldw, pws, ldws, T, N, K, fmt, po, ldo, pos, ldos,
+                        _vec(row_pos, "row_pos", _INT32, dev, T), rope_head, rope_theta, 1 if w_ready else 0),
+           "csa2_fp8_linear", dev, stream)
 
 
-def _cap(**arrays) -> int:
-    """The one length of the given arrays (0 when none is given)."""
-    sizes = {k: t.shape[0] for k, t in arrays.items() if t is not None}
-    if len(set(sizes.values())) > 1:
-        raise ValueError(f"these arrays must have one length: {sizes}")
-    return next(iter(sizes.values()), 0)
+def _one_length(*arrays) -> int:
+    """The one length of the (name, tensor) pairs whose tensor is given (0 when none is)."""
+    n = -1
+    for name, t in arrays:
+        if t is not None:
+            m = t.shape[0]
+            if n >= 0 and m != n:
+                raise ValueError(f"{name}: {m} places, the other arrays of its kind have {n}")
+            n = m
+    return max(n, 0)
 
 
 def batch_plan(ctx_len, new_len, ratio_m=1, page_table=None, free_pages=None, free_head=None, free_head_out=None,
@@ -417,28 +446,28 @@ def batch_plan(ctx_len, new_len, ratio_m=1, page_table=None, free_pages=None, fr
     new_len [B] more (csa2_batch_plan).  Every output is optional, int32, and written in
     place; row arrays share one length (rows the step may have), entry arrays another;
     page_table [B, pages] is extended from free_pages when that is given."""
-    lib = load()
-    i32 = torch.int32
+    dev = _device(ctx_len, "ctx_len")
+
+    def vec(t, name, n=None):
+        return 0 if t is None else _vec(t, name, _INT32, dev, n)
+
+    ctx = vec(ctx_len, "ctx_len")
     B = ctx_len.shape[0]
-    pt, ldp = (None, 0) if page_table is None else _mat(page_table, "page_table", i32, B)
-    if page_table is not None and ldp != page_table.shape[1]:
+    pt, ldp = (0, 0) if page_table is None else _mat(page_table, "page_table", _INT32, dev, B, None)
+    if pt and ldp != page_table.shape[1]:
         raise ValueError("page_table: expected a contiguous tensor")
-    ss, lds = (None, 0) if swa_slot is None else _mat(swa_slot, "swa_slot", i32)
-    a = BatchPlanArgs(
-        B, _vec(ctx_len, "ctx_len", i32), _vec(new_len, "new_len", i32, B), ratio_m, pt, ldp,
-        _vec(free_pages, "free_pages", i32), 0 if free_pages is None else free_pages.shape[0],
-        _vec(free_head, "free_head", i32, 1), _vec(free_head_out, "free_head_out", i32, 1),
-        _vec(row_start, "row_start", i32, B + 1), _vec(n_visible, "n_visible", i32, B),
-        _vec(entry_start, "entry_start", i32, B + 1),
-        _cap(row_seq=row_seq, row_pos=row_pos, swa_new=swa_new, swa_slot=swa_slot),
-        _vec(row_seq, "row_seq", i32), _vec(row_pos, "row_pos", i32),
-        _cap(entry_slot=entry_slot, entry_pos=entry_pos, entry_row=entry_row),
-        _vec(entry_slot, "entry_slot", i32), _vec(entry_pos, "entry_pos", i32), _vec(entry_row, "entry_row", i32),
-        swa_ring, _vec(ring_id, "ring_id", i32, B), _vec(swa_new, "swa_new", i32), ss,
-        0 if swa_slot is None else swa_slot.shape[1], lds, 1 if pad else 0)
-    _call(lib.csa2_batch_plan, a, "csa2_batch_plan", stream, ctx_len, new_len, page_table, free_pages, free_head,
-          free_head_out, row_start, n_visible, entry_start, row_seq, row_pos, entry_slot, entry_pos, entry_row, ring_id,
-          swa_new, swa_slot)
+    ss, lds = (0, 0) if swa_slot is None else _mat(swa_slot, "swa_slot", _INT32, dev, None, None)
+    _issue(load().csa2_batch_plan, _pack_plan(
+        B, ctx, vec(new_len, "new_len", B), ratio_m, pt, ldp,
+        vec(free_pages, "free_pages"), 0 if free_pages is None else free_pages.shape[0],
+        vec(free_head, "free_head", 1), vec(free_head_out, "free_head_out", 1),
+        vec(row_start, "row_start", B + 1), vec(n_visible, "n_visible", B), vec(entry_start, "entry_start", B + 1),
+        _one_length(("row_seq", row_seq), ("row_pos", row_pos), ("swa_new", swa_new), ("swa_slot", swa_slot)),
+        vec(row_seq, "row_seq"), vec(row_pos, "row_pos"),
+        _one_length(("entry_slot", entry_slot), ("entry_pos", entry_pos), ("entry_row", entry_row)),
+        vec(entry_slot, "entry_slot"), vec(entry_pos, "entry_pos"), vec(entry_row, "entry_row"),
+        swa_ring, vec(ring_id, "ring_id", B), vec(swa_new, "swa_new"), ss, 0 if swa_slot is None else swa_slot.shape[1],
+        lds, 1 if pad else 0), "csa2_batch_plan", dev, stream)
 
 
 def check_device_error(stream=None) -> int:

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(const __grid_c
 cudaError_t launch_batch_plan(const csa2_batch_plan_args& a, const DeviceCtx& ctx, cudaStream_t st) {
   PlanParams p{a, ctx.err};
   const size_t smem = (static_cast<size_t>(a.B) * 4 + 3) * sizeof(int);
-  cudaError_t e = prefer_max_smem(batch_plan_kernel, smem);
+  cudaError_t e = prefer_max_smem_once<batch_plan_kernel>(ctx.device, (kPlanMaxSeqs * 4 + 3) * sizeof(int));
   if (e != cudaSuccess) return e;
   // four rows a warp; the sums are made in every CTA, so no more CTAs than four an SM
   long long grid = (static_cast<long long>(a.max_rows) + 31) / 32;

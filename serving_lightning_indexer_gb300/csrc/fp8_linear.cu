@@ -5,11 +5,9 @@
 // accumulator of its own: four tcgen05.mma (K = 32 each) into one slot of a TMEM
 // ring, from which the accumulation warps take it, times the two scales, into
 // fp32 registers while the tensor core works on the next block.  Warp roles:
-// eight accumulation warps, one TMA producer, one MMA issuer.  A CTA walks
+// eight accumulation warps, a TMA producer, two MMA issuers, one warp for the scales.  A CTA walks
 // output tiles of 128 rows x BN columns (persistent grid).
 #include <cuda_bf16.h>
-
-#include <atomic>
 
 #include "csa2_device.cuh"
 #include "csa2_e4m3.cuh"
@@ -22,7 +20,7 @@ namespace {
 constexpr int kTileM = 128;   // rows of x a tile
 constexpr int kBlockK = 128;  // input dims of a scale block: one swizzled 128-B row of codes
 constexpr int kAccWarps = 8;
-constexpr int kThreads = (kAccWarps + 4) * 32;  // three warpgroups: the last holds the producer and the MMA issuer
+constexpr int kThreads = (kAccWarps + 4) * 32;  // 168 registers a thread: what the sums need; the other four warps are the roles below
 
 struct LinearParams {
   const float* x_scale;
@@ -54,10 +52,16 @@ struct WideCfg {
   static constexpr int kSmem = 1024 + kOffBars + 256;
 };
 
-// Registers move from the producer's warpgroup to the two accumulation
-// warpgroups: 384 threads start with 168 each; 2 * 128 * 224 + 128 * 56 = 384 * 168.
-__device__ __forceinline__ void regs_accumulate() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
-__device__ __forceinline__ void regs_produce() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
+// mbar_wait with the first look in line: half the time (46 against 92 cycles) where
+// the phase is complete.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
 
 // Four consecutive scales of a row, of which n (<= 0: none) exist; 0 for the others.
 __device__ __forceinline__ float4 load_scales(const float* s, int n, bool vec) {
@@ -109,82 +113,57 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
   const int m_tiles = (p.T + kTileM - 1) / kTileM, n_tiles = (p.N + BN - 1) / BN;
   const int blocks = (p.K + kBlockK - 1) / kBlockK;
   const long long tiles = static_cast<long long>(m_tiles) * n_tiles;
-  // A wait on a completed barrier still costs its round trip (some 100 cycles),
-  // so the next block's accumulator and scales are asked for under this block's
-  // last sums.
-  uint32_t a = 0, a_phase = 0, st = 0;      // accumulator ring, stage ring
-  uint32_t sl = 0, sl_phase = 0, in4 = 0;   // scale ring, block within its group
-  const float* sc = reinterpret_cast<const float*>(smem + Cfg::kOffScales);
-  bool ready = false;
-  float s = 0.f;
-  if (blockIdx.x < tiles) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&sfull[0], 0, s_abort))) return false;
-    s = sc[r] * sc[kTileM + half];
-  }
+  const uint32_t row_scales = smem_u32(smem) + Cfg::kOffScales + r * 4;
+  const uint32_t half_scales = smem_u32(smem) + Cfg::kOffScales + (kTileM + half) * 4;
+  uint32_t it = 0, g = 0;  // blocks and groups of four blocks so far
   for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int n0 = static_cast<int>(tile / m_tiles) * BN + half * C, t0 = static_cast<int>(tile % m_tiles) * kTileM;
     const int row = t0 + r;
-    const bool last_tile = tile + gridDim.x >= tiles;
-    uint64_t acc[C / 2];  // this row's sums, in pairs of columns
+    float y[C];  // this row's sums
 #pragma unroll
-    for (int i = 0; i < C / 2; ++i) acc[i] = 0;
+    for (int i = 0; i < C; ++i) y[i] = 0.f;
 #pragma unroll 1
-    for (int b = blocks; b > 0; --b) {
-      if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, mbar_wait(&tfull[a], a_phase, s_abort))) return false;
+    for (int b = 0; b < blocks; ++b, ++it) {
+      if ((b & 3) == 0 && !__all_sync(0xffffffffu, wait(&sfull[g % SS], (g / SS) & 1, s_abort))) return false;
+      const uint32_t at = (g % SS) * Cfg::kScaleBytes + (b & 3) * (kTileM + 2) * 4;
+      const float sx = ld_shared_f32(row_scales + at), sw = ld_shared_f32(half_scales + at);
+      if (!__all_sync(0xffffffffu, wait(&tfull[it % NA], (it / NA) & 1, s_abort))) return false;
       tc_fence_after();
       // the products have read the stage: one commit a block serves both rings
       // (a second one costs the tensor pipe some 60 cycles)
-      if (warp == 0 && lane == 0) mbar_arrive(&empty[st]);
-      const uint64_t s2 = pack_f32x2(s, s);
-      uint32_t v[2][32];
-      tmem_ld32x32(taddr + a * BN, v[0]);
+      if (warp == 0 && lane == 0) mbar_arrive(&empty[it % S]);
+      const uint64_t s2 = pack_f32x2(sx * sw, sx * sw);
+      const uint32_t ta = taddr + (it % NA) * BN;
 #pragma unroll
-      for (int c = 0; c < C / 32; ++c) {
-        tmem_wait_ld(v[c & 1]);
-        if (c + 1 < C / 32) {
-          tmem_ld32x32(taddr + a * BN + (c + 1) * 32, v[(c + 1) & 1]);
-        } else {  // all of it is in registers: the next product may have the accumulator
+      for (int c = 0; c < C / 16; ++c) {
+        uint32_t v[16];
+        tmem_ld32x16_async(ta + c * 16, v);
+        tmem_wait_ld16(v);
+        if (c + 1 == C / 16) {  // all of it is in registers: the next product may have the accumulator
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[a]);
-          if (++a == NA) {
-            a = 0;
-            a_phase ^= 1;
+          if (lane == 0) {
+            mbar_arrive(&tempty[it % NA]);
+            if ((b & 3) == 3 || b + 1 == blocks) mbar_arrive(&sempty[g % SS]);
           }
-          if (++st == S) st = 0;
-          ready = mbar_test(&tfull[a], a_phase);
-          if (++in4 == 4 || b == 1) {
-            if (lane == 0) mbar_arrive(&sempty[sl]);
-            in4 = 0;
-            if (++sl == SS) {
-              sl = 0;
-              sl_phase ^= 1;
-            }
-            if (!(last_tile && b == 1) && !__all_sync(0xffffffffu, mbar_wait(&sfull[sl], sl_phase, s_abort))) return false;
-          }
-          const float* sn = sc + sl * (Cfg::kScaleBytes / 4) + in4 * (kTileM + 2);
-          s = sn[r] * sn[kTileM + half];
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          acc[c * 16 + i] = fma_f32x2(pack_f32x2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2,
-                                      acc[c * 16 + i]);
+        for (int i = 0; i < 16; i += 2) {
+          const float2 sum = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2,
+                                                    pack_f32x2(y[c * 16 + i], y[c * 16 + i + 1])));
+          y[c * 16 + i] = sum.x;
+          y[c * 16 + i + 1] = sum.y;
+        }
       }
+      if ((b & 3) == 3 || b + 1 == blocks) ++g;
     }
     if (n0 >= p.N || t0 + (warp & 3) * 32 >= p.T) continue;
-    float y[C];
-#pragma unroll
-    for (int i = 0; i < C / 2; ++i) {
-      const float2 f = unpack_f32x2(acc[i]);
-      y[2 * i] = f.x;
-      y[2 * i + 1] = f.y;
-    }
     if (p.rope_head && (n0 + C) % p.rope_head == 0) {  // the 64 columns below a head's end
       const int pos = __ldg(p.row_pos + min(row, p.T - 1));
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         float sn, cs;
-        rope_angle(pos, p.turn[i], &sn, &cs);
+        rope_half_turns(pos, p.turn[i], &sn, &cs);
         const float u = y[C - 64 + 2 * i], v = y[C - 63 + 2 * i];
         y[C - 64 + 2 * i] = u * cs - v * sn;
         y[C - 63 + 2 * i] = u * sn + v * cs;
@@ -270,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tempty[i], kAccWarps);
     }
     for (int i = 0; i < SS; ++i) {
-      mbar_init(&sfull[i], 2);
+      mbar_init(&sfull[i], 1);
       mbar_init(&sempty[i], kAccWarps);
     }
     fence_mbar_init();
@@ -292,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long tiles = static_cast<long long>(m_tiles) * n_tiles;
 
   if (warp >= kAccWarps) {
-   regs_produce();
    if (warp == kAccWarps) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -318,32 +296,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long i = (it > S ? it - S : 0); i < it; ++i)
         mbar_wait(&full[i % S], static_cast<uint32_t>((i / S) & 1), nullptr);
     }
-   } else if (warp == kAccWarps + 1) {
-    // ------------------------------------------------------------ MMA issuer
+   } else if (warp <= kAccWarps + NA) {
+    // ------------------------------------------------------------ MMA issuers
+    // One warp for each accumulator: the products of a block are queued while the
+    // other warp still waits for its accumulator.
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(kTileM, BN);
       constexpr uint64_t kStageDesc = Cfg::kStageBytes >> 4;
       const uint64_t x_desc = smem_desc_sw128(smem), w_desc = smem_desc_sw128(smem + kTileM * kBlockK);
       const long long mine = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * blocks;  // blocks of this CTA's tiles
-      uint32_t s = 0, phase = 0, a = 0, a_phase = 1;
+      const int a = warp - kAccWarps - 1;
+      const uint32_t d = tmem + a * BN;
+      uint32_t s = a, phase = 0, a_phase = 1;
       bool ok = true;
-      for (long long i = 0; i < mine; ++i) {
-        if (!(ok = mbar_wait(&full[s], phase, s_abort))) break;
+      for (long long i = a; i < mine; i += NA) {
+        if (!(ok = wait(&full[s], phase, s_abort))) break;
         const uint64_t ad = x_desc + s * kStageDesc, bd = w_desc + s * kStageDesc;
-        const uint32_t d = tmem + a * BN;
-        if (!(ok = mbar_wait(&tempty[a], a_phase, s_abort))) break;
+        if (!(ok = wait(&tempty[a], a_phase, s_abort))) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 32 B of the swizzled rows a step
           mma_e4m3(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
         mma_commit(&tfull[a]);
-        if (++s == S) {
-          s = 0;
+        a_phase ^= 1;
+        s += NA;
+        if (s >= S) {
+          s -= S;
           phase ^= 1;
-        }
-        if (++a == NA) {
-          a = 0;
-          a_phase ^= 1;
         }
       }
       if (!ok) {
@@ -353,18 +332,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
    } else {
     // ------------------------------------------------------------ scales
-    // Two warps bring the scales of four blocks at a time into shared memory: a
-    // load in flight in an accumulation warp would be waited for at its next
-    // barrier arrival (570 against 400 ns a block).
-    const int r0 = (warp - kAccWarps - 2) * 32 + lane;
+    // A warp brings the scales of four blocks at a time into shared memory.
     long long g = 0;
     bool ok = true;
     for (long long tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
       const int n0 = static_cast<int>(tile / m_tiles) * BN, t0 = static_cast<int>(tile % m_tiles) * kTileM;
-      const float* xs0 = p.x_scale + static_cast<long long>(min(t0 + r0, p.T - 1)) * p.ld_xs;
-      const float* xs1 = p.x_scale + static_cast<long long>(min(t0 + r0 + 64, p.T - 1)) * p.ld_xs;
-      const int nw = n0 + (warp - kAccWarps - 2) * C;  // lane 0: this column half's weight scales
-      const float* ws = p.w_scale + static_cast<long long>(min(nw, p.N - 1) >> 7) * p.ld_ws;
+      const float* xs[4];  // of rows lane, lane + 32, ..
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xs[i] = p.x_scale + static_cast<long long>(min(t0 + i * 32 + lane, p.T - 1)) * p.ld_xs;
+      // lanes 0 and 1: the weight scales of a column half
+      const float* ws = p.w_scale + static_cast<long long>(min(n0 + (lane & 1) * C, p.N - 1) >> 7) * p.ld_ws;
       for (int b = 0; b < blocks; b += 4, ++g) {
         const int s = static_cast<int>(g % SS);
         ok = __all_sync(0xffffffffu, mbar_wait(&sempty[s], static_cast<uint32_t>((g / SS) & 1) ^ 1u, s_abort));
@@ -376,10 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           dst[i + 2 * (kTileM + 2)] = v.z;
           dst[i + 3 * (kTileM + 2)] = v.w;
         };
-        const float4 v0 = load_scales(xs0 + b, blocks - b, p.vec_scales), v1 = load_scales(xs1 + b, blocks - b, p.vec_scales);
-        if (lane == 0) put(kTileM + warp - kAccWarps - 2, load_scales(ws + b, blocks - b, p.vec_scales));
-        put(r0, v0);
-        put(r0 + 64, v1);
+        float4 v[4], vw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = load_scales(xs[i] + b, blocks - b, p.vec_scales);
+        if (lane < 2) vw = load_scales(ws + b, blocks - b, p.vec_scales);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) put(i * 32 + lane, v[i]);
+        if (lane < 2) put(kTileM + lane, vw);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sfull[s]);
       }
@@ -390,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
    }
   } else {
-    regs_accumulate();
     if (!accumulate_and_store<BN, OUT>(map_out, p, smem, tmem, tfull, tempty, empty, sfull, sempty, s_abort)) {
       *s_abort = 1;
       set_error(p.err, kErrTimeout);
@@ -416,7 +395,7 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
     return cudaErrorInvalidValue;
   }
   auto kern = fp8_linear_wide_kernel<BN, OUT>;
-  cudaError_t e = prefer_max_smem(kern, WideCfg<BN>::kSmem);
+  cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT>>(ctx.device, WideCfg<BN>::kSmem);
   if (e != cudaSuccess) return e;
   const long long tiles = ((static_cast<long long>(a.T) + kTileM - 1) / kTileM) * ((static_cast<long long>(a.N) + BN - 1) / BN);
   const unsigned grid = static_cast<unsigned>(tiles < ctx.num_sms ? tiles : ctx.num_sms);
@@ -690,14 +669,16 @@ int narrow_clusters(const cudaLaunchConfig_t& cfg, int splits, int device) {
   static std::atomic<int> known[64][5];
   int i = 0;
   while ((1 << i) < splits) ++i;
-  int n = known[device][i].load(std::memory_order_relaxed);
+  int n = known[device][i].load(std::memory_order_acquire);
   if (n == 0) {
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_linear_narrow_kernel<NT, OUT>, &cfg) != cudaSuccess) {
+    // clusters above 8 CTAs have to be allowed, once, before the first is asked for
+    if (cudaFuncSetAttribute(fp8_linear_narrow_kernel<NT, OUT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fp8_linear_narrow_kernel<NT, OUT>, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       n = -1;
     }
     if (n == 0) n = -1;
-    known[device][i].store(n, std::memory_order_relaxed);
+    known[device][i].store(n, std::memory_order_release);
   }
   return n;
 }
@@ -712,9 +693,7 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
   const int t_tiles = (a.T + NT - 1) / NT, blocks = (a.K + 127) / 128;
   *taken = NT < 64 || n_tiles * t_tiles <= ctx.num_sms;
   if (!*taken) return cudaSuccess;
-  cudaError_t e = prefer_max_smem(kern, NarrowCfg<NT>::kSmem);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  cudaError_t e = prefer_max_smem_once<fp8_linear_narrow_kernel<NT, OUT>>(ctx.device, NarrowCfg<NT>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kNarrowThreads);
