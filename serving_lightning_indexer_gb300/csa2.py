@@ -329,7 +329,8 @@ def _device(t, name: str) -> int:
     return dev
 
 
-def _check_tensor(t, name: str, dtype, dev: int):
+def _refuse(t, name: str, dtype, dev: int):
+    """Says what is wrong with a tensor of another type or device than a call's."""
     if not isinstance(t, _Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
     if t.dtype != dtype:
@@ -339,37 +340,43 @@ def _check_tensor(t, name: str, dtype, dev: int):
     raise ValueError(f"{name}: on cuda:{t.get_device()}, the call's first tensor on cuda:{dev}")
 
 
-def _mat(t, name: str, dtype, dev: int, rows, cols):
-    """(pointer, row stride) of a 2-D tensor [rows, cols] whose rows are contiguous (the
-    rows may be apart); rows or cols None: any."""
+# The checks below run on every call, before a launch of a few microseconds: each
+# attribute of a tensor is asked for once.
+def _mat(t, name: str, dtype, dev: int, shape):
+    """(pointer, row stride) of a 2-D tensor of the given shape whose rows are contiguous
+    (the rows may be apart)."""
     if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
-        _check_tensor(t, name, dtype, dev)
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name}: expected a 2-D tensor, got {list(shape)}")
-    n, m = shape
-    if (rows is not None and n != rows) or (cols is not None and m != cols):
-        raise ValueError(f"{name}: expected shape [{rows}, {cols}], got {[n, m]}")
+        _refuse(t, name, dtype, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    m = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr() or _EMPTY, m
     ld, step = t.stride()
-    if n <= 1:
-        ld = m
     if (step != 1 and m > 1) or ld < m:
         raise ValueError(f"{name}: expected contiguous rows that do not overlap, got strides {t.stride()}")
     return t.data_ptr() or _EMPTY, ld
 
 
-def _vec(t, name: str, dtype, dev: int, n=None) -> int:
+def _vec(t, name: str, dtype, dev: int, n: int) -> int:
     """Pointer of a contiguous 1-D tensor of n elements (0 for None)."""
     if t is None:
         return 0
     if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
-        _check_tensor(t, name, dtype, dev)
-    shape = t.shape
-    if len(shape) != 1 or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous 1-D tensor")
-    if n is not None and shape[0] != n:
-        raise ValueError(f"{name}: expected {n} elements, got {shape[0]}")
+        _refuse(t, name, dtype, dev)
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous elements, got {list(t.shape)}")
     return t.data_ptr() or _EMPTY
+
+
+def _two_d(t, name: str):
+    """Shape of a 2-D tensor."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got {list(shape)}")
+    return shape
 
 
 def _issue(fn, packed: bytes, where: str, dev: int, stream):
@@ -388,10 +395,10 @@ def quant_fp8(x, codes, scale, gamma=None, eps=1e-6, block_rows=1, stream=None):
     with gamma [K] of the row's RMSNorm) or per 128 x 128 tile (block_rows=128, weights):
     codes uint8 [T,K], scale [ceil(T/block_rows), ceil(K/128)] (csa2_quant_fp8)."""
     dev = _device(x, "x")
-    px, ldx = _mat(x, "x", _BF16, dev, None, None)
-    T, K = x.shape
-    pc, ldc = _mat(codes, "codes", _U8, dev, T, K)
-    ps, lds = _mat(scale, "scale", _F32, dev, T if block_rows == 1 else (T + 127) // 128, (K + 127) // 128)
+    T, K = shape = _two_d(x, "x")
+    px, ldx = _mat(x, "x", _BF16, dev, shape)
+    pc, ldc = _mat(codes, "codes", _U8, dev, shape)
+    ps, lds = _mat(scale, "scale", _F32, dev, (T if block_rows == 1 else (T + 127) // 128, (K + 127) // 128))
     _issue(load().csa2_quant_fp8, _pack_quant(px, ldx, T, K, block_rows, _vec(gamma, "gamma", _F32, dev, K), eps, pc, ldc,
                                               ps, lds), "csa2_quant_fp8", dev, stream)
 
@@ -407,35 +414,23 @@ def fp8_linear(x, x_scale, w, w_scale, out, out_scale=None, row_pos=None, rope_h
     out_scale [T,N/128]; rope_head turns the last 64 columns of every head of that many
     columns by row_pos [T] (csa2_fp8_linear)."""
     dev = _device(x, "x")
-    px, ldx = _mat(x, "x", _U8, dev, None, None)
-    T, K = x.shape
-    pw, ldw = _mat(w, "w", _U8, dev, None, K)
-    N = w.shape[0]
+    T, K = x_shape = _two_d(x, "x")
+    N, _ = w_shape = _two_d(w, "w")
     nb = (K + 127) // 128
-    pxs, ldxs = _mat(x_scale, "x_scale", _F32, dev, T, nb)
-    pws, ldws = _mat(w_scale, "w_scale", _F32, dev, (N + 127) // 128, nb)
+    px, ldx = _mat(x, "x", _U8, dev, x_shape)
+    pw, ldw = _mat(w, "w", _U8, dev, (N, K))
+    pxs, ldxs = _mat(x_scale, "x_scale", _F32, dev, (T, nb))
+    pws, ldws = _mat(w_scale, "w_scale", _F32, dev, ((N + 127) // 128, nb))
     kind = out.dtype
     fmt = _OUT_FORMAT.get(kind)
     if fmt is None:
         raise TypeError(f"out: expected float32, bfloat16 or uint8, got {kind}")
-    po, ldo = _mat(out, "out", kind, dev, T, N)
-    pos, ldos = (0, 0) if out_scale is None else _mat(out_scale, "out_scale", _F32, dev, T, N // 128)
+    po, ldo = _mat(out, "out", kind, dev, (T, N))
+    pos, ldos = (0, 0) if out_scale is None else _mat(out_scale, "out_scale", _F32, dev, (T, N // 128))
     _issue(load().csa2_fp8_linear,
            _pack_linear(px, ldx, pxs, ldxs, pw, ldw, pws, ldws, T, N, K, fmt, po, ldo, pos, ldos,
                         _vec(row_pos, "row_pos", _INT32, dev, T), rope_head, rope_theta, 1 if w_ready else 0),
            "csa2_fp8_linear", dev, stream)
-
-
-def _one_length(*arrays) -> int:
-    """The one length of the (name, tensor) pairs whose tensor is given (0 when none is)."""
-    n = -1
-    for name, t in arrays:
-        if t is not None:
-            m = t.shape[0]
-            if n >= 0 and m != n:
-                raise ValueError(f"{name}: {m} places, the other arrays of its kind have {n}")
-            n = m
-    return max(n, 0)
 
 
 def batch_plan(ctx_len, new_len, ratio_m=1, page_table=None, free_pages=None, free_head=None, free_head_out=None,
@@ -447,27 +442,39 @@ def batch_plan(ctx_len, new_len, ratio_m=1, page_table=None, free_pages=None, fr
     place; row arrays share one length (rows the step may have), entry arrays another;
     page_table [B, pages] is extended from free_pages when that is given."""
     dev = _device(ctx_len, "ctx_len")
-
-    def vec(t, name, n=None):
-        return 0 if t is None else _vec(t, name, _INT32, dev, n)
-
-    ctx = vec(ctx_len, "ctx_len")
-    B = ctx_len.shape[0]
-    pt, ldp = (0, 0) if page_table is None else _mat(page_table, "page_table", _INT32, dev, B, None)
-    if pt and ldp != page_table.shape[1]:
-        raise ValueError("page_table: expected a contiguous tensor")
-    ss, lds = (0, 0) if swa_slot is None else _mat(swa_slot, "swa_slot", _INT32, dev, None, None)
+    i32 = _INT32
+    B = ctx_len.shape[0] if ctx_len.dim() == 1 else -1
+    row_cap = entry_cap = 0   # the one length of the row arrays, and of the entry arrays
+    for t in (row_seq, row_pos, swa_new, swa_slot):
+        if t is not None:
+            row_cap = len(t)
+            break
+    for t in (entry_slot, entry_pos, entry_row):
+        if t is not None:
+            entry_cap = len(t)
+            break
+    pt = pt_stride = ss = lds = n_swa = fp = n_free = 0
+    if page_table is not None:
+        pt_stride = _two_d(page_table, "page_table")[1]
+        pt, ld = _mat(page_table, "page_table", i32, dev, (B, pt_stride))
+        if ld != pt_stride:
+            raise ValueError("page_table: expected a contiguous tensor")
+    if swa_slot is not None:
+        n_swa = _two_d(swa_slot, "swa_slot")[1]
+        ss, lds = _mat(swa_slot, "swa_slot", i32, dev, (row_cap, n_swa))
+    if free_pages is not None:
+        n_free = len(free_pages)
+        fp = _vec(free_pages, "free_pages", i32, dev, n_free)
     _issue(load().csa2_batch_plan, _pack_plan(
-        B, ctx, vec(new_len, "new_len", B), ratio_m, pt, ldp,
-        vec(free_pages, "free_pages"), 0 if free_pages is None else free_pages.shape[0],
-        vec(free_head, "free_head", 1), vec(free_head_out, "free_head_out", 1),
-        vec(row_start, "row_start", B + 1), vec(n_visible, "n_visible", B), vec(entry_start, "entry_start", B + 1),
-        _one_length(("row_seq", row_seq), ("row_pos", row_pos), ("swa_new", swa_new), ("swa_slot", swa_slot)),
-        vec(row_seq, "row_seq"), vec(row_pos, "row_pos"),
-        _one_length(("entry_slot", entry_slot), ("entry_pos", entry_pos), ("entry_row", entry_row)),
-        vec(entry_slot, "entry_slot"), vec(entry_pos, "entry_pos"), vec(entry_row, "entry_row"),
-        swa_ring, vec(ring_id, "ring_id", B), vec(swa_new, "swa_new"), ss, 0 if swa_slot is None else swa_slot.shape[1],
-        lds, 1 if pad else 0), "csa2_batch_plan", dev, stream)
+        B, _vec(ctx_len, "ctx_len", i32, dev, B), _vec(new_len, "new_len", i32, dev, B), ratio_m, pt, pt_stride, fp, n_free,
+        _vec(free_head, "free_head", i32, dev, 1), _vec(free_head_out, "free_head_out", i32, dev, 1),
+        _vec(row_start, "row_start", i32, dev, B + 1), _vec(n_visible, "n_visible", i32, dev, B),
+        _vec(entry_start, "entry_start", i32, dev, B + 1),
+        row_cap, _vec(row_seq, "row_seq", i32, dev, row_cap), _vec(row_pos, "row_pos", i32, dev, row_cap),
+        entry_cap, _vec(entry_slot, "entry_slot", i32, dev, entry_cap), _vec(entry_pos, "entry_pos", i32, dev, entry_cap),
+        _vec(entry_row, "entry_row", i32, dev, entry_cap),
+        swa_ring, _vec(ring_id, "ring_id", i32, dev, B), _vec(swa_new, "swa_new", i32, dev, row_cap), ss, n_swa, lds,
+        1 if pad else 0), "csa2_batch_plan", dev, stream)
 
 
 def check_device_error(stream=None) -> int:

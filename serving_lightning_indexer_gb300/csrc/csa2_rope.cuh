@@ -31,12 +31,15 @@ __device__ __forceinline__ void rope_angle(long long pos, uint64_t turn_rate, fl
   sincosf(static_cast<float>(t) * 1.4629180792671596e-09f, sn, cs);  // 2 pi / 2^32
 }
 
-// The same angle through sincospif, which takes the fraction of a half turn as it
-// is (no argument reduction): half the instructions where a thread needs many.
-__device__ __forceinline__ void rope_half_turns(long long pos, uint64_t turn_rate, float* sn, float* cs) {
+// The same angle through the fast sine and cosine, whose absolute error on
+// [-pi, pi] is below 2^-20.9: a fifth of the instructions where a thread turns
+// many pairs.  The rotated values are then off by under 2^-20 of the pair.
+__device__ __forceinline__ void rope_angle_fast(long long pos, uint64_t turn_rate, float* sn, float* cs) {
   const uint64_t frac = static_cast<uint64_t>(pos) * turn_rate;
   const int32_t t = static_cast<int32_t>(static_cast<uint32_t>(frac >> 32));
-  sincospif(static_cast<float>(t) * 4.656612873077393e-10f, sn, cs);  // 2^-31
+  const float a = static_cast<float>(t) * 1.4629180792671596e-09f;  // 2 pi / 2^32
+  *sn = __sinf(a);
+  *cs = __cosf(a);
 }
 
 // Inverse RoPE of one interleaved pair (a, b): rotation by -pos * rate.

@@ -163,7 +163,7 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         float sn, cs;
-        rope_half_turns(pos, p.turn[i], &sn, &cs);
+        rope_angle_fast(pos, p.turn[i], &sn, &cs);
         const float u = y[C - 64 + 2 * i], v = y[C - 63 + 2 * i];
         y[C - 64 + 2 * i] = u * cs - v * sn;
         y[C - 63 + 2 * i] = u * sn + v * cs;
