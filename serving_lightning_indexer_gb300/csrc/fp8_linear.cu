@@ -97,9 +97,37 @@ __host__ __device__ constexpr int out_size(int format) {
   return format == CSA2_OUT_F32 ? 4 : (format == CSA2_OUT_BF16 ? 2 : 1);
 }
 
+// A CTA's share of the work: tiles first, first + step, .. and of each the blocks
+// [b0, b0 + blocks).  SPLIT: a cluster of two CTAs has one tile and halves its
+// blocks (the first share a multiple of 4, as scales come in fours).
+template <int BN, bool SPLIT>
+struct Share {
+  int m_tiles, b0, blocks;
+  long long tiles, first, step;
+  __device__ __forceinline__ explicit Share(const LinearParams& p) {
+    m_tiles = (p.T + kTileM - 1) / kTileM;
+    tiles = static_cast<long long>(m_tiles) * ((p.N + BN - 1) / BN);
+    const int all = (p.K + kBlockK - 1) / kBlockK;
+    if (SPLIT) {
+      const int half = ((all + 1) / 2 + 3) & ~3;
+      b0 = (blockIdx.x & 1) ? half : 0;
+      blocks = (blockIdx.x & 1) ? all - half : half;
+      first = blockIdx.x >> 1;
+      step = tiles;
+    } else {
+      b0 = 0;
+      blocks = all;
+      first = blockIdx.x;
+      step = gridDim.x;
+    }
+  }
+  __device__ __forceinline__ int row(long long tile) const { return static_cast<int>(tile % m_tiles) * kTileM; }
+  __device__ __forceinline__ int column(long long tile) const { return static_cast<int>(tile / m_tiles) * BN; }
+};
+
 // The accumulation warps' part: sums each tile in registers and writes it.
 // False when a wait gave up (the same in a warp's lanes).
-template <int BN, int OUT>
+template <int BN, int OUT, bool SPLIT>
 __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out, const LinearParams& p, uint8_t* smem,
                                                      uint32_t tmem, uint64_t* tfull, uint64_t* tempty, uint64_t* empty,
                                                      uint64_t* sfull, uint64_t* sempty, volatile int* s_abort) {
@@ -110,14 +138,13 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
   const int r = (warp & 3) * 32 + lane;  // row of the tile: TMEM lane
   const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * C;
   uint8_t* s_out = smem + Cfg::kOffOut + warp * 2048;
-  const int m_tiles = (p.T + kTileM - 1) / kTileM, n_tiles = (p.N + BN - 1) / BN;
-  const int blocks = (p.K + kBlockK - 1) / kBlockK;
-  const long long tiles = static_cast<long long>(m_tiles) * n_tiles;
+  const Share<BN, SPLIT> mine(p);
+  const int blocks = mine.blocks;
   const uint32_t row_scales = smem_u32(smem) + Cfg::kOffScales + r * 4;
   const uint32_t half_scales = smem_u32(smem) + Cfg::kOffScales + (kTileM + half) * 4;
   uint32_t it = 0, g = 0;  // blocks and groups of four blocks so far
-  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int n0 = static_cast<int>(tile / m_tiles) * BN + half * C, t0 = static_cast<int>(tile % m_tiles) * kTileM;
+  for (long long tile = mine.first; tile < mine.tiles; tile += mine.step) {
+    const int n0 = mine.column(tile) + half * C, t0 = mine.row(tile);
     const int row = t0 + r;
     float y[C];  // this row's sums
 #pragma unroll
@@ -156,6 +183,25 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
         }
       }
       if ((b & 3) == 3 || b + 1 == blocks) ++g;
+    }
+    if (SPLIT) {
+      // Rank 0 finishes the left half of the columns, rank 1 the right one: the
+      // other half's sums go to the peer through the stages, which are done with
+      // (every product of this CTA is complete, and the peer reads its own).
+      const int rank = static_cast<int>(blockIdx.x & 1);
+      float* part = reinterpret_cast<float*>(smem) + r;
+      if (half != rank) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) part[i * kTileM] = y[i];
+      }
+      cluster_sync();
+      if (half == rank) {
+        const uint32_t at = map_rank(smem_u32(part), static_cast<uint32_t>(rank ^ 1));
+#pragma unroll
+        for (int i = 0; i < C; ++i) y[i] += ld_cluster_f32(at + i * kTileM * 4);
+      }
+      cluster_sync();  // no CTA leaves while its sums may still be read
+      if (half != rank) break;
     }
     if (n0 >= p.N || t0 + (warp & 3) * 32 >= p.T) continue;
     if (p.rope_head && (n0 + C) % p.rope_head == 0) {  // the 64 columns below a head's end
@@ -220,7 +266,7 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
   return true;
 }
 
-template <int BN, int OUT>
+template <int BN, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_linear_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p) {
@@ -266,9 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int m_tiles = (p.T + kTileM - 1) / kTileM, n_tiles = (p.N + BN - 1) / BN;
-  const int blocks = (p.K + kBlockK - 1) / kBlockK;
-  const long long tiles = static_cast<long long>(m_tiles) * n_tiles;
+  const Share<BN, SPLIT> mine(p);
+  const int blocks = mine.blocks;
 
   if (warp >= kAccWarps) {
    if (warp == kAccWarps) {
@@ -277,15 +322,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t keep = l2_policy_evict_last();
       long long it = 0;
       bool ok = true;
-      for (long long tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const int n0 = static_cast<int>(tile / m_tiles) * BN, t0 = static_cast<int>(tile % m_tiles) * kTileM;
+      for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
+        const int n0 = mine.column(tile), t0 = mine.row(tile);
         for (int b = 0; b < blocks; ++b, ++it) {
           const int s = static_cast<int>(it % S);
           if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
           uint8_t* dst = smem + s * Cfg::kStageBytes;
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
-          tma_load_2d(dst, &map_x, b * kBlockK, t0, &full[s], keep);
-          tma_load_2d(dst + kTileM * kBlockK, &map_w, b * kBlockK, n0, &full[s], keep);
+          tma_load_2d(dst, &map_x, (mine.b0 + b) * kBlockK, t0, &full[s], keep);
+          tma_load_2d(dst + kTileM * kBlockK, &map_w, (mine.b0 + b) * kBlockK, n0, &full[s], keep);
         }
       }
       if (!ok) {
@@ -304,12 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc = idesc_e4m3_f32(kTileM, BN);
       constexpr uint64_t kStageDesc = Cfg::kStageBytes >> 4;
       const uint64_t x_desc = smem_desc_sw128(smem), w_desc = smem_desc_sw128(smem + kTileM * kBlockK);
-      const long long mine = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * blocks;  // blocks of this CTA's tiles
+      const long long all = (mine.tiles - mine.first + mine.step - 1) / mine.step * blocks;  // blocks of this CTA's tiles
       const int a = warp - kAccWarps - 1;
       const uint32_t d = tmem + a * BN;
       uint32_t s = a, phase = 0, a_phase = 1;
       bool ok = true;
-      for (long long i = a; i < mine; i += NA) {
+      for (long long i = a; i < all; i += NA) {
         if (!(ok = wait(&full[s], phase, s_abort))) break;
         const uint64_t ad = x_desc + s * kStageDesc, bd = w_desc + s * kStageDesc;
         if (!(ok = wait(&tempty[a], a_phase, s_abort))) break;
@@ -335,13 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A warp brings the scales of four blocks at a time into shared memory.
     long long g = 0;
     bool ok = true;
-    for (long long tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const int n0 = static_cast<int>(tile / m_tiles) * BN, t0 = static_cast<int>(tile % m_tiles) * kTileM;
+    for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
+      const int n0 = mine.column(tile), t0 = mine.row(tile);
       const float* xs[4];  // of rows lane, lane + 32, ..
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xs[i] = p.x_scale + static_cast<long long>(min(t0 + i * 32 + lane, p.T - 1)) * p.ld_xs;
+      for (int i = 0; i < 4; ++i) xs[i] = p.x_scale + static_cast<long long>(min(t0 + i * 32 + lane, p.T - 1)) * p.ld_xs + mine.b0;
       // lanes 0 and 1: the weight scales of a column half
-      const float* ws = p.w_scale + static_cast<long long>(min(n0 + (lane & 1) * C, p.N - 1) >> 7) * p.ld_ws;
+      const float* ws = p.w_scale + static_cast<long long>(min(n0 + (lane & 1) * C, p.N - 1) >> 7) * p.ld_ws + mine.b0;
       for (int b = 0; b < blocks; b += 4, ++g) {
         const int s = static_cast<int>(g % SS);
         ok = __all_sync(0xffffffffu, mbar_wait(&sempty[s], static_cast<uint32_t>((g / SS) & 1) ^ 1u, s_abort));
@@ -370,10 +415,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
    }
   } else {
-    if (!accumulate_and_store<BN, OUT>(map_out, p, smem, tmem, tfull, tempty, empty, sfull, sempty, s_abort)) {
+    if (!accumulate_and_store<BN, OUT, SPLIT>(map_out, p, smem, tmem, tfull, tempty, empty, sfull, sempty, s_abort)) {
       *s_abort = 1;
       set_error(p.err, kErrTimeout);
+      if (SPLIT) {  // the waits that gave up came before the cluster's two barriers
+        cluster_sync();
+        cluster_sync();
+      }
     }
+  }
+  if (SPLIT && warp >= kAccWarps) {
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
   }
   tc_fence_before();
   __syncthreads();
@@ -383,7 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BN, int OUT>
+template <int BN>
+long long wide_tiles(const csa2_fp8_linear_args& a) {
+  return ((static_cast<long long>(a.T) + kTileM - 1) / kTileM) * ((static_cast<long long>(a.N) + BN - 1) / BN);
+}
+
+template <int BN, int OUT, bool SPLIT>
 cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, const DeviceCtx& ctx, cudaStream_t st,
                         const char** why) {
   CUtensorMap map_x, map_w, map_out = {};
@@ -394,12 +453,25 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
     *why = "csa2_fp8_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
   }
-  auto kern = fp8_linear_wide_kernel<BN, OUT>;
-  cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT>>(ctx.device, WideCfg<BN>::kSmem);
+  auto kern = fp8_linear_wide_kernel<BN, OUT, SPLIT>;
+  cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT, SPLIT>>(ctx.device, WideCfg<BN>::kSmem);
   if (e != cudaSuccess) return e;
-  const long long tiles = ((static_cast<long long>(a.T) + kTileM - 1) / kTileM) * ((static_cast<long long>(a.N) + BN - 1) / BN);
-  const unsigned grid = static_cast<unsigned>(tiles < ctx.num_sms ? tiles : ctx.num_sms);
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), WideCfg<BN>::kSmem, st, map_x, map_w, map_out, p);
+  const long long tiles = wide_tiles<BN>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? 2 * tiles : (tiles < ctx.num_sms ? tiles : ctx.num_sms)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = WideCfg<BN>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, map_out, p);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -683,8 +755,23 @@ int narrow_clusters(const cudaLaunchConfig_t& cfg, int splits, int device) {
   return n;
 }
 
-// Launches the few-rows kernel, or sets *taken to false where its CTAs would not
-// all run at once and the rows are enough for 128 x 256 tiles.
+// Time of the wide kernel's launch, in the time of one block's products of one
+// tile (about 0.43 us): rounds of tiles with their output, or half the blocks and
+// the exchange, and what a launch takes before its first and after its last block.
+bool wide_splits(const csa2_fp8_linear_args& a, const DeviceCtx& ctx) {
+  return 2 * wide_tiles<256>(a) <= ctx.num_sms && (a.K + 127) / 128 >= 16;
+}
+long long wide_time(const csa2_fp8_linear_args& a, const DeviceCtx& ctx) {
+  const int blocks = (a.K + 127) / 128;
+  if (wide_splits(a, ctx)) return blocks / 2 + 14;
+  return (wide_tiles<256>(a) + ctx.num_sms - 1) / ctx.num_sms * (blocks + 4) + 8;
+}
+
+// Launches the few-rows kernel, or sets *taken to false where 128 x 256 tiles take
+// less time.  Up to 32 rows the weights' bytes decide, and this kernel reads them
+// once; with more it has to run at once (one CTA an SM) and be the quicker by
+// wide_time's measure, a CTA's blocks and 7 (K = 7168, N = 512: 12.3 us here, 20 us
+// there for 512 rows, 32 and 20 us for 2,048).
 template <int NT, int OUT>
 cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, const DeviceCtx& ctx, cudaStream_t st,
                           const char** why, bool* taken) {
@@ -715,6 +802,8 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
     attr[1].val.clusterDim.z = splits;
     if (2 * splits <= blocks && n_tiles * t_tiles <= narrow_clusters<NT, OUT>(cfg, splits, ctx.device)) break;
   }
+  *taken = NT < 64 || (blocks + splits - 1) / splits + 7 <= wide_time(a, ctx);
+  if (!*taken) return cudaSuccess;
   cfg.gridDim = dim3(static_cast<unsigned>(n_tiles), t_tiles, splits);
   attr[1].val.clusterDim.z = splits;
   CUtensorMap map_x, map_w;
@@ -734,7 +823,10 @@ cudaError_t launch_out(const csa2_fp8_linear_args& a, const LinearParams& p, con
                   : a.T <= 32 ? launch_narrow<32, OUT>(a, p, ctx, st, why, &taken)
                               : launch_narrow<64, OUT>(a, p, ctx, st, why, &taken);
   if (e != cudaSuccess || taken) return e;
-  return launch_wide<256, OUT>(a, p, ctx, st, why);
+  // Tiles for less than half the SMs share their blocks between two CTAs (4,096 x
+  // 7,168 x 512: 28.9 -> 19.9 us).
+  return wide_splits(a, ctx) ? launch_wide<256, OUT, true>(a, p, ctx, st, why)
+                             : launch_wide<256, OUT, false>(a, p, ctx, st, why);
 }
 
 }  // namespace
