@@ -516,8 +516,8 @@ int csa2_quant_fp8(const csa2_quant_fp8_args* a, void* stream) {
   if (!aligned16(a->x) || !aligned16(a->codes) || (a->gamma && !aligned16(a->gamma)) || (a->ld_x & 7) || (a->ld_codes & 15))
     return fail(CSA2_ERR_ALIGN, "csa2_quant_fp8: x, codes, gamma must be 16-B aligned, ld_x a multiple of 8, ld_codes of 16");
   if (!aligned4(a->scale)) return fail(CSA2_ERR_ALIGN, "csa2_quant_fp8: scale must be 4-B aligned");
-  // one thread block per 8 runs of 512 columns, per row or per tile
-  if (static_cast<long long>(a->T) * ((a->K + 511) / 512) / 8 > 0x7FFFFFFELL)
+  // runs of 512 columns are counted in 31 bits (a terabyte of codes)
+  if (static_cast<long long>(a->T) * ((a->K + 511) / 512) > 0x7FFFFF00LL)
     return fail(CSA2_ERR_SHAPE, "csa2_quant_fp8: T=%d rows of %d are too many for one call", a->T, a->K);
   cudaError_t e = csa2::launch_quant_fp8(*a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "csa2_quant_fp8: launch");

@@ -58,29 +58,37 @@ __device__ __forceinline__ float max8(float a) {
   return a;
 }
 
-// Rows without a norm: a warp takes 512 columns of a row, a lane 16 of them.
+// Rows without a norm: a warp takes U runs of 512 columns, a lane 16 of each; all
+// of them are loaded before the first is used.
+template <int U>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantParams p, int chunks) {
   pdl_wait();
   pdl_trigger();
-  const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int t = static_cast<int>(item / chunks);
-  if (t >= p.T) return;
-  const int c = static_cast<int>(item - static_cast<long long>(t) * chunks) * 512 + lane * 16;
-  const bool in = c < p.K;
-  uint4 v[2] = {};
-  if (in) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.x + t * p.ld_x + c);
-    v[0] = __ldg(src);
-    v[1] = __ldg(src + 1);
+  const uint32_t item0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * U;
+  uint4 v[U][2];
+  int t[U], c[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    t[u] = static_cast<int>((item0 + u) / static_cast<uint32_t>(chunks));
+    c[u] = static_cast<int>(item0 + u - static_cast<uint32_t>(t[u]) * chunks) * 512 + lane * 16;
+    v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+    if (t[u] < p.T && c[u] < p.K) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.x + t[u] * p.ld_x + c[u]);
+      v[u][0] = __ldg(src);
+      v[u][1] = __ldg(src + 1);
+    }
   }
-  float y[16];
-  unpack16(v, y);
-  float f;
-  const float s = e4m3_block(max8(amax16(y)), &f);
-  if (!in) return;
-  *reinterpret_cast<uint4*>(p.codes + t * p.ld_codes + c) = codes16(y, f);
-  if ((lane & 7) == 0) p.scale[t * p.ld_scale + (c >> 7)] = s;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float y[16];
+    unpack16(v[u], y);
+    float f;
+    const float s = e4m3_block(max8(amax16(y)), &f);
+    if (t[u] >= p.T || c[u] >= p.K) continue;
+    *reinterpret_cast<uint4*>(p.codes + t[u] * p.ld_codes + c[u]) = codes16(y, f);
+    if ((lane & 7) == 0) p.scale[t[u] * p.ld_scale + (c[u] >> 7)] = s;
+  }
 }
 
 // Rows with RMSNorm: one CTA a row; the row stays in registers between the sum
@@ -212,8 +220,8 @@ cudaError_t launch_quant_fp8(const csa2_quant_fp8_args& a, cudaStream_t st) {
     return launch_pdl(quant_norm_kernel<4>, grid, block, 0, st, p);
   }
   const int chunks = (a.K + 511) / 512;
-  const long long blocks = (static_cast<long long>(a.T) * chunks + 7) / 8;
-  return launch_pdl(quant_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p, chunks);
+  const long long items = static_cast<long long>(a.T) * chunks;
+  return launch_pdl(quant_rows_kernel<2>, dim3(static_cast<unsigned>((items + 15) / 16)), dim3(256), 0, st, p, chunks);
 }
 
 }  // namespace csa2
