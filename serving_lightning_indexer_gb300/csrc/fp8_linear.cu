@@ -8,6 +8,7 @@
 // eight accumulation warps, a TMA producer, two MMA issuers, one warp for the scales.  A CTA walks
 // output tiles of 128 rows x BN columns (persistent grid).
 #include <cuda_bf16.h>
+#include <string.h>
 
 #include "csa2_device.cuh"
 #include "csa2_e4m3.cuh"
@@ -852,8 +853,15 @@ cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ct
   p.w_ready = a.w_ready;
   p.err = ctx.err;
   if (a.rope_head) {
+    // the 32 powers take longer than the launch: the thread keeps the last theta's
+    static thread_local double known = 0.0;
+    static thread_local uint64_t turn[32];
     const double theta = a.rope_theta > 0.f ? a.rope_theta : 10000.0;
-    for (int i = 0; i < 32; ++i) p.turn[i] = rope_turn_rate(theta, i);
+    if (theta != known) {
+      for (int i = 0; i < 32; ++i) turn[i] = rope_turn_rate(theta, i);
+      known = theta;
+    }
+    memcpy(p.turn, turn, sizeof(turn));
   }
   switch (a.out_format) {
     case CSA2_OUT_F32: return launch_out<CSA2_OUT_F32>(a, p, ctx, st, why);

@@ -114,9 +114,10 @@ class DecodeStep:
                 continue
             pc = W.make_paged_cache(ents, seed=seed * 100 + ci, device=dev)
             ld = (max(ents) + 127) // 128 * 128
-            newest = torch.tensor([e - 1 for e in ents], dtype=torch.int64, device=dev)
-            slot = (pc.page_table.gather(1, (newest // 64)[:, None]).squeeze(1).long() * 64 + newest % 64).to(torch.int32)
-            pos = torch.tensor([(e - 1) * m for e in ents], dtype=torch.int32, device=dev)
+            # the step completes each sequence's newest entry: its slot and position
+            ctx = torch.tensor([(e - 1) * m for e in ents], dtype=torch.int32, device=dev)
+            slot, pos = torch.empty_like(ctx), torch.empty_like(ctx)
+            csa2.batch_plan(ctx, torch.full_like(ctx, m), m, page_table=pc.page_table, entry_slot=slot, entry_pos=pos)
             self.caches.append(CacheCopy(m, ents, pc, pc.n_entries, ld, slot, pos))
         self.inputs: dict[int, LayerInputs] = {}
         for l in self.layers:

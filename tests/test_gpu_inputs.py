@@ -466,6 +466,57 @@ def test_batch_plan_in_a_graph_follows_the_lengths():
         c, h = [a + b for a, b in zip(c, n)], want["free_head_out"][0]
 
 
+def test_batch_plan_more_rows_than_31_bits_count():
+    dev = need_gpu()
+    i32 = dict(dtype=torch.int32, device=dev)
+    big = 2 ** 31 - 1
+    start, seq, pos = torch.zeros(4, **i32), torch.full((40,), -9, **i32), torch.full((40,), -9, **i32)
+    csa2.batch_plan(torch.tensor([0, 0, 5], **i32), torch.tensor([big, big, 1], **i32), 2, row_start=start, row_seq=seq, row_pos=pos)
+    torch.cuda.synchronize()
+    assert csa2.check_device_error() == 6
+    assert np_(start).tolist() == [0, big, big, big] and (np_(seq) == 0).all() and np_(pos).tolist() == list(range(40))
+
+
+def test_decode_step_finds_its_newest_entries():
+    dev = need_gpu()
+    from serving_lightning_indexer_gb300.decode_step import DecodeStep
+    lengths = [4096, 130, 64, 2]
+    step = DecodeStep(lengths, seed=3, device=dev, layers=(2, 20))
+    torch.cuda.synchronize()
+    assert csa2.check_device_error() == 0
+    for ci, m in ((0, 2), (3, 1)):
+        c = step.caches[ci]
+        pt = np_(c.pc.page_table)
+        e = [n // m - 1 for n in lengths]
+        assert np_(c.entry_slot_new).tolist() == [int(pt[b, x // 64]) * 64 + x % 64 for b, x in enumerate(e)]
+        assert np_(c.entry_pos_new).tolist() == [x * m for x in e]
+
+
+@pytest.mark.parametrize("T", [24, 2200])
+def test_offsets_past_32_bits(T):
+    """Rows 2^20 elements apart (T = 2200: the last ones past 2^31 elements), and T = 24 rows 2^27 apart."""
+    dev = need_gpu()
+    g = _gen(dev, 31)
+    ld = 1 << (20 if T == 2200 else 27)
+    K, N = 272, 96
+    hidden = torch.empty(T * ld, dtype=torch.bfloat16, device=dev).view(T, ld)[:, :K]
+    hidden.copy_(torch.randn(T, K, generator=g, device=dev))
+    codes = torch.empty(T * ld, dtype=torch.uint8, device=dev).view(T, ld)[:, 64:64 + K]
+    scale = torch.empty(T, 3, device=dev)
+    csa2.quant_fp8(hidden, codes, scale)
+    w, ws = _codes((N, K), g, dev, 128)
+    out = torch.empty(T * ld, dtype=torch.bfloat16, device=dev).view(T, ld)[:, 128:128 + N]
+    csa2.fp8_linear(codes, scale, w, ws, out)
+    _sync_ok()
+    c2, s2, o2 = torch.empty(T, K, dtype=torch.uint8, device=dev), torch.empty(T, 3, device=dev), torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+    csa2.quant_fp8(hidden.contiguous(), c2, s2)
+    csa2.fp8_linear(c2, s2, w, ws, o2)
+    _sync_ok()
+    assert torch.equal(codes.contiguous(), c2) and torch.equal(scale, s2) and torch.equal(out.contiguous(), o2)
+    y, tol = _linear_ref(c2, s2, w, ws, None, 0, 0.0)
+    assert np.all(np.abs(np_(o2.float()) - y) <= 2.0 ** -8 * (np.abs(y) + tol) + tol)
+
+
 # ---------------------------------------------------------------- together, as a step uses them
 def test_a_step_from_lengths_and_hidden_states():
     """Two decode steps of three sequences: batch_plan, quant_fp8 and fp8_linear make every
