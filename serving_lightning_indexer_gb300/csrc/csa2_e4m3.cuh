@@ -11,11 +11,10 @@ constexpr float kE4m3Max = 448.f;
 // 448 / a stays finite in fp32 (a = 448 * 2^-120).
 constexpr float kAmaxFloor = 448.f * 7.52316384526264e-37f;
 
+constexpr float kLargest = 3.402823466e38f;  // finite fp32
 // An infinity or NaN as NaN, everything else unchanged.  fmaxf drops the NaN
 // from a block's maximum and the conversion below codes it 0x7F.
-__device__ __forceinline__ float finite_or_nan(float y) {
-  return fabsf(y) <= 3.402823466e38f ? y : __int_as_float(0x7FC00000);
-}
+__device__ __forceinline__ float finite_or_nan(float y) { return fabsf(y) <= kLargest ? y : __int_as_float(0x7FC00000); }
 // Scale of a block with the largest magnitude amax >= 0, and the factor that
 // takes its values to codes.
 __device__ __forceinline__ float e4m3_block(float amax, float* to_code) {

@@ -34,10 +34,11 @@ __device__ __forceinline__ void rope_angle(long long pos, uint64_t turn_rate, fl
 // The same angle through the fast sine and cosine, whose absolute error on
 // [-pi, pi] is below 2^-20.9: a fifth of the instructions where a thread turns
 // many pairs.  The rotated values are then off by under 2^-20 of the pair.
-__device__ __forceinline__ void rope_angle_fast(long long pos, uint64_t turn_rate, float* sn, float* cs) {
-  const uint64_t frac = static_cast<uint64_t>(pos) * turn_rate;
-  const int32_t t = static_cast<int32_t>(static_cast<uint32_t>(frac >> 32));
-  const float a = static_cast<float>(t) * 1.4629180792671596e-09f;  // 2 pi / 2^32
+__device__ __forceinline__ void rope_angle_fast(int pos, uint64_t turn_rate, float* sn, float* cs) {
+  // the top half of the product's low 64 bits, for pos in [0, 2^31)
+  const uint32_t p = static_cast<uint32_t>(pos);
+  const uint32_t top = p * static_cast<uint32_t>(turn_rate >> 32) + __umulhi(p, static_cast<uint32_t>(turn_rate));
+  const float a = static_cast<float>(static_cast<int32_t>(top)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
   *sn = __sinf(a);
   *cs = __cosf(a);
 }

@@ -36,6 +36,7 @@ __device__ __forceinline__ void unpack16(const uint4 (&v)[2], float (&y)[16]) {
     }
   }
 }
+// Largest finite magnitude; infinities become NaN.
 __device__ __forceinline__ float amax16(float (&y)[16]) {
   float a = 0.f;
 #pragma unroll
@@ -44,6 +45,15 @@ __device__ __forceinline__ float amax16(float (&y)[16]) {
     a = fmaxf(a, fabsf(y[i]));
   }
   return a;
+}
+// The same with the finite case apart (a NaN is dropped by fmaxf and coded as
+// such): 14.4 against 15.3 us for rows of 4,096 x 7,168, but registers that the
+// tiles' kernel has not (38.9 against 32.8 us there).
+__device__ __forceinline__ float amax16_rows(float (&y)[16]) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(y[i]));
+  return a > kLargest ? amax16(y) : a;
 }
 __device__ __forceinline__ uint4 codes16(const float (&y)[16], float f) {
   uint32_t r[4];
@@ -84,7 +94,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
     float y[16];
     unpack16(v[u], y);
     float f;
-    const float s = e4m3_block(max8(amax16(y)), &f);
+    const float s = e4m3_block(max8(amax16_rows(y)), &f);
     if (t[u] >= p.T || c[u] >= p.K) continue;
     *reinterpret_cast<uint4*>(p.codes + t[u] * p.ld_codes + c[u]) = codes16(y, f);
     if ((lane & 7) == 0) p.scale[t[u] * p.ld_scale + (c[u] >> 7)] = s;
@@ -146,7 +156,7 @@ __global__ void __launch_bounds__(256) quant_norm_kernel(const __grid_constant__
       for (int i = 0; i < 16; ++i) y[i] = 0.f;  // 0 * inv is NaN where inv is infinite
     }
     float f;
-    const float s = e4m3_block(max8(amax16(y)), &f);
+    const float s = e4m3_block(max8(amax16_rows(y)), &f);
     if (in) {
       *reinterpret_cast<uint4*>(p.codes + t * p.ld_codes + c) = codes16(y, f);
       if ((tid & 7) == 0) p.scale[t * p.ld_scale + (c >> 7)] = s;

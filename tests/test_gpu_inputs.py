@@ -190,7 +190,7 @@ def _check_linear(T, N, K, out, head=0, seed=0, theta=10000.0, x=None, xs=None, 
 
 SHAPES = [(1, 1, 16), (1, 512, 7168), (2, 130, 144), (7, 1001, 1360), (8, 4096, 2048), (16, 256, 128), (17, 384, 4112),
           (33, 640, 640), (64, 512, 7168), (65, 96, 2000), (128, 128, 256), (129, 257, 400), (200, 1024, 1024),
-          (333, 1001, 1360), (512, 512, 7168), (1000, 300, 272), (1300, 1001, 2064), (1300, 1000, 2192), (2500, 300, 1040)]
+          (333, 1001, 1360), (512, 512, 7168), (1000, 300, 272), (1300, 1001, 2064), (1300, 1000, 2192), (2500, 300, 1040), (2700, 2001, 400), (2700, 2000, 144)]
 
 
 @pytest.mark.parametrize("T,N,K", SHAPES)
@@ -203,7 +203,7 @@ def test_fp8_linear_matches_oracle(T, N, K, out):
     (1, 128, 128, "fp8", 0), (8, 4096, 2048, "fp8", 128), (3, 1024, 144, "bf16", 512), (130, 512, 272, "fp8", 0),
     (130, 768, 1040, "fp8", 128), (16, 1024, 2048, "fp8", 512), (33, 512, 640, "fp8", 256), (40, 1536, 528, "fp32", 256),
     (257, 2048, 512, "bf16", 512), (300, 640, 2048, "fp8", 128), (700, 4096, 384, "fp8", 128), (90, 384, 784, "bf16", 128),
-    (1300, 1024, 2064, "fp8", 128), (1300, 1152, 2192, "bf16", 384),
+    (1300, 1024, 2064, "fp8", 128), (1300, 1152, 2192, "bf16", 384), (1300, 4096, 272, "fp8", 128), (1411, 4352, 1040, "bf16", 256),
 ])
 def test_fp8_linear_rope_and_e4m3_output(T, N, K, out, head):
     _check_linear(T, N, K, out, head, seed=T * N + K, extra=32)
