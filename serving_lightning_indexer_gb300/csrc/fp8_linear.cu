@@ -3,10 +3,11 @@
 //
 // The tensor core applies no fp32 scale, so each block of 128 input dims gets an
 // accumulator of its own: four tcgen05.mma (K = 32 each) into one slot of a TMEM
-// ring, from which the accumulation warps take it, times the two scales, into
-// fp32 registers while the tensor core works on the next block.  Warp roles:
-// eight accumulation warps, a TMA producer, two MMA issuers, one warp for the scales.  A CTA walks
-// output tiles of 128 rows x BN columns (persistent grid).
+// ring, from which warps add it, times the two scales, to fp32 sums in registers
+// while the tensor core works on the next block.  Two kernels: 128 x 256 tiles for
+// many rows, bound by that chain (2.2 PFLOP/s at 4,096 x 2,048 x 32,768), and one for
+// few rows, bound by the weights' bytes (8 x 2,048 x 32,768: 12.7 us, 5.3 TB/s) or, where
+// they are few, by latency (8 x 7,168 x 512: 5.3 us).
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -21,7 +22,7 @@ namespace {
 constexpr int kTileM = 128;   // rows of x a tile
 constexpr int kBlockK = 128;  // input dims of a scale block: one swizzled 128-B row of codes
 constexpr int kAccWarps = 8;
-constexpr int kThreads = (kAccWarps + 4) * 32;  // 168 registers a thread: what the sums need; the other four warps are the roles below
+constexpr int kThreads = (kAccWarps + 4) * 32;  // 168 registers a thread, which 128 sums just fit
 
 struct LinearParams {
   const float* x_scale;
@@ -39,6 +40,14 @@ struct LinearParams {
   uint64_t turn[32];  // RoPE turn rates of the 32 pairs
 };
 
+// ---------------------------------------------------------------- many rows
+// A CTA walks output tiles of 128 rows x 256 columns (persistent grid, the tiles of
+// one column block behind each other so that its weights stay in L2).  Warps 0..7
+// add and write (a lane is a row, four warps a column half), 8 is the TMA producer,
+// 9 and 10 issue the products of one accumulator each, 11 brings the scales.  N =
+// 256 because an instruction costs 137 cycles there and 92 at N = 128.  A block
+// takes about 830 cycles: product and commit 566, sums 480, joined by four waits,
+// with two accumulators to overlap them.
 template <int BN>
 struct WideCfg {
   static constexpr int kStages = 4;
@@ -87,8 +96,8 @@ __device__ __forceinline__ uint4 out_piece(const float (&y)[C], int i, float f) 
     return make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
                       __float_as_uint(y[4 * i + 3]));
   if (OUT == CSA2_OUT_BF16)
-    return make_uint4(bf16x2(y[8 * i], y[8 * i + 1]), bf16x2(y[8 * i + 2], y[8 * i + 3]), bf16x2(y[8 * i + 4], y[8 * i + 5]),
-                      bf16x2(y[8 * i + 6], y[8 * i + 7]));
+    return make_uint4(bf16x2(y[8 * i], y[8 * i + 1]), bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                      bf16x2(y[8 * i + 4], y[8 * i + 5]), bf16x2(y[8 * i + 6], y[8 * i + 7]));
   return make_uint4(e4m3x4(y[16 * i] * f, y[16 * i + 1] * f, y[16 * i + 2] * f, y[16 * i + 3] * f),
                     e4m3x4(y[16 * i + 4] * f, y[16 * i + 5] * f, y[16 * i + 6] * f, y[16 * i + 7] * f),
                     e4m3x4(y[16 * i + 8] * f, y[16 * i + 9] * f, y[16 * i + 10] * f, y[16 * i + 11] * f),
@@ -230,8 +239,7 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
     constexpr int kSize = out_size(OUT), kPieces = C * kSize / 16;
     // 32 rows x 64 B at a time through shared memory (swizzled, so that the lanes'
     // 16-byte stores do not collide) and out by a tensor store; rows that are not
-    // 16-byte aligned (never e4m3) element by element, a row's 64 B by one half warp or
-    // warp
+    // 16-byte aligned (never e4m3) element by element, 64 B of a row side by side
 #pragma unroll
     for (int c = 0; c < kPieces; c += 4) {
       if (lane == 0) bulk_wait_read();
@@ -316,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Share<BN, SPLIT> mine(p);
   const int blocks = mine.blocks;
 
-  if (warp >= kAccWarps) {
-   if (warp == kAccWarps) {
+  if (warp == kAccWarps) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t keep = l2_policy_evict_last();
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long i = (it > S ? it - S : 0); i < it; ++i)
         mbar_wait(&full[i % S], static_cast<uint32_t>((i / S) & 1), nullptr);
     }
-   } else if (warp <= kAccWarps + NA) {
+  } else if (warp > kAccWarps && warp <= kAccWarps + NA) {
     // ------------------------------------------------------------ MMA issuers
     // One warp for each accumulator: the products of a block are queued while the
     // other warp still waits for its accumulator.
@@ -376,16 +383,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_error(p.err, kErrTimeout);
       }
     }
-   } else {
+  } else if (warp > kAccWarps + NA) {
     // ------------------------------------------------------------ scales
-    // A warp brings the scales of four blocks at a time into shared memory.
+    // Four blocks' at a time into shared memory: a load of an accumulation warp would
+    // be waited for at its next barrier arrival.
     long long g = 0;
     bool ok = true;
     for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
       const int n0 = mine.column(tile), t0 = mine.row(tile);
       const float* xs[4];  // of rows lane, lane + 32, ..
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xs[i] = p.x_scale + static_cast<long long>(min(t0 + i * 32 + lane, p.T - 1)) * p.ld_xs + mine.b0;
+      for (int i = 0; i < 4; ++i)
+        xs[i] = p.x_scale + static_cast<long long>(min(t0 + i * 32 + lane, p.T - 1)) * p.ld_xs + mine.b0;
       // lanes 0 and 1: the weight scales of a column half
       const float* ws = p.w_scale + static_cast<long long>(min(n0 + (lane & 1) * C, p.N - 1) >> 7) * p.ld_ws + mine.b0;
       for (int b = 0; b < blocks; b += 4, ++g) {
@@ -414,7 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       *s_abort = 1;
       set_error(p.err, kErrTimeout);
     }
-   }
   } else {
     if (!accumulate_and_store<BN, OUT, SPLIT>(map_out, p, smem, tmem, tfull, tempty, empty, sfull, sempty, s_abort)) {
       *s_abort = 1;
@@ -483,7 +491,7 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
 // MMA issuer, 2..9 accumulation (a lane is an output column; two groups of four
 // take the blocks in turn), all of them the output (a warp is a row of x).
 constexpr int kNarrowThreads = 320;
-constexpr int kScaleSeg = 32;  // blocks whose scales are staged at a time
+constexpr int kScaleSeg = 16;  // blocks whose scales are staged at a time (even)
 
 template <int NT>
 struct NarrowCfg {
@@ -606,7 +614,8 @@ __global__ void __launch_bounds__(kNarrowThreads)
       if (seg > 0) named_bar_sync(1, 256);  // the last segment has been used
       for (int i = tid; i < n * NT; i += 256) {
         const int t = i / n, b = i - t * n;
-        s_scale[b * NT + t] = t0 + t < p.T ? __ldg(p.x_scale + (t0 + t) * p.ld_xs + b0 + seg + b) * __ldg(ws + seg + b) : 0.f;
+        const float* xs = p.x_scale + (t0 + t) * p.ld_xs + b0 + seg;
+        s_scale[b * NT + t] = t0 + t < p.T ? __ldg(xs + b) * __ldg(ws + seg + b) : 0.f;
       }
       named_bar_sync(1, 256);
       for (int j = group; j < n && ok; j += 2) {  // kScaleSeg is even: a group keeps its blocks' parity
@@ -745,7 +754,8 @@ int narrow_clusters(const cudaLaunchConfig_t& cfg, int splits, int device) {
   int n = known[device][i].load(std::memory_order_acquire);
   if (n == 0) {
     // clusters above 8 CTAs have to be allowed, once, before the first is asked for
-    if (cudaFuncSetAttribute(fp8_linear_narrow_kernel<NT, OUT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+    if (cudaFuncSetAttribute(fp8_linear_narrow_kernel<NT, OUT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, fp8_linear_narrow_kernel<NT, OUT>, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       n = -1;

@@ -209,6 +209,48 @@ def test_fp8_linear_rope_and_e4m3_output(T, N, K, out, head):
     _check_linear(T, N, K, out, head, seed=T * N + K, extra=32)
 
 
+@pytest.mark.parametrize("T", [6, 1300])
+def test_fp8_linear_rope_far_positions_and_other_thetas(T):
+    """Positions up to 2^31 - 1 (the float64 angle is off by under 2^-21 there); the thetas in
+    turn, as a thread keeps the last one's rates."""
+    dev = need_gpu()
+    g = _gen(dev, 17)
+    x, xs = _codes((T, 272), g, dev, 1)
+    w, ws = _codes((1024, 272), g, dev, 128)
+    pos = torch.randint(2 ** 31 - 5000, 2 ** 31 - 1, (T,), generator=g, device=dev, dtype=torch.int64).to(torch.int32)
+    outs = {}
+    for theta in (500000.0, 0.0, 10000.0, 500000.0):
+        out = torch.empty(T, 1024, device=dev)
+        csa2.fp8_linear(x, xs, w, ws, out, row_pos=pos, rope_head=512, rope_theta=theta)
+        if theta in outs:
+            assert torch.equal(out, outs[theta])
+        outs[theta] = out
+    _sync_ok()
+    assert torch.equal(outs[0.0], outs[10000.0]) and not torch.equal(outs[0.0], outs[500000.0])
+    for theta in (10000.0, 500000.0):
+        y, tol = _linear_ref(x, xs, w, ws, pos, 512, theta)
+        z = np.abs(y).reshape(T, -1, 512)
+        extra = np.zeros_like(z)
+        extra[..., 448::2] = extra[..., 449::2] = 2.0 ** -21 * 1.5 * (z[..., 448::2] + z[..., 449::2])
+        assert np.all(np.abs(np_(outs[theta]) - y) <= tol + extra.reshape(T, -1) + U * np.abs(y))
+
+
+@pytest.mark.parametrize("T", [16, 300])
+def test_fp8_linear_padded_rows_stay_in_their_rows(T):
+    """Rows that batch_plan pads (position -1) change no other row."""
+    dev = need_gpu()
+    g = _gen(dev, 18)
+    x, xs = _codes((T, 512), g, dev, 1)
+    w, ws = _codes((512, 512), g, dev, 128)
+    pos = torch.arange(T, dtype=torch.int32, device=dev)
+    a, b = torch.empty(T, 512, device=dev), torch.empty(T, 512, device=dev)
+    csa2.fp8_linear(x, xs, w, ws, a, row_pos=pos, rope_head=128)
+    pos[T // 2:] = -1
+    csa2.fp8_linear(x, xs, w, ws, b, row_pos=pos, rope_head=128)
+    _sync_ok()
+    assert torch.equal(a[:T // 2], b[:T // 2]) and torch.isfinite(b).all()
+
+
 def test_fp8_linear_prefill_width_rows():
     """A prefill chunk's attention query projection, on sampled rows (the oracle takes whole rows)."""
     dev = need_gpu()
@@ -285,12 +327,13 @@ def test_fp8_linear_is_repeatable(T):
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
-def test_fp8_linear_on_two_streams_and_in_a_graph():
+@pytest.mark.parametrize("T", [12, 50, 700])
+def test_fp8_linear_on_two_streams_and_in_a_graph(T):
     dev = need_gpu()
     g = _gen(dev, 14)
-    x, xs = _codes((12, 1024), g, dev, 1)
+    x, xs = _codes((T, 1024), g, dev, 1)
     w, ws = _codes((4096, 1024), g, dev, 128)
-    want = torch.empty(12, 4096, device=dev)
+    want = torch.empty(T, 4096, device=dev)
     csa2.fp8_linear(x, xs, w, ws, want)
     torch.cuda.synchronize()
     a, b = torch.empty_like(want), torch.empty_like(want)
@@ -302,7 +345,7 @@ def test_fp8_linear_on_two_streams_and_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(a, want) and torch.equal(b, want)
     # captured: quantise, project; the weights' codes are not the previous launch's
-    h = torch.randn(12, 1024, generator=g, device=dev).to(torch.bfloat16)
+    h = torch.randn(T, 1024, generator=g, device=dev).to(torch.bfloat16)
     codes, sc, y = torch.empty_like(x), torch.empty_like(xs), torch.empty_like(want)
     with torch.cuda.stream(s1):
         gr = torch.cuda.CUDAGraph()
@@ -310,7 +353,7 @@ def test_fp8_linear_on_two_streams_and_in_a_graph():
             csa2.quant_fp8(h, codes, sc)
             csa2.fp8_linear(codes, sc, w, ws, y, w_ready=True)
     for k in range(3):
-        h.copy_(torch.randn(12, 1024, generator=g, device=dev))
+        h.copy_(torch.randn(T, 1024, generator=g, device=dev))
         gr.replay()
         torch.cuda.synchronize()
         y2 = torch.empty_like(want)
@@ -464,6 +507,20 @@ def test_batch_plan_in_a_graph_follows_the_lengths():
         assert np_(slot)[:k].tolist() == want["entry_slot"] and (np_(seq)[k:] == -1).all() and (np_(slot)[k:] == -1).all()
         assert np.array_equal(np_(table), t)
         c, h = [a + b for a, b in zip(c, n)], want["free_head_out"][0]
+
+
+@pytest.mark.parametrize("first,W", [(0, 64), (4, 64), (3, 64), (1, 30)])
+def test_batch_plan_writes_a_strided_window(first, W):
+    dev = need_gpu()
+    i32 = dict(dtype=torch.int32, device=dev)
+    wide = torch.full((50, 80), -7, **i32)
+    ctx, new = [0, 100, 17, 3], [9, 20, 0, 11]
+    csa2.batch_plan(torch.tensor(ctx, **i32), torch.tensor(new, **i32), 1, swa_ring=90, swa_slot=wide[:, first:first + W])
+    _sync_ok()
+    want = np.array(o.batch_plan(ctx, new, 1, ring=90, n_swa=W)[0]["swa_slot"])
+    got = np_(wide)
+    assert np.array_equal(got[:40, first:first + W], want)
+    assert (got[40:] == -7).all() and (got[:, :first] == -7).all() and (got[:, first + W:] == -7).all()
 
 
 def test_batch_plan_more_rows_than_31_bits_count():
