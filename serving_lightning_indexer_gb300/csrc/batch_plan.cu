@@ -1,11 +1,11 @@
 // The batch's rows, pages and slots from its sequences' lengths, in one launch.
 //
 // Per sequence: rows, new entries and new pages; an exclusive prefix sum of the
-// three places every row, entry and page.  Each CTA makes the sums for itself
-// (two loads a sequence, B <= 8192, in shared memory), which costs less than a
-// second launch or a wait between CTAs, and then fills its share of the
-// outputs: a warp a row, a thread an entry or a page.  Bound: launch latency for
-// a decode batch, the stores of swa_slot (4 * n_swa bytes a row) for prompts.
+// three places every row, entry and page.  Each CTA makes the sums that it needs
+// for itself (two loads a sequence, B <= 8192, in shared memory), which costs less
+// than a second launch or a wait between CTAs, and then fills its share of the
+// outputs: 32 rows at a time, or a thread an entry or a page.  Bound: launch and load
+// latency (8 sequences: 2.8 us; 256 with 8,260 rows: 5.5 us for 4.5 MB).
 #include <limits.h>
 
 #include "csa2_device.cuh"

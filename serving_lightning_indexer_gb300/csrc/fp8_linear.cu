@@ -7,7 +7,7 @@
 // while the tensor core works on the next block.  Two kernels: 128 x 256 tiles for
 // many rows, bound by that chain (2.2 PFLOP/s at 4,096 x 2,048 x 32,768), and one for
 // few rows, bound by the weights' bytes (8 x 2,048 x 32,768: 12.7 us, 5.3 TB/s) or, where
-// they are few, by latency (8 x 7,168 x 512: 5.3 us).
+// they are few, by latency (8 x 7,168 x 512: 4.7 us).
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -506,7 +506,7 @@ struct NarrowCfg {
 };
 
 template <int NT, int OUT>
-__global__ void __launch_bounds__(kNarrowThreads)
+__global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     fp8_linear_narrow_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                              const __grid_constant__ LinearParams p) {
   using Cfg = NarrowCfg<NT>;
@@ -624,21 +624,24 @@ __global__ void __launch_bounds__(kNarrowThreads)
         if (!ok) break;
         tc_fence_after();
         if (quad == 0 && lane == 0) mbar_arrive(&empty[b % S]);  // the products have read the stage
-        uint32_t v[NT / 16][16];
-#pragma unroll
-        for (int c = 0; c < NT / 16; ++c) tmem_ld32x16_async(taddr + a * NT + c * 16, v[c]);
-#pragma unroll
-        for (int c = 0; c < NT / 16; ++c) tmem_wait_ld16(v[c]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[a]);
         const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s_scale + j * NT);
 #pragma unroll
-        for (int i = 0; i < NT / 4; ++i) {
-          const ulonglong2 m = sc[i];
-          const uint32_t* q = &v[i / 4][(i % 4) * 4];
-          acc[2 * i] = fma_f32x2(pack_f32x2(__uint_as_float(q[0]), __uint_as_float(q[1])), m.x, acc[2 * i]);
-          acc[2 * i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(q[2]), __uint_as_float(q[3])), m.y, acc[2 * i + 1]);
+        for (int c = 0; c < NT / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld32x16_async(taddr + a * NT + c * 16, v);
+          tmem_wait_ld16(v);
+          if (c + 1 == NT / 16) {  // all of it is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[a]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const ulonglong2 m = sc[c * 4 + i];
+            uint64_t* s2 = acc + c * 8 + i * 2;
+            s2[0] = fma_f32x2(pack_f32x2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), m.x, s2[0]);
+            s2[1] = fma_f32x2(pack_f32x2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), m.y, s2[1]);
+          }
         }
       }
     }
@@ -744,23 +747,23 @@ __global__ void __launch_bounds__(kNarrowThreads)
   }
 }
 
-// Clusters of `splits` CTAs that run at once on the device (asked of the runtime
-// once a device, kernel and size).
+// Clusters of `splits` CTAs that run at once on the device, by the runtime's count
+// (one CTA an SM), which is asked for once a device, kernel and size.
 template <int NT, int OUT>
 int narrow_clusters(const cudaLaunchConfig_t& cfg, int splits, int device) {
+  constexpr auto kern = fp8_linear_narrow_kernel<NT, OUT>;
   static std::atomic<int> known[64][5];
   int i = 0;
   while ((1 << i) < splits) ++i;
   int n = known[device][i].load(std::memory_order_acquire);
   if (n == 0) {
     // clusters above 8 CTAs have to be allowed, once, before the first is asked for
-    if (cudaFuncSetAttribute(fp8_linear_narrow_kernel<NT, OUT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, fp8_linear_narrow_kernel<NT, OUT>, &cfg) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
-      n = -1;
+      n = 0;
     }
-    if (n == 0) n = -1;
+    if (n < 1) n = -1;
     known[device][i].store(n, std::memory_order_release);
   }
   return n;
@@ -805,13 +808,17 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
   attr[1].val.clusterDim.y = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  // The largest split whose clusters all run at once and whose CTAs keep two
-  // blocks each.
+  // The largest split whose CTAs keep two blocks each and run at once: up to 32 rows
+  // two CTAs an SM (8 rows, K = 4,096, N = 7,168: 8.6 us split by 4, 10.2 by 2; K = 7,168,
+  // N = 4,096: 8.2 by 8, 9.9 by 4), above and in clusters of 16 one.
+  const long long tiles = n_tiles * t_tiles;
   int splits = 16;
   for (; splits > 1; splits >>= 1) {
     cfg.gridDim = dim3(static_cast<unsigned>(n_tiles), t_tiles, splits);
     attr[1].val.clusterDim.z = splits;
-    if (2 * splits <= blocks && n_tiles * t_tiles <= narrow_clusters<NT, OUT>(cfg, splits, ctx.device)) break;
+    if (2 * splits <= blocks && (NT < 64 && splits <= 8 ? tiles * splits <= 2 * ctx.num_sms
+                                                        : tiles <= narrow_clusters<NT, OUT>(cfg, splits, ctx.device)))
+      break;
   }
   *taken = NT < 64 || (blocks + splits - 1) / splits + 7 <= wide_time(a, ctx);
   if (!*taken) return cudaSuccess;

