@@ -315,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
+  pdl_trigger();  // every CTA holds its TMEM
   const uint32_t tmem = *s_tmem;
   const Share<BN, SPLIT> mine(p);
   const int blocks = mine.blocks;
