@@ -397,7 +397,8 @@ CSA2_API int csa2_quant_fp8(const csa2_quant_fp8_args* args, void* stream);
  *   y[t][n] = sum_b x_scale[t][b] * w_scale[n / 128][b] * sum_{k in block b} x[t][k] * w[n][k]
  * x and its scales as csa2_quant_fp8 writes them with block_rows = 1, w (row =
  * output column) and its scales with block_rows = 128; products and sums are
- * held in fp32 and rounded once, to the output's type.
+ * held in fp32 and rounded once, to the output's type.  The two scales are
+ * multiplied first, and their product has to be in fp32's range.
  * RoPE (rope_head != 0): the columns form heads of rope_head columns (a
  * multiple of 128 that divides N); the last 64 of each head are turned in
  * interleaved pairs (D-64+2p, D-63+2p) by row_pos[t] * rope_theta^(-2p/64), the
@@ -407,7 +408,7 @@ CSA2_API int csa2_quant_fp8(const csa2_quant_fp8_args* args, void* stream);
  * scale for each 128 columns by the rule of csa2_quant_fp8: with N = 32 * 128
  * the query that csa2_index_score and csa2_reindex take.
  * Rows t < T and columns n < N are written and nothing else.  K is a multiple
- * of 16, at most 65536; N at most 2^28.  Alignment: x, w, out 16 B; ld_x and ld_w multiples of
+ * of 16, at most 65536; N at most 2^28, T at most 2^30.  Alignment: x, w, out 16 B; ld_x and ld_w multiples of
  * 16; row_pos, scales 4 B; for CSA2_OUT_FP8 ld_out a multiple of 16.  out must
  * not overlap an input.  No workspace; results do not depend on the launch's
  * timing (no atomics). */
@@ -463,7 +464,8 @@ CSA2_API int csa2_fp8_linear(const csa2_fp8_linear_args* args, void* stream);
  * negative length (read as 0), a sequence past pt_stride pages or INT32_MAX
  * tokens, an empty free list, a page that the table lacks, a ring shorter than
  * the above (the keys and records that this step overwrites become -1), a slot
- * past INT32_MAX.  B <= 8192.  No workspace. */
+ * past INT32_MAX.  B <= 8192.  No output may overlap an input (n_visible is not
+ * ctx_len: the lengths of the next step are the caller's to add).  No workspace. */
 typedef struct {
   int32_t B;
   const int32_t* ctx_len;                      /* [B] */

@@ -421,7 +421,7 @@ def fp8_linear(x, x_scale, w, w_scale, out, out_scale=None, row_pos=None, rope_h
     pw, ldw = _mat(w, "w", _U8, dev, (N, K))
     pxs, ldxs = _mat(x_scale, "x_scale", _F32, dev, (T, nb))
     pws, ldws = _mat(w_scale, "w_scale", _F32, dev, ((N + 127) // 128, nb))
-    kind = out.dtype
+    kind = getattr(out, "dtype", None)
     fmt = _OUT_FORMAT.get(kind)
     if fmt is None:
         raise TypeError(f"out: expected float32, bfloat16 or uint8, got {kind}")

@@ -532,6 +532,8 @@ int csa2_fp8_linear(const csa2_fp8_linear_args* a, void* stream) {
   if (a->K < 16 || a->K > 65536 || (a->K & 15))
     return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: K=%d must be a multiple of 16 in 16..65536", a->K);
   if (a->N > (1 << 28)) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: N=%d is above 2^28", a->N);
+  // a tile's last row is counted in 31 bits
+  if (a->T > (1 << 30)) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: T=%d is above 2^30", a->T);
   const int nb = (a->K + 127) / 128;
   if (a->ld_x < a->K || a->ld_w < a->K || a->ld_out < a->N || a->ld_x_scale < nb || a->ld_w_scale < nb)
     return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: a row stride is smaller than its row");
@@ -594,6 +596,18 @@ int csa2_batch_plan(const csa2_batch_plan_args* a, void* stream) {
                          a->entry_pos, a->entry_row, a->ring_id, a->swa_new, a->swa_slot};
   for (const void* w : words)
     if (!aligned4(w)) return fail(CSA2_ERR_ALIGN, "csa2_batch_plan: arrays must be 4-B aligned");
+  // every CTA reads the inputs while the first may be writing already
+  struct Words { const int32_t* at; long long n; };
+  const Words in[] = {{a->ctx_len, a->B}, {a->new_len, a->B}, {a->free_pages, a->n_free}, {a->free_head, 1}, {a->ring_id, a->B}};
+  const Words out[] = {{a->page_table, static_cast<long long>(a->B) * a->pt_stride}, {a->free_head_out, 1},
+                       {a->row_start, a->B + 1}, {a->n_visible, a->B}, {a->entry_start, a->B + 1},
+                       {a->row_seq, a->max_rows}, {a->row_pos, a->max_rows}, {a->entry_slot, a->max_entries},
+                       {a->entry_pos, a->max_entries}, {a->entry_row, a->max_entries}, {a->swa_new, a->max_rows},
+                       {a->swa_slot, a->max_rows * a->ld_swa}};
+  for (const Words& o : out)
+    for (const Words& i : in)
+      if (o.at && i.at && o.at < i.at + i.n && i.at < o.at + o.n)
+        return fail(CSA2_ERR_UNSUPPORTED, "csa2_batch_plan: an output overlaps an input");
   DeviceCtx ctx;
   cudaError_t e = csa2::device_ctx(&ctx);
   if (e != cudaSuccess) return cuda_fail(e, "csa2_batch_plan: device");

@@ -128,3 +128,31 @@ def test_binding_refuses_what_it_cannot_pass():
     n = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
         csa2.batch_plan(n, n)
+
+
+@pytest.mark.parametrize("T", [(1 << 30) + 1, (1 << 31) - 1])
+def test_fp8_linear_refuses_rows_past_its_counters(lib, T):
+    assert lib.csa2_fp8_linear(C.byref(_linear(T=T)), None) == 2
+    assert b"2^30" in lib.csa2_last_error_detail()
+
+
+_IN, _OUT = 0x100000, 0x200000   # 4-B aligned, never dereferenced, a megabyte apart
+
+
+@pytest.mark.parametrize("kw", [
+    {"n_visible": _IN}, {"n_visible": _IN + 7 * 4}, {"n_visible": _IN - 7 * 4}, {"row_start": _IN - 8 * 4},
+    {"entry_start": _IN + 0x1000}, {"row_pos": _IN + 0x1000 - 15 * 4, "max_rows": 16},
+    {"entry_pos": _IN + 7 * 4, "max_entries": 1}, {"swa_new": _IN, "swa_ring": 8, "max_rows": 1},
+    {"swa_slot": _IN - 0x1000, "swa_ring": 8, "n_swa": 4, "ld_swa": 1024, "max_rows": 2},
+    {"ring_id": _OUT, "row_seq": _OUT + 4, "max_rows": 3},
+    {"page_table": _OUT, "pt_stride": 4, "free_pages": _OUT + 31 * 4, "n_free": 9},
+    {"page_table": _OUT, "pt_stride": 4, "free_pages": _IN + 0x2000, "n_free": 9, "free_head": _OUT},
+    {"page_table": _OUT, "pt_stride": 4, "free_pages": _IN + 0x2000, "n_free": 9, "free_head_out": _IN + 0x2000 + 32},
+])
+def test_batch_plan_refuses_outputs_over_inputs(lib, kw):
+    """ctx_len and new_len of 8 sequences at _IN and _IN + 0x1000: a write over a word that
+    other CTAs still read."""
+    from serving_lightning_indexer_gb300 import csa2
+    a = csa2.BatchPlanArgs(**{**dict(B=8, ctx_len=_IN, new_len=_IN + 0x1000, ratio_m=1), **kw})
+    assert lib.csa2_batch_plan(C.byref(a), None) == 4
+    assert b"overlaps" in lib.csa2_last_error_detail()
