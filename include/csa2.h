@@ -378,8 +378,10 @@ CSA2_API int csa2_kv_project(const csa2_kv_project_args* args, void* stream);
  *   y = x, or with gamma (block_rows = 1 only) x / sqrt(mean(x^2) + eps) * gamma
  *   a = the largest |y| of the block's finite values, raised to 448 * 2^-120
  *   scale = a / 448 (1 for a block without a finite value other than 0)
- *   code  = e4m3 round-to-nearest-even of y * (448 / a), saturating at 448;
- *           an infinity or NaN becomes the NaN code 0x7F (its own element only)
+ *   code  = e4m3 round-to-nearest-even of y * 448 / a, saturating at 448; an
+ *           infinity or NaN becomes the NaN code 0x7F (its own element only).
+ *           Without gamma the code is the exact quotient's, ties included; with
+ *           it y and 448 / a carry fp32 roundings
  * The row's sum of squares is held in fp32.  K is a multiple of 16, at most
  * 16384.  Alignment: x, codes, gamma 16 B; ld_x a multiple of 8 and ld_codes of
  * 16.  codes must not overlap x.  No workspace. */

@@ -2,8 +2,8 @@
 // of the row's RMSNorm), or per 128 x 128 tile.
 //
 // Bound: HBM (2 B read and 1 B + 4/128 B written per value): rows of 4,096 x 7,168
-// take 14.4 us, 6.2 TB/s (a copy of as many bytes 14.3 us), tiles of 32,768 x 2,048
-// 32.8 us, 6.1 TB/s.  A decode step's few rows are launch and load latency (8 x
+// take 14.7 us, 6.1 TB/s (a copy of as many bytes 14.3 us), tiles of 32,768 x 2,048
+// 33.1 us, 6.1 TB/s.  A decode step's few rows are launch and load latency (8 x
 // 7,168 with the norm: 2.4 us).
 #include <cuda_bf16.h>
 
@@ -63,6 +63,27 @@ __device__ __forceinline__ uint4 codes16(const float (&y)[16], float f) {
   for (int i = 0; i < 4; ++i) r[i] = e4m3x4(y[4 * i] * f, y[4 * i + 1] * f, y[4 * i + 2] * f, y[4 * i + 3] * f);
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
+// The exact quotients' codes of bf16 values.  PACKED: two values an instruction, for
+// the rows (14.7 us for 4,096 x 7,168, 14.9 without); the tiles have not the registers
+// (32,768 x 2,048: 33.1 us without, 37.5 packed).
+template <bool PACKED>
+__device__ __forceinline__ uint4 codes16_exact(const float (&y)[16], float f, float low) {
+  float q[16];
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    if (PACKED) {
+      const uint64_t y2 = pack_f32x2(y[i], y[i + 1]);
+      const uint64_t rest = fma_f32x2(y2, pack_f32x2(low, low), pack_f32x2(-0.f, -0.f));
+      const float2 v = unpack_f32x2(fma_f32x2(y2, pack_f32x2(f, f), rest));
+      q[i] = v.x;
+      q[i + 1] = v.y;
+    } else {
+      q[i] = fmaf(y[i], f, y[i] * low);
+      q[i + 1] = fmaf(y[i + 1], f, y[i + 1] * low);
+    }
+  }
+  return codes16(q, 1.f);
+}
 // Maximum over the 8 lanes that hold one block of 128 columns.
 __device__ __forceinline__ float max8(float a) {
 #pragma unroll
@@ -72,7 +93,7 @@ __device__ __forceinline__ float max8(float a) {
 
 // Rows without a norm: a warp takes U runs of 512 columns, a lane 16 of each (a
 // block of 128 is 8 lanes, its maximum three shuffles); all of them are loaded
-// before the first is used (U = 2: 15.3 us where U = 1 took 16.5).
+// before the first is used (U = 2: 14.7 us where U = 1 took 15.6).
 template <int U>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantParams p, int chunks) {
   pdl_wait();
@@ -96,10 +117,10 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
   for (int u = 0; u < U; ++u) {
     float y[16];
     unpack16(v[u], y);
-    float f;
-    const float s = e4m3_block(max8(amax16_rows(y)), &f);
+    float f, low;
+    const float s = e4m3_block_exact(max8(amax16_rows(y)), &f, &low);
     if (t[u] >= p.T || c[u] >= p.K) continue;
-    *reinterpret_cast<uint4*>(p.codes + t[u] * p.ld_codes + c[u]) = codes16(y, f);
+    *reinterpret_cast<uint4*>(p.codes + t[u] * p.ld_codes + c[u]) = codes16_exact<true>(y, f, low);
     if ((lane & 7) == 0) p.scale[t[u] * p.ld_scale + (c[u] >> 7)] = s;
   }
 }
@@ -200,8 +221,8 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const __grid_constant_
   a = 0.f;
 #pragma unroll
   for (int w = 0; w < 8; ++w) a = fmaxf(a, part[w]);
-  float f;
-  const float s = e4m3_block(a, &f);
+  float f, low;
+  const float s = e4m3_block_exact(a, &f, &low);
   if (tid == 0) p.scale[rt * p.ld_scale + ct] = s;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -211,7 +232,7 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const __grid_constant_
       unpack16(v[r], y);
 #pragma unroll
       for (int i = 0; i < 16; ++i) y[i] = finite_or_nan(y[i]);
-      *reinterpret_cast<uint4*>(p.codes + row * p.ld_codes + c) = codes16(y, f);
+      *reinterpret_cast<uint4*>(p.codes + row * p.ld_codes + c) = codes16_exact<false>(y, f, low);
     }
   }
 }
