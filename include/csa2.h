@@ -467,7 +467,9 @@ CSA2_API int csa2_fp8_linear(const csa2_fp8_linear_args* args, void* stream);
  * tokens, an empty free list, a page that the table lacks, a ring shorter than
  * the above (the keys and records that this step overwrites become -1), a slot
  * past INT32_MAX.  B <= 8192.  No output may overlap an input (n_visible is not
- * ctx_len: the lengths of the next step are the caller's to add).  No workspace. */
+ * ctx_len: the lengths of the next step are the caller's to add), page_table
+ * being one of entry_slot's; the words between the rows of swa_slot are free.  No
+ * workspace. */
 typedef struct {
   int32_t B;
   const int32_t* ctx_len;                      /* [B] */

@@ -49,6 +49,23 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// `rows` runs of n words of device memory, ld words apart (ld >= n).
+struct PlanWords {
+  const int32_t* at;
+  long long n, rows = 1, ld = 0;
+  // Whether a run has a word in common with the words i (4-B aligned, i.rows == 1).
+  bool meets(const PlanWords& i) const {
+    if (!at || !i.at || n < 1 || i.n < 1 || rows < 1) return false;
+    // start of i as an offset into this window; of the runs that end behind it, the first
+    const long long s = static_cast<long long>(reinterpret_cast<uintptr_t>(i.at) / 4) -
+                        static_cast<long long>(reinterpret_cast<uintptr_t>(at) / 4);
+    if (s < n) return s + i.n > 0;
+    if (rows == 1) return false;
+    const long long q = (s - n) / ld;  // run q ends at or before s, run q + 1 behind it
+    return q + 1 < rows && s - q * ld + i.n > ld;
+  }
+};
+
 constexpr int kMaxDevices = 64;
 std::mutex g_ctx_mu;
 csa2::DeviceCtx g_ctx[kMaxDevices];
@@ -596,17 +613,19 @@ int csa2_batch_plan(const csa2_batch_plan_args* a, void* stream) {
                          a->entry_pos, a->entry_row, a->ring_id, a->swa_new, a->swa_slot};
   for (const void* w : words)
     if (!aligned4(w)) return fail(CSA2_ERR_ALIGN, "csa2_batch_plan: arrays must be 4-B aligned");
-  // every CTA reads the inputs while the first may be writing already
-  struct Words { const int32_t* at; long long n; };
-  const Words in[] = {{a->ctx_len, a->B}, {a->new_len, a->B}, {a->free_pages, a->n_free}, {a->free_head, 1}, {a->ring_id, a->B}};
-  const Words out[] = {{a->page_table, static_cast<long long>(a->B) * a->pt_stride}, {a->free_head_out, 1},
-                       {a->row_start, a->B + 1}, {a->n_visible, a->B}, {a->entry_start, a->B + 1},
-                       {a->row_seq, a->max_rows}, {a->row_pos, a->max_rows}, {a->entry_slot, a->max_entries},
-                       {a->entry_pos, a->max_entries}, {a->entry_row, a->max_entries}, {a->swa_new, a->max_rows},
-                       {a->swa_slot, a->max_rows * a->ld_swa}};
-  for (const Words& o : out)
-    for (const Words& i : in)
-      if (o.at && i.at && o.at < i.at + i.n && i.at < o.at + o.n)
+  // every CTA reads the inputs while others may be writing already; the table is an
+  // input of the entries' slots, an output where pages are handed out
+  const long long table = static_cast<long long>(a->B) * a->pt_stride;
+  const PlanWords in[] = {{a->ctx_len, a->B}, {a->new_len, a->B}, {a->free_pages, a->n_free}, {a->free_head, 1},
+                          {a->ring_id, a->B}, {a->entry_slot ? a->page_table : nullptr, table}};
+  const PlanWords out[] = {{a->free_pages ? a->page_table : nullptr, table}, {a->free_head_out, 1},
+                           {a->row_start, a->B + 1}, {a->n_visible, a->B}, {a->entry_start, a->B + 1},
+                           {a->row_seq, a->max_rows}, {a->row_pos, a->max_rows}, {a->entry_slot, a->max_entries},
+                           {a->entry_pos, a->max_entries}, {a->entry_row, a->max_entries}, {a->swa_new, a->max_rows},
+                           {a->swa_slot, a->n_swa, a->max_rows, a->ld_swa}};
+  for (const PlanWords& o : out)
+    for (const PlanWords& i : in)
+      if (!(&o == out && &i == in + 5) && o.meets(i))  // the table is extended in place
         return fail(CSA2_ERR_UNSUPPORTED, "csa2_batch_plan: an output overlaps an input");
   DeviceCtx ctx;
   cudaError_t e = csa2::device_ctx(&ctx);

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from gpu_util import need_gpu, np_
+from oracle import csa2_oracle as o
 from serving_lightning_indexer_gb300 import csa2
 from test_gpu_inputs import _sync_ok
 
@@ -53,3 +54,21 @@ def test_quant_fp8_borders_go_to_the_even_code(rows, exponent):
     assert np.array_equal(np_(scale)[:, 0], (a[::rows, 0].astype(np.float32) / np.float32(448)))
     bad = np_(codes) != want
     assert not bad.any(), f"{bad.sum()} of {bad.size} codes"
+
+
+# ---------------------------------------------------------------- the batch's arrays
+def test_batch_plan_writes_a_window_right_before_and_around_the_lengths():
+    """One allocation: the lengths between the rows of the window and right behind its last row."""
+    dev = need_gpu()
+    i32 = dict(dtype=torch.int32, device=dev)
+    ctx, new = [0, 100, 17, 3, 500, 0, 64, 9], [1, 1, 2, 0, 1, 1, 1, 1]
+    buf = torch.full((8 * 256 + 8,), -7, **i32)
+    buf[:8] = torch.tensor(ctx, **i32)
+    buf[2048:] = torch.tensor(new, **i32)
+    wide = buf[:2048].view(8, 256)
+    csa2.batch_plan(buf[:8], buf[2048:], 1, swa_ring=130, swa_slot=wide[:, 128:])
+    _sync_ok()
+    want = np.full(2056, -7)
+    want[:8], want[2048:] = ctx, new
+    want[:2048].reshape(8, 256)[:, 128:] = o.batch_plan(ctx, new, 1, ring=130, n_swa=128)[0]["swa_slot"]
+    assert np.array_equal(np_(buf), want)
