@@ -97,13 +97,18 @@ class StepBuffers:
 
 
 class DecodeStep:
-    """The 38-layer decode step of one batch of sequences with the given context lengths."""
+    """The 38-layer decode step of one batch of sequences with the given context lengths.
+    Every sequence completes an entry of each cache that the layers read, so it has at least
+    ratio_m tokens (2 with encoder layers, else 1)."""
 
     def __init__(self, lengths: list[int], seed: int, device, layers=LAYERS, out_bf16=True):
+        self.layers = tuple(layers)
+        need = max(ratio_of(cache_of(l)) for l in self.layers)
+        if not lengths or min(lengths) < need:
+            raise ValueError(f"DecodeStep: lengths {list(lengths)}: a sequence needs {need} tokens or more to complete an entry")
         self.lengths = list(lengths)
         self.B = len(lengths)
         self.device = device
-        self.layers = tuple(layers)
         dev = device
         self.caches: list[CacheCopy] = []
         for ci in range(4):
