@@ -404,7 +404,9 @@ CSA2_API int csa2_quant_fp8(const csa2_quant_fp8_args* args, void* stream);
  * RoPE (rope_head != 0): the columns form heads of rope_head columns (a
  * multiple of 128 that divides N); the last 64 of each head are turned in
  * interleaved pairs (D-64+2p, D-63+2p) by row_pos[t] * rope_theta^(-2p/64), the
- * rotation of the keys (csa2_compress_m2), before the rounding.  A row whose
+ * rotation of the keys (csa2_compress_m2), before the rounding.  The sine and
+ * cosine put fp32 output off by at most 2^-22 of the pair's length, bf16 and e4m3
+ * output, before its rounding, by at most 2^-21.  A row whose
  * position is negative (csa2_batch_plan's padding) gets values of no meaning.
  * Output: fp32, bf16, or (CSA2_OUT_FP8, N a multiple of 128) e4m3 codes with a
  * scale for each 128 columns by the rule of csa2_quant_fp8: with N = 32 * 128

@@ -31,16 +31,33 @@ __device__ __forceinline__ void rope_angle(long long pos, uint64_t turn_rate, fl
   sincosf(static_cast<float>(t) * 1.4629180792671596e-09f, sn, cs);  // 2 pi / 2^32
 }
 
-// The same angle through the fast sine and cosine, whose absolute error on
-// [-pi, pi] is below 2^-20.9: a fifth of the instructions where a thread turns
-// many pairs.  The rotated values are then off by under 2^-20 of the pair.
-__device__ __forceinline__ void rope_angle_fast(int pos, uint64_t turn_rate, float* sn, float* cs) {
-  // the top half of the product's low 64 bits, for pos in [0, 2^31)
+// The top 32 bits of the turn's fraction, for pos in [0, 2^31), in 32-bit products.
+__device__ __forceinline__ int32_t rope_turn(int pos, uint64_t turn_rate) {
   const uint32_t p = static_cast<uint32_t>(pos);
-  const uint32_t top = p * static_cast<uint32_t>(turn_rate >> 32) + __umulhi(p, static_cast<uint32_t>(turn_rate));
-  const float a = static_cast<float>(static_cast<int32_t>(top)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
+  return static_cast<int32_t>(p * static_cast<uint32_t>(turn_rate >> 32) + __umulhi(p, static_cast<uint32_t>(turn_rate)));
+}
+// The same angle as a fraction of a half turn through sincospif, which needs no
+// reduction and no product with pi: the turned pair is off by at most 2^-22.6 of its
+// length (all 2^32 angles against float64 on the GPU; rope_angle 2^-21.5).
+__device__ __forceinline__ void rope_angle_turns(int pos, uint64_t turn_rate, float* sn, float* cs) {
+  sincospif(static_cast<float>(rope_turn(pos, turn_rate)) * 4.656612873077393e-10f, sn, cs);  // 2^-31
+}
+
+// The same angle through the fast sine and cosine, for outputs whose rounding hides
+// their error, a fifth of the instructions: at most 2^-21.1 each, 2^-21.07 of the
+// pair's length together (all 2^32 angles against float64).
+__device__ __forceinline__ void rope_angle_fast(int pos, uint64_t turn_rate, float* sn, float* cs) {
+  const float a = static_cast<float>(rope_turn(pos, turn_rate)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
   *sn = __sinf(a);
   *cs = __cosf(a);
+}
+
+// RoPE of one interleaved pair (a, b) by the angle of (sn, cs), with its roundings
+// written out: the same bits from every kernel that turns the same pair.
+__device__ __forceinline__ void rope_pair(float& a, float& b, float sn, float cs) {
+  const float x = a, y = b;
+  a = __fmaf_rn(x, cs, -__fmul_rn(y, sn));
+  b = __fmaf_rn(x, sn, __fmul_rn(y, cs));
 }
 
 // Inverse RoPE of one interleaved pair (a, b): rotation by -pos * rate.

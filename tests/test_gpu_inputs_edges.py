@@ -6,7 +6,7 @@ import torch
 from gpu_util import need_gpu, np_
 from oracle import csa2_oracle as o
 from serving_lightning_indexer_gb300 import csa2
-from test_gpu_inputs import _sync_ok
+from test_gpu_inputs import _gen, _sync_ok
 
 pytestmark = pytest.mark.gpu
 
@@ -54,6 +54,71 @@ def test_quant_fp8_borders_go_to_the_even_code(rows, exponent):
     assert np.array_equal(np_(scale)[:, 0], (a[::rows, 0].astype(np.float32) / np.float32(448)))
     bad = np_(codes) != want
     assert not bad.any(), f"{bad.sum()} of {bad.size} codes"
+
+
+# ---------------------------------------------------------------- projection
+def _linear64(x, xs, w, ws):
+    """The product of the decoded codes with their scales in float64, and that of the magnitudes."""
+    T, K = x.shape
+    xd = x.view(torch.float8_e4m3fn).double() * xs.double().repeat_interleave(128, 1)[:, :K]
+    wd = w.view(torch.float8_e4m3fn).double() * ws.double().repeat_interleave(128, 0)[:len(w)].repeat_interleave(128, 1)[:, :K]
+    return xd @ wd.t(), xd.abs() @ wd.abs().t()
+
+
+def test_fp8_linear_one_row_through_both_kernels():
+    """Whole numbers whose sums are exact in any order, so that a row's fp32 output has the
+    same bits whether 8 rows or 1,300 are projected, rotated columns included."""
+    dev = need_gpu()
+    g = _gen(dev, 41)
+    table = torch.tensor([0x00, 0x38, 0xB8, 0x40, 0xC0], dtype=torch.uint8, device=dev)   # 0, 1, -1, 2, -2
+    T, N, K = 1300, 1024, 400
+    x = table[torch.randint(0, 5, (T, K), generator=g, device=dev)]
+    w = table[torch.randint(0, 5, (N, K), generator=g, device=dev)]
+    xs, ws = torch.ones(T, 4, device=dev), torch.ones(8, 4, device=dev)
+    pos = torch.randint(0, 2 ** 31 - 1, (T,), generator=g, device=dev, dtype=torch.int64).to(torch.int32)
+    many = torch.empty(T, N, device=dev)
+    csa2.fp8_linear(x, xs, w, ws, many, row_pos=pos, rope_head=256)
+    for n in (8, 20, 60):
+        few = torch.empty(n, N, device=dev)
+        csa2.fp8_linear(x[:n], xs[:n], w, ws, few, row_pos=pos[:n], rope_head=256)
+        _sync_ok()
+        assert torch.equal(few, many[:n]), f"{n}: {(few != many[:n]).sum().item()} of {few.numel()} values differ"
+    # the unrotated columns are the sums themselves
+    y, _ = _linear64(x, xs, w, ws)
+    keep = (torch.arange(N, device=dev) % 256) < 192
+    assert torch.equal(many[:, keep].double(), y[:, keep])
+
+
+def _rope64(y, pos, head, theta=10000.0):
+    rate = theta ** (-torch.arange(32, dtype=torch.float64, device=y.device) / 32)
+    ang = pos.double()[:, None] * rate
+    c, s = torch.cos(ang)[:, None], torch.sin(ang)[:, None]
+    z = y.reshape(len(y), -1, head).clone()
+    a, b = z[..., head - 64::2].clone(), z[..., head - 63::2].clone()
+    z[..., head - 64::2], z[..., head - 63::2] = a * c - b * s, a * s + b * c
+    return z.reshape(y.shape)
+
+
+@pytest.mark.parametrize("T", [8, 60, 1300])
+def test_fp8_linear_turns_fp32_output_to_fp32(T):
+    """Exact sums, so that the turn's own error shows.  Of a pair's length: the angle 2^-23.3
+    (its top bits as fp32: half a step of 2^7 in 2^32 turns) and 2^-26 (the rate); sine and
+    cosine of 2 steps of 2^-24 each, 2^-22.5 together; a product's and a sum's rounding 2^-23:
+    2^-21.2 in all.  float64's own angle is off by 2^-33 here."""
+    dev = need_gpu()
+    g = _gen(dev, 42)
+    table = torch.tensor([0x00, 0x38, 0xB8, 0x40, 0xC0], dtype=torch.uint8, device=dev)
+    x = table[torch.randint(0, 5, (T, 272), generator=g, device=dev)]
+    w = table[torch.randint(0, 5, (1024, 272), generator=g, device=dev)]
+    xs, ws = torch.ones(T, 3, device=dev), torch.ones(8, 3, device=dev)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=dev, dtype=torch.int32)
+    out = torch.empty(T, 1024, device=dev)
+    csa2.fp8_linear(x, xs, w, ws, out, row_pos=pos, rope_head=128)
+    _sync_ok()
+    y = _linear64(x, xs, w, ws)[0]
+    err = (out.double() - _rope64(y, pos, 128)).abs().view(T, -1, 2)
+    length = torch.linalg.vector_norm(y.view(T, -1, 2), dim=-1, keepdim=True)
+    assert bool((err <= 2.0 ** -21.2 * length).all()), f"worst {(err / length.clamp(min=1e-30)).max().log2().item()}"
 
 
 # ---------------------------------------------------------------- the batch's arrays
