@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         *s_abort = 1;
         set_error(p.err, kErrTimeout);
+        // the last product of this accumulator still reads its stage and writes TMEM
+        mbar_wait(&tfull[a], a_phase, nullptr);
       }
     }
   } else if (warp > kAccWarps + NA) {
@@ -429,6 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!accumulate_and_store<BN, OUT, SPLIT>(map_out, p, smem, tmem, tfull, tempty, empty, sfull, sempty, s_abort)) {
       *s_abort = 1;
       set_error(p.err, kErrTimeout);
+      if (lane == 0) bulk_wait_all();  // the last tile's output still leaves shared memory
+      __syncwarp();
       if (SPLIT) {  // the waits that gave up came before the cluster's two barriers
         cluster_sync();
         cluster_sync();
@@ -585,7 +589,8 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(128, NT);
-      for (int b = 0; b < blocks; ++b) {
+      int b = 0;
+      for (; b < blocks; ++b) {
         const int s = b % S, a = b % NA;
         if (!(ok = mbar_wait(&full[s], static_cast<uint32_t>(b / S) & 1u, s_abort))) break;
         if (b >= NA && !(ok = mbar_wait(&tempty[a], static_cast<uint32_t>(b / NA - 1) & 1u, s_abort))) break;
@@ -599,6 +604,9 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
       if (!ok) {
         *s_abort = 1;
         set_error(p.err, kErrTimeout);
+        // the last products still read their stages and write TMEM
+        for (int i = (b > NA ? b - NA : 0); i < b; ++i)
+          mbar_wait(&tfull[i % NA], static_cast<uint32_t>(i / NA) & 1u, nullptr);
       }
     }
   } else {
