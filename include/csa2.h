@@ -466,12 +466,12 @@ CSA2_API int csa2_fp8_linear(const csa2_fp8_linear_args* args, void* stream);
  * What does not fit is -1 (or not written, past max_rows, max_entries or
  * pt_stride) and recorded in the device error word (CSA2_ERR_DEVICE_BOUNDS): a
  * negative length (read as 0), a sequence past pt_stride pages or INT32_MAX
- * tokens, an empty free list, a page that the table lacks, a ring shorter than
- * the above (the keys and records that this step overwrites become -1), a slot
- * past INT32_MAX.  B <= 8192.  No output may overlap an input (n_visible is not
- * ctx_len: the lengths of the next step are the caller's to add), page_table
- * being one of entry_slot's; the words between the rows of swa_slot are free.  No
- * workspace. */
+ * tokens, a batch of INT32_MAX rows or more (row_start stops there), an empty
+ * free list, a page that the table lacks, a ring shorter than the above (the keys
+ * and records that this step overwrites become -1), a slot past INT32_MAX.
+ * B <= 8192.  No output may overlap an input (n_visible is not ctx_len: the
+ * lengths of the next step are the caller's to add), page_table being one of
+ * entry_slot's; the words between the rows of swa_slot are free.  No workspace. */
 typedef struct {
   int32_t B;
   const int32_t* ctx_len;                      /* [B] */

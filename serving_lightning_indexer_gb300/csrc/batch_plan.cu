@@ -190,7 +190,9 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(const __grid_c
     if (a.row_start) a.row_start[B] = rows;
     if (a.entry_start) a.entry_start[B] = entries;
     if (a.free_head_out) a.free_head_out[0] = clip(head + (a.free_pages ? pages : 0));
-    if ((has_rows && rows > a.max_rows) || (has_entries && entries > a.max_entries)) set_error(p.err, kErrBounds);
+    // sums stop at INT_MAX, which may then be short of the rows (the other counts are smaller)
+    if (rows == INT_MAX || (has_rows && rows > a.max_rows) || (has_entries && entries > a.max_entries))
+      set_error(p.err, kErrBounds);
   }
   if (is_rows) {
     fill_rows(p, ctx, row0, ring);

@@ -137,3 +137,18 @@ def test_batch_plan_writes_a_window_right_before_and_around_the_lengths():
     want[:8], want[2048:] = ctx, new
     want[:2048].reshape(8, 256)[:, 128:] = o.batch_plan(ctx, new, 1, ring=130, n_swa=128)[0]["swa_slot"]
     assert np.array_equal(np_(buf), want)
+
+
+def test_batch_plan_records_counts_past_31_bits_without_row_arrays():
+    """The counts of places stop at 2^31 - 1, also where only they are asked for."""
+    dev = need_gpu()
+    i32 = dict(dtype=torch.int32, device=dev)
+    big = 2 ** 31 - 1
+    zero = torch.zeros(2, **i32)
+    for new, bad in (([big, big], True), ([big, 1], True), ([big - 3, 2], False)):
+        start = torch.full((3,), -9, **i32)
+        csa2.batch_plan(zero, torch.tensor(new, **i32), 2, row_start=start)
+        torch.cuda.synchronize()
+        assert csa2.check_device_error() == (6 if bad else 0), new
+        if not bad:
+            assert np_(start).tolist() == [0, new[0], sum(new)]
