@@ -400,7 +400,9 @@ CSA2_API int csa2_quant_fp8(const csa2_quant_fp8_args* args, void* stream);
  * x and its scales as csa2_quant_fp8 writes them with block_rows = 1, w (row =
  * output column) and its scales with block_rows = 128; products and sums are
  * held in fp32 and rounded once, to the output's type.  The two scales are
- * multiplied first, and their product has to be in fp32's range.
+ * multiplied first, and their product has to be 0 or in fp32's normal range: one
+ * below 2^-126 loses bits or vanishes, one above 2^128 is infinite, whatever the
+ * codes bring it to.
  * RoPE (rope_head != 0): the columns form heads of rope_head columns (a
  * multiple of 128 that divides N); the last 64 of each head are turned in
  * interleaved pairs (D-64+2p, D-63+2p) by row_pos[t] * rope_theta^(-2p/64), the

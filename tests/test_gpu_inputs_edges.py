@@ -121,6 +121,23 @@ def test_fp8_linear_turns_fp32_output_to_fp32(T):
     assert bool((err <= 2.0 ** -21.2 * length).all()), f"worst {(err / length.clamp(min=1e-30)).max().log2().item()}"
 
 
+@pytest.mark.parametrize("T", [4, 40, 1300])
+@pytest.mark.parametrize("ex,ew", [(-63, -63), (-120, -6), (60, 60), (100, -100)])
+def test_fp8_linear_scales_at_the_ends_of_the_range(T, ex, ew):
+    """Products of two scales down to 2^-126, fp32's smallest normal number, are exact."""
+    dev = need_gpu()
+    g = _gen(dev, 43)
+    table = torch.tensor([0x00, 0x38, 0xB8], dtype=torch.uint8, device=dev)
+    K, N = 272, 256
+    x = table[torch.randint(0, 3, (T, K), generator=g, device=dev)]
+    w = table[torch.randint(0, 3, (N, K), generator=g, device=dev)]
+    xs, ws = torch.full((T, 3), 2.0 ** ex, device=dev), torch.full((2, 3), 2.0 ** ew, device=dev)
+    out = torch.empty(T, N, device=dev)
+    csa2.fp8_linear(x, xs, w, ws, out)
+    _sync_ok()
+    assert torch.equal(out.double(), _linear64(x, xs, w, ws)[0])
+
+
 # ---------------------------------------------------------------- the batch's arrays
 def test_batch_plan_writes_a_window_right_before_and_around_the_lengths():
     """One allocation: the lengths between the rows of the window and right behind its last row."""
