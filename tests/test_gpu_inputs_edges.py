@@ -6,9 +6,10 @@ import torch
 from gpu_util import need_gpu, np_
 from oracle import csa2_oracle as o
 from serving_lightning_indexer_gb300 import csa2
-from test_gpu_inputs import _gen, _sync_ok
+from test_gpu_inputs import _codes, _gen, _sync_ok
 
 pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
 
 
 # ---------------------------------------------------------------- quantiser
@@ -119,6 +120,41 @@ def test_fp8_linear_turns_fp32_output_to_fp32(T):
     err = (out.double() - _rope64(y, pos, 128)).abs().view(T, -1, 2)
     length = torch.linalg.vector_norm(y.view(T, -1, 2), dim=-1, keepdim=True)
     assert bool((err <= 2.0 ** -21.2 * length).all()), f"worst {(err / length.clamp(min=1e-30)).max().log2().item()}"
+
+
+# (T, N, K).  On 152 SMs a CTA of the few-rows kernel has 34 blocks (153 column tiles leave
+# no CTAs to split the input dims over), 33 (60 tiles split by 2), 32 (K = 65,536 split by
+# 16), 16 (the attention query's 256 tiles); the last is the many-rows kernel's, 256 a CTA.
+DEEP = [(8, 19500, 4240), (24, 19500, 4240), (64, 7680, 8208), (5, 130, 65536), (20, 130, 65536), (40, 130, 65536),
+        (8, 32768, 2048), (4096, 130, 65536)]
+
+
+@pytest.mark.parametrize("w_ready", [False, True])
+@pytest.mark.parametrize("T,N,K", DEEP)
+def test_fp8_linear_over_many_blocks(T, N, K, w_ready):
+    """The rings of stages, accumulators and scale segments go round several times.  Error:
+    (130 + 2 blocks) roundings of the sum of magnitudes, then the output's."""
+    dev = need_gpu()
+    g = _gen(dev, T + N + K)
+    x, xs = _codes((T, K), g, dev, 1)
+    w, ws = _codes((N, K), g, dev, 128)
+    y, mag = _linear64(x, xs, w, ws)
+    torch.cuda.synchronize()
+    tol = (130 + 2 * xs.shape[1]) * U * mag
+    out = torch.full((T, N), 7.0, device=dev)
+    csa2.fp8_linear(x, xs, w, ws, out, w_ready=w_ready)
+    _sync_ok()
+    assert bool(((out.double() - y).abs() <= U * y.abs() + tol).all())
+    if N % 512 == 0:
+        pos = torch.randint(0, 1 << 20, (T,), generator=g, device=dev, dtype=torch.int32)
+        out = torch.zeros(T, N, dtype=torch.bfloat16, device=dev)
+        csa2.fp8_linear(x, xs, w, ws, out, row_pos=pos, rope_head=512, w_ready=w_ready)
+        _sync_ok()
+        y = _rope64(y, pos, 512)
+        # a pair's values share their errors; RoPE's own are 2^-20 of the pair
+        z, t = y.abs().view(T, -1, 2), tol.view(T, -1, 2)
+        both = (t.sum(-1) + 2.0 ** -20 * z.sum(-1))[..., None].expand_as(z).reshape(T, N)
+        assert bool(((out.double() - y).abs() <= 2.0 ** -8 * (y.abs() + both) + both).all())
 
 
 @pytest.mark.parametrize("T", [4, 40, 1300])
