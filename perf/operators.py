@@ -147,6 +147,7 @@ def prepare(case, seed):
         kind = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.uint8}[case["out"]]
         s["out"] = torch.empty(T, N, dtype=kind, device=dev)
         s["out_scale"] = torch.empty(T, N // 128, device=dev) if case["out"] == "fp8" else None
+        torch.cuda.synchronize()  # run() passes w_ready: the weights were written well before the first call
         return s
     B, m, cap = case["B"], case["ratio_m"], case["max_rows"]
     ctx = torch.randint(0, case["max_ctx"] + 1, (B,), generator=g, device=dev, dtype=torch.int32)
