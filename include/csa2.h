@@ -382,8 +382,9 @@ CSA2_API int csa2_kv_project(const csa2_kv_project_args* args, void* stream);
  *           infinity or NaN becomes the NaN code 0x7F (its own element only).
  *           Without gamma the code is the exact quotient's, ties included; with
  *           it y and 448 / a carry fp32 roundings
- * The row's sum of squares is held in fp32.  K is a multiple of 16, at most
- * 16384.  Alignment: x, codes, gamma 16 B; ld_x a multiple of 8 and ld_codes of
+ * The row's sum of squares is held in fp32; where it passes that range (from
+ * magnitudes of 2^57 on) the row is normalised to zeros.  K is a multiple of 16, at
+ * most 16384.  Alignment: x, codes, gamma 16 B; ld_x a multiple of 8 and ld_codes of
  * 16.  codes must not overlap x.  No workspace. */
 typedef struct {
   const uint16_t* x; int64_t ld_x;             /* [T, K] bf16, row stride ld_x >= K */

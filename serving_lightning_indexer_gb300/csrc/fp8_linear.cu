@@ -7,7 +7,7 @@
 // while the tensor core works on the next block.  Two kernels: 128 x 256 tiles for
 // many rows, bound by that chain (2.2 PFLOP/s at 4,096 x 2,048 x 32,768), and one for
 // few rows, bound by the weights' bytes (8 x 2,048 x 32,768: 12.7 us, 5.3 TB/s) or, where
-// they are few, by latency (8 x 7,168 x 512: 4.7 us).
+// they are few, by latency (8 x 7,168 x 512: 4.6 us).
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -756,8 +756,9 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   }
 }
 
-// Clusters of `splits` CTAs that run at once on the device, by the runtime's count
-// (one CTA an SM), which is asked for once a device, kernel and size.
+// Clusters of `splits` CTAs that run at once on the device, by the runtime's count (an
+// SM holds one CTA of NT = 64, by its registers, and two of the others), which is asked
+// for once a device, kernel and size.
 template <int NT, int OUT>
 int narrow_clusters(const cudaLaunchConfig_t& cfg, int splits, int device) {
   constexpr auto kern = fp8_linear_narrow_kernel<NT, OUT>;
@@ -792,7 +793,7 @@ long long wide_time(const csa2_fp8_linear_args& a, const DeviceCtx& ctx) {
 
 // Launches the few-rows kernel, or sets *taken to false where 128 x 256 tiles take
 // less time.  Up to 32 rows the weights' bytes decide, and this kernel reads them
-// once; with more it has to run at once (one CTA an SM) and be the quicker by
+// once; with more it has to run at once (one CTA an SM, by its registers) and be the quicker by
 // wide_time's measure, a CTA's blocks and 7 (K = 7168, N = 512: 12.3 us here, 20 us
 // there for 512 rows, 32 and 20 us for 2,048).
 template <int NT, int OUT>
@@ -819,7 +820,8 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
   cfg.numAttrs = 2;
   // The largest split whose CTAs keep two blocks each and run at once: up to 32 rows
   // two CTAs an SM (8 rows, K = 4,096, N = 7,168: 8.6 us split by 4, 10.2 by 2; K = 7,168,
-  // N = 4,096: 8.2 by 8, 9.9 by 4), above and in clusters of 16 one.
+  // N = 4,096: 8.2 by 8, 9.9 by 4), above one; clusters of 16, and all above 32 rows, by
+  // the runtime's count, as clusters do not fill every SM.
   const long long tiles = n_tiles * t_tiles;
   int splits = 16;
   for (; splits > 1; splits >>= 1) {

@@ -49,8 +49,9 @@ __device__ __forceinline__ float amax16(float (&y)[16]) {
   return a;
 }
 // The same with the finite case apart (a NaN is dropped by fmaxf and coded as
-// such): 14.4 against 15.3 us for rows of 4,096 x 7,168, but registers that the
-// tiles' kernel has not (38.9 against 32.8 us there).
+// such): 14.7 against 15.7 us for rows of 4,096 x 7,168.  The tiles' kernel keeps the
+// one above, at the 80 registers that three CTAs an SM leave it (33.1 against 39.4 us
+// for 32,768 x 2,048).
 __device__ __forceinline__ float amax16_rows(float (&y)[16]) {
   float a = 0.f;
 #pragma unroll
