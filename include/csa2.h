@@ -27,6 +27,13 @@
  *   8. rows, page table, entry and SWA slots of a batch, from the lengths of
  *      its sequences                                        -> csa2_batch_plan
  *
+ * what stands between the layers and behind the last one (none in the pages):
+ *
+ *   9. the residual's addition, its RMSNorm and e4m3 codes  -> csa2_add_norm_fp8
+ *  10. projections with low-rank adapters of many requests  -> csa2_lora_linear
+ *  11. log probabilities, entropy and alternatives of the
+ *      answer's logits                                      -> csa2_logprobs
+ *
  * Conventions shared by every call
  *   - All pointers in the argument structs are DEVICE pointers to
  *     caller-owned memory (except the struct itself, which lives on the host
@@ -497,8 +504,93 @@ typedef struct {
 } csa2_batch_plan_args;
 CSA2_API int csa2_batch_plan(const csa2_batch_plan_args* args, void* stream);
 
+/* ---- 9. the residual's addition, RMSNorm and e4m3 codes -----------------------
+ *   r = x + residual, rounded to the residual's type (bf16 or fp32)
+ *   y = r / sqrt(mean(r^2) + eps) * gamma       (of the rounded r)
+ * residual_out receives r; codes and scale receive y by the rule of csa2_quant_fp8
+ * with block_rows = 1 and gamma (the input of csa2_fp8_linear); y, if given, receives
+ * y in bf16 (the input of csa2_kv_project).  At least one of codes and y; scale goes
+ * with codes.  residual_out may be residual itself (in place: the same pointer and
+ * row stride); apart from that no output may overlap an input or another output,
+ * which the call checks by the rows' places.  Rows t < T and columns k < K are
+ * written and nothing else.  The row's sum of squares is held in fp32; where it
+ * passes that range (from magnitudes of 2^57 on) y is zeros.  K is a multiple of 16,
+ * at most 16384.  Alignment: x, residual, residual_out, codes, y, gamma 16 B; row
+ * strides multiples of 16 B; scale 4 B.  No workspace. */
+typedef struct {
+  const uint16_t* x; int64_t ld_x;             /* [T, K] bf16, row stride ld_x >= K */
+  const void* residual; int64_t ld_residual;   /* [T, K] bf16 or fp32 */
+  void* residual_out; int64_t ld_residual_out; /* [T, K], the residual's type */
+  int32_t residual_f32;                        /* 0: bf16, 1: fp32 */
+  int32_t T, K;
+  const float* gamma; float eps;               /* [K] */
+  uint8_t* codes; int64_t ld_codes;            /* optional [T, K] */
+  float* scale; int64_t ld_scale;              /* [T, ceil(K / 128)], with codes */
+  uint16_t* y; int64_t ld_y;                   /* optional [T, K] bf16 */
+} csa2_add_norm_fp8_args;
+CSA2_API int csa2_add_norm_fp8(const csa2_add_norm_fp8_args* args, void* stream);
+
+/* ---- 10. projection with low-rank adapters of many requests --------------------
+ * The projection of csa2_fp8_linear, and beside it, for the rows that have one, an
+ * adapter i = row_adapter[t] of rank `rank`:
+ *   v[t][r] = adapter_scale[i] * sum_b x_scale[t][b] * sum_{k in block b} x[t][k] * a[i][r][k]
+ *   y[t][n] = (as csa2_fp8_linear) + sum_r v[t][r] * b[i][n][r]
+ * before RoPE and the rounding to the output's type.  row_adapter[t] = -1: none (the
+ * row's output is then that of csa2_fp8_linear); an id outside [-1, n_adapters)
+ * counts as none and is recorded (CSA2_ERR_DEVICE_BOUNDS).  Rows of one adapter may
+ * be anywhere; side by side they take the least time.  v is held as the bf16 nearest
+ * to its fp32 sum for bf16 output, as the sum of two bf16 (2^-17 of it) for fp32 and
+ * e4m3 output.  An infinity or NaN of one adapter stays in its own rows.
+ * base: the arguments of csa2_fp8_linear, with its rules; T at most 2^20; w_ready = 1
+ * says the same of a, b, adapter_scale and row_adapter as of w and w_scale.  rank is
+ * a multiple of 8, at most 128; n_adapters >= 1, n_adapters * N at most 2^30.  An
+ * adapter of a smaller rank is padded with zeros.  Alignment: a, b 16 B; row_adapter,
+ * adapter_scale 4 B; workspace 16 B: csa2_workspace_size(CSA2_CALL_LORA_LINEAR, args,
+ * &bytes), read and written until the call's work is done.  Results do not depend on
+ * the launch's timing (no atomics); the order in which a row's parts are added, and so
+ * its last bits, can depend on which adapters the rows around it have. */
+typedef struct {
+  csa2_fp8_linear_args base;
+  const int32_t* row_adapter;                  /* [T] in [0, n_adapters) or -1 */
+  int32_t n_adapters, rank;
+  const uint16_t* a;                           /* [n_adapters, rank, K] bf16 */
+  const uint16_t* b;                           /* [n_adapters, N, rank] bf16 */
+  const float* adapter_scale;                  /* optional [n_adapters]; NULL: 1 */
+} csa2_lora_linear_args;
+CSA2_API int csa2_lora_linear(const csa2_lora_linear_args* args, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- 11. log probabilities, entropy and alternatives ---------------------------
+ * Of a row x of V logits (as csa2_fp8_linear writes them), over its finite ones:
+ *   lse = ln sum_v e^x[v]
+ *   logprob = x[token] - lse                    (-inf if x[token] is not finite)
+ *   entropy = -sum_v p[v] ln p[v],  p[v] = e^(x[v] - lse)
+ *   top_id, top_logprob: the n_top largest x, best first, ties to the lower id, and
+ *   their log probabilities; -1 and -inf where fewer are finite.
+ * An infinity or NaN among the logits has no part in a row (a masked token's -inf;
+ * the type's lowest value is a logit like any other).  A row without a finite logit
+ * has lse -inf and entropy 0; a log probability past fp32's range is -inf.  token[t] = -1: no token, logprob 0; an id outside
+ * [-1, V) counts as none and is recorded (CSA2_ERR_DEVICE_BOUNDS).  Every output is
+ * optional, but one has to be there; logprob goes with token.  Sums are held in fp32,
+ * the largest term apart, so that a likely token's log probability keeps its digits.
+ * T * V is not limited; V at most 2^30, T at most 2^27, n_top at most 32.
+ * Alignment: logits their own size (rows may start anywhere; 16-B aligned rows are
+ * read fastest), the rest 4 B.  Outputs must not overlap the logits.  No workspace. */
+typedef struct {
+  const void* logits; int64_t ld_logits;       /* [T, V] bf16 or fp32, row stride ld_logits >= V */
+  int32_t logits_f32;                          /* 0: bf16, 1: fp32 */
+  int32_t T, V;
+  const int32_t* token;                        /* [T], with logprob */
+  float* logprob;                              /* optional [T] */
+  float* entropy;                              /* optional [T] */
+  float* lse;                                  /* optional [T] */
+  int32_t n_top;                               /* 0..32 */
+  int32_t* top_id; float* top_logprob; int64_t ld_top; /* optional [T, n_top], row stride ld_top >= n_top */
+} csa2_logprobs_args;
+CSA2_API int csa2_logprobs(const csa2_logprobs_args* args, void* stream);
+
 /* ---- workspace, device errors ------------------------------------------------ */
-enum { CSA2_CALL_INDEX_SCORE = 1, CSA2_CALL_TOPK = 2, CSA2_CALL_REINDEX = 3, CSA2_CALL_SPARSE_ATTN = 4 };
+enum { CSA2_CALL_INDEX_SCORE = 1, CSA2_CALL_TOPK = 2, CSA2_CALL_REINDEX = 3, CSA2_CALL_SPARSE_ATTN = 4,
+       CSA2_CALL_LORA_LINEAR = 5 };
 /* Bytes of workspace the call needs with these arguments (0 if none). */
 CSA2_API int csa2_workspace_size(int which_call, const void* args, size_t* bytes);
 /* Synchronises the stream, then returns CSA2_ERR_DEVICE_BOUNDS or

@@ -686,3 +686,55 @@ def batch_plan(ctx_len, new_len, ratio_m, page_table=None, free_pages=None, free
     out["entry_start"].append(len(out["entry_pos"]))
     out["free_head_out"] = [free_head]
     return out, table, bad
+
+
+# ---------------------------------------------------------------------------
+# Between the layers and behind the last one (no counterpart in the pages): the
+# residual's addition with its norm, low-rank adapters, log probabilities
+# ---------------------------------------------------------------------------
+
+def bf16_round(v: np.ndarray) -> np.ndarray:
+    """The bf16 value nearest to v, ties to the even one (float64 in and out; finite v)."""
+    v = np.asarray(v, dtype=np.float64)
+    _, e = np.frexp(v)                      # |v| in [2^(e-1), 2^e)
+    step = np.exp2(np.maximum(e, -125) - 8.0)
+    r = np.rint(v / step) * step
+    return np.where(np.abs(r) >= 2.0 ** 128, np.copysign(np.inf, r), r)
+
+
+def add_norm_rows(x, residual, gamma, eps, fp32=False):
+    """(r, y): r = x + residual rounded to bf16 or fp32, y its RMSNorm."""
+    r = np.asarray(x, dtype=np.float64) + np.asarray(residual, dtype=np.float64)
+    r = r.astype(np.float32).astype(np.float64) if fp32 else bf16_round(r)
+    return r, rms_norm_rows(r, gamma, eps)
+
+
+def lora_rows(x, a, b, row_adapter, adapter_scale):
+    """What the adapters add: of row t with adapter i, scale[i] * (x[t] a[i]^T) b[i]^T (0 without
+    one).  x [T,K] the decoded rows, a [n,rank,K], b [n,N,rank]."""
+    out = np.zeros((x.shape[0], b.shape[1]))
+    for t, i in enumerate(row_adapter):
+        if i >= 0:
+            out[t] = adapter_scale[i] * (b[i] @ (a[i] @ x[t]))
+    return out
+
+
+def logprobs_row(x, token=-1, n_top=0):
+    """Of a row of logits, over its finite ones: (log probability of token, entropy, log-sum-exp,
+    the n_top best ids, their log probabilities)."""
+    x = np.asarray(x, dtype=np.float64)
+    fin = np.isfinite(x)
+    ids, best = np.full(n_top, -1), np.full(n_top, -np.inf)
+    if not fin.any():
+        return (0.0 if token < 0 else -np.inf), 0.0, -np.inf, ids, best
+    top = x[fin].max()
+    at = int(np.argmax(np.where(fin, x, -np.inf)))
+    e = np.where(fin, np.exp(np.where(fin, x, -np.inf) - top), 0.0)
+    rest = np.delete(e, at).sum()
+    lt = np.log1p(rest)
+    d = np.where(e > 0, np.where(fin, x, top) - top, 0.0)
+    entropy = lt - (e * d).sum() / (1 + rest)
+    order = np.lexsort((np.arange(x.size), -np.where(fin, x, -np.inf)))[:min(n_top, int(fin.sum()))]
+    ids[:order.size], best[:order.size] = order, (x[order] - top) - lt
+    lp = 0.0 if token < 0 else ((x[token] - top) - lt if fin[token] else -np.inf)
+    return lp, entropy, top + lt, ids, best

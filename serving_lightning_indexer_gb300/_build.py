@@ -18,7 +18,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libcsa2.so")
 SOURCES = ["csa2_api.cu", "index_score.cu", "select.cu", "sparse_attn.cu", "compress.cu", "topk_noalloc.cu",
-           "quant_fp8.cu", "fp8_linear.cu", "batch_plan.cu"]
+           "quant_fp8.cu", "fp8_linear.cu", "batch_plan.cu", "add_norm.cu", "lora.cu", "logprobs.cu"]
 HEADERS = [os.path.join(ROOT, "include", "csa2.h")] + [
     os.path.join(CSRC, f) for f in ("csa2_device.cuh", "csa2_rope.cuh", "csa2_e4m3.cuh", "csa2_internal.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,0 +1,181 @@
+// The residual's addition, its RMSNorm, and the e4m3 codes of the result:
+//   r = round(x + residual),  y = r / sqrt(mean(r^2) + eps) * gamma,  codes(y)
+//
+// Bound: HBM, each value read and written once: 7 B a value with a bf16 residual
+// (2 + 2 read, 2 + 1 written), 11 with an fp32 one.  A decode step's few rows are
+// launch and load latency.
+#include <cuda_bf16.h>
+
+#include "csa2_device.cuh"
+#include "csa2_e4m3.cuh"
+#include "csa2_internal.h"
+
+namespace csa2 {
+namespace {
+
+struct AddNormParams {
+  const __nv_bfloat16* x;
+  const void* residual;
+  void* residual_out;
+  const float* gamma;
+  uint8_t* codes;
+  float* scale;
+  __nv_bfloat16* y;
+  long long ld_x, ld_res, ld_out, ld_codes, ld_scale, ld_y;
+  int K;
+  float eps;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void pack16(const float (&y)[16], uint4 (&v)[2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    v[h] = make_uint4(pack_bf16(y[8 * h], y[8 * h + 1]), pack_bf16(y[8 * h + 2], y[8 * h + 3]),
+                      pack_bf16(y[8 * h + 4], y[8 * h + 5]), pack_bf16(y[8 * h + 6], y[8 * h + 7]));
+}
+
+// A CTA takes a row and keeps it in registers between the sum of squares and the
+// codes; V: runs of 16 columns a thread holds.  The sum is normalised as it is
+// stored, so that the result does not depend on whether a later launch reads the
+// residual again.  A thread writes only columns that it has read, which is what
+// allows residual_out to be residual.
+template <int V, bool F32>
+__global__ void __launch_bounds__(256) add_norm_kernel(const __grid_constant__ AddNormParams p) {
+  constexpr int kWords = F32 ? 4 : 2;  // 16-byte words of a run of the residual
+  __shared__ float part[8];
+  pdl_wait();
+  pdl_trigger();
+  const long long t = blockIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const __nv_bfloat16* x = p.x + t * p.ld_x;
+  const uint4* res = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.residual) + t * p.ld_res * (F32 ? 4 : 2));
+  uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.residual_out) + t * p.ld_out * (F32 ? 4 : 2));
+  uint4 xv[V][2], rv[V][kWords];
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    const int c = (r * threads + tid) * 16;
+    if (c < p.K) {
+      const uint4* src = reinterpret_cast<const uint4*>(x + c);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) xv[r][i] = src[i];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) rv[r][i] = res[c / 16 * kWords + i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) xv[r][i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) rv[r][i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    float a[16], b[16];
+    unpack16(xv[r], a);
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        b[4 * i] = a[4 * i] + __uint_as_float(rv[r][i].x);
+        b[4 * i + 1] = a[4 * i + 1] + __uint_as_float(rv[r][i].y);
+        b[4 * i + 2] = a[4 * i + 2] + __uint_as_float(rv[r][i].z);
+        b[4 * i + 3] = a[4 * i + 3] + __uint_as_float(rv[r][i].w);
+        rv[r][i] = make_uint4(__float_as_uint(b[4 * i]), __float_as_uint(b[4 * i + 1]), __float_as_uint(b[4 * i + 2]),
+                              __float_as_uint(b[4 * i + 3]));
+      }
+    } else {
+      unpack16(rv[r], b);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) b[i] += a[i];
+      pack16(b, rv[r]);
+      unpack16(rv[r], b);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ss = fmaf(b[i], b[i], ss);
+  }
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    const int c = (r * threads + tid) * 16;
+    if (c < p.K) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) out[c / 16 * kWords + i] = rv[r][i];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (threads > 32) {
+    if ((tid & 31) == 0) part[tid >> 5] = ss;
+    __syncthreads();
+    ss = 0.f;
+    for (int w = 0; w < threads >> 5; ++w) ss += part[w];
+  }
+  const float inv = 1.0f / sqrtf(ss / static_cast<float>(p.K) + p.eps);
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    const int c = (r * threads + tid) * 16;
+    const bool in = c < p.K;
+    float y[16];
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[4 * i] = __uint_as_float(rv[r][i].x);
+        y[4 * i + 1] = __uint_as_float(rv[r][i].y);
+        y[4 * i + 2] = __uint_as_float(rv[r][i].z);
+        y[4 * i + 3] = __uint_as_float(rv[r][i].w);
+      }
+    } else {
+      unpack16(rv[r], y);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 g = in ? __ldg(reinterpret_cast<const float4*>(p.gamma + c + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      y[i] = y[i] * inv * g.x;
+      y[i + 1] = y[i + 1] * inv * g.y;
+      y[i + 2] = y[i + 2] * inv * g.z;
+      y[i + 3] = y[i + 3] * inv * g.w;
+    }
+    if (!in) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = 0.f;  // 0 * inv is NaN where inv is infinite
+    }
+    if (p.y && in) {
+      uint4 h[2];
+      pack16(y, h);
+      uint4* dst = reinterpret_cast<uint4*>(p.y + t * p.ld_y + c);
+      dst[0] = h[0];
+      dst[1] = h[1];
+    }
+    if (p.codes) {
+      float f;
+      const float s = e4m3_block(max8(amax16_rows(y)), &f);
+      if (in) {
+        *reinterpret_cast<uint4*>(p.codes + t * p.ld_codes + c) = codes16(y, f);
+        if ((tid & 7) == 0) p.scale[t * p.ld_scale + (c >> 7)] = s;
+      }
+    }
+  }
+}
+
+template <int V>
+cudaError_t launch_v(const csa2_add_norm_fp8_args& a, const AddNormParams& p, cudaStream_t st) {
+  // whole warps, no more than the row's runs need
+  const int threads = ((a.K + 16 * V - 1) / (16 * V) + 31) / 32 * 32;
+  const dim3 grid(static_cast<unsigned>(a.T)), block(threads);
+  return a.residual_f32 ? launch_pdl(add_norm_kernel<V, true>, grid, block, 0, st, p)
+                        : launch_pdl(add_norm_kernel<V, false>, grid, block, 0, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_add_norm_fp8(const csa2_add_norm_fp8_args& a, cudaStream_t st) {
+  const AddNormParams p{reinterpret_cast<const __nv_bfloat16*>(a.x), a.residual, a.residual_out, a.gamma, a.codes, a.scale,
+                        reinterpret_cast<__nv_bfloat16*>(a.y), a.ld_x, a.ld_residual, a.ld_residual_out, a.ld_codes,
+                        a.ld_scale, a.ld_y, a.K, a.eps};
+  if (a.K <= 4096) return launch_v<1>(a, p, st);
+  if (a.K <= 8192) return launch_v<2>(a, p, st);
+  return launch_v<4>(a, p, st);
+}
+
+}  // namespace csa2

@@ -71,6 +71,23 @@ std::mutex g_ctx_mu;
 csa2::DeviceCtx g_ctx[kMaxDevices];
 bool g_ctx_ok[kMaxDevices];
 
+// `rows` runs of n bytes of device memory, ld bytes apart (ld >= n); NULL: none.
+struct ByteRows {
+  const void* at;
+  long long n, rows, ld;
+  // Whether a run of this and a run of o have a byte in common: exact for equal
+  // strides or one run each, else whether the runs' spans meet.
+  bool meets(const ByteRows& o) const {
+    if (!at || !o.at) return false;
+    const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(o.at)) -
+                        static_cast<long long>(reinterpret_cast<uintptr_t>(at));
+    if (d >= (rows - 1) * ld + n || -d >= (o.rows - 1) * o.ld + o.n) return false;
+    if (ld != o.ld || rows == 1 || o.rows == 1) return true;
+    const long long r = ((d % ld) + ld) % ld, q = (d - r) / ld;  // o's first run starts at byte r of run q's stride
+    return (r < n && q < rows && -q < o.rows) || (r + o.n > ld && q + 1 < rows && -(q + 1) < o.rows);
+  }
+};
+
 int rows_check(const csa2_rows& r, const char* who) {
   if (r.T < 1 || r.B < 1) return fail(CSA2_ERR_SHAPE, "%s: T=%d and B=%d must be >= 1", who, r.T, r.B);
   if (!r.n_visible && !r.row_pos) return fail(CSA2_ERR_NULL, "%s: one of n_visible, row_pos is required", who);
@@ -82,6 +99,60 @@ int rows_check(const csa2_rows& r, const char* who) {
 
 csa2::RowsHost rows_host(const csa2_rows& r) {
   return csa2::RowsHost{r.T, r.B, r.row_seq, r.row_pos, r.n_visible, r.row_pos ? r.ratio_m : 1};
+}
+
+// The rules of csa2_fp8_linear's arguments; `who` names the entry point.
+int linear_check(const csa2_fp8_linear_args* a, const char* who) {
+  if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->out)
+    return fail(CSA2_ERR_NULL, "%s: x/x_scale/w/w_scale/out is NULL", who);
+  if (a->T < 1 || a->N < 1) return fail(CSA2_ERR_SHAPE, "%s: T=%d and N=%d must be >= 1", who, a->T, a->N);
+  if (a->K < 16 || a->K > 65536 || (a->K & 15))
+    return fail(CSA2_ERR_SHAPE, "%s: K=%d must be a multiple of 16 in 16..65536", who, a->K);
+  if (a->N > (1 << 28)) return fail(CSA2_ERR_SHAPE, "%s: N=%d is above 2^28", who, a->N);
+  // a tile's last row is counted in 31 bits
+  if (a->T > (1 << 30)) return fail(CSA2_ERR_SHAPE, "%s: T=%d is above 2^30", who, a->T);
+  const int nb = (a->K + 127) / 128;
+  if (a->ld_x < a->K || a->ld_w < a->K || a->ld_out < a->N || a->ld_x_scale < nb || a->ld_w_scale < nb)
+    return fail(CSA2_ERR_SHAPE, "%s: a row stride is smaller than its row", who);
+  if (a->ld_x >= (1LL << 39) || a->ld_w >= (1LL << 39))
+    return fail(CSA2_ERR_SHAPE, "%s: ld_x and ld_w must be below 2^39", who);
+  if (a->out_format != CSA2_OUT_F32 && a->out_format != CSA2_OUT_BF16 && a->out_format != CSA2_OUT_FP8)
+    return fail(CSA2_ERR_UNSUPPORTED, "%s: out_format=%d is not fp32 (0), bf16 (1) or e4m3 (2)", who, a->out_format);
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->out) || (a->ld_x & 15) || (a->ld_w & 15))
+    return fail(CSA2_ERR_ALIGN, "%s: x, w, out must be 16-B aligned, ld_x and ld_w multiples of 16", who);
+  if (!aligned4(a->x_scale) || !aligned4(a->w_scale) || !aligned4(a->row_pos) || !aligned4(a->out_scale))
+    return fail(CSA2_ERR_ALIGN, "%s: scales and row_pos must be 4-B aligned", who);
+  if (a->out_format == CSA2_OUT_FP8) {
+    if (!a->out_scale) return fail(CSA2_ERR_NULL, "%s: e4m3 output needs out_scale", who);
+    if (a->N & 127) return fail(CSA2_ERR_SHAPE, "%s: e4m3 output needs N=%d to be a multiple of 128", who, a->N);
+    if (a->ld_out_scale < a->N / 128) return fail(CSA2_ERR_SHAPE, "%s: ld_out_scale < N / 128", who);
+    if (a->ld_out & 15) return fail(CSA2_ERR_ALIGN, "%s: e4m3 output needs ld_out to be a multiple of 16", who);
+  }
+  if (a->rope_head) {
+    if (!a->row_pos) return fail(CSA2_ERR_NULL, "%s: rope_head needs row_pos", who);
+    if (a->rope_head < 128 || (a->rope_head & 127) || a->N % a->rope_head)
+      return fail(CSA2_ERR_SHAPE, "%s: rope_head=%d must be a multiple of 128 that divides N=%d", who,
+                  a->rope_head, a->N);
+    if (!(a->rope_theta >= 0.f) || !isfinite(a->rope_theta))
+      return fail(CSA2_ERR_SHAPE, "%s: rope_theta must be finite and >= 0", who);
+  }
+  if (a->w_ready != 0 && a->w_ready != 1) return fail(CSA2_ERR_SHAPE, "%s: w_ready=%d must be 0 or 1", who, a->w_ready);
+  return CSA2_OK;
+}
+
+int lora_check(const csa2_lora_linear_args* a, const char* who) {
+  int rc = linear_check(&a->base, who);
+  if (rc) return rc;
+  if (!a->row_adapter || !a->a || !a->b) return fail(CSA2_ERR_NULL, "%s: row_adapter/a/b is NULL", who);
+  if (a->base.T > csa2::kLoraMaxRows) return fail(CSA2_ERR_SHAPE, "%s: T=%d is above 2^20", who, a->base.T);
+  if (a->rank < 8 || a->rank > 128 || (a->rank & 7))
+    return fail(CSA2_ERR_SHAPE, "%s: rank=%d must be a multiple of 8 in 8..128", who, a->rank);
+  if (a->n_adapters < 1 || static_cast<long long>(a->n_adapters) * a->base.N > (1 << 30))
+    return fail(CSA2_ERR_SHAPE, "%s: n_adapters=%d must be >= 1, and n_adapters * N at most 2^30", who, a->n_adapters);
+  if (!aligned16(a->a) || !aligned16(a->b)) return fail(CSA2_ERR_ALIGN, "%s: a and b must be 16-B aligned", who);
+  if (!aligned4(a->row_adapter) || !aligned4(a->adapter_scale))
+    return fail(CSA2_ERR_ALIGN, "%s: row_adapter and adapter_scale must be 4-B aligned", who);
+  return CSA2_OK;
 }
 
 }  // namespace
@@ -543,46 +614,103 @@ int csa2_quant_fp8(const csa2_quant_fp8_args* a, void* stream) {
 
 int csa2_fp8_linear(const csa2_fp8_linear_args* a, void* stream) {
   if (!a) return fail(CSA2_ERR_NULL, "csa2_fp8_linear: args is NULL");
-  if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->out)
-    return fail(CSA2_ERR_NULL, "csa2_fp8_linear: x/x_scale/w/w_scale/out is NULL");
-  if (a->T < 1 || a->N < 1) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: T=%d and N=%d must be >= 1", a->T, a->N);
-  if (a->K < 16 || a->K > 65536 || (a->K & 15))
-    return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: K=%d must be a multiple of 16 in 16..65536", a->K);
-  if (a->N > (1 << 28)) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: N=%d is above 2^28", a->N);
-  // a tile's last row is counted in 31 bits
-  if (a->T > (1 << 30)) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: T=%d is above 2^30", a->T);
-  const int nb = (a->K + 127) / 128;
-  if (a->ld_x < a->K || a->ld_w < a->K || a->ld_out < a->N || a->ld_x_scale < nb || a->ld_w_scale < nb)
-    return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: a row stride is smaller than its row");
-  if (a->ld_x >= (1LL << 39) || a->ld_w >= (1LL << 39))
-    return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: ld_x and ld_w must be below 2^39");
-  if (a->out_format != CSA2_OUT_F32 && a->out_format != CSA2_OUT_BF16 && a->out_format != CSA2_OUT_FP8)
-    return fail(CSA2_ERR_UNSUPPORTED, "csa2_fp8_linear: out_format=%d is not fp32 (0), bf16 (1) or e4m3 (2)", a->out_format);
-  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->out) || (a->ld_x & 15) || (a->ld_w & 15))
-    return fail(CSA2_ERR_ALIGN, "csa2_fp8_linear: x, w, out must be 16-B aligned, ld_x and ld_w multiples of 16");
-  if (!aligned4(a->x_scale) || !aligned4(a->w_scale) || !aligned4(a->row_pos) || !aligned4(a->out_scale))
-    return fail(CSA2_ERR_ALIGN, "csa2_fp8_linear: scales and row_pos must be 4-B aligned");
-  if (a->out_format == CSA2_OUT_FP8) {
-    if (!a->out_scale) return fail(CSA2_ERR_NULL, "csa2_fp8_linear: e4m3 output needs out_scale");
-    if (a->N & 127) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: e4m3 output needs N=%d to be a multiple of 128", a->N);
-    if (a->ld_out_scale < a->N / 128) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: ld_out_scale < N / 128");
-    if (a->ld_out & 15) return fail(CSA2_ERR_ALIGN, "csa2_fp8_linear: e4m3 output needs ld_out to be a multiple of 16");
-  }
-  if (a->rope_head) {
-    if (!a->row_pos) return fail(CSA2_ERR_NULL, "csa2_fp8_linear: rope_head needs row_pos");
-    if (a->rope_head < 128 || (a->rope_head & 127) || a->N % a->rope_head)
-      return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: rope_head=%d must be a multiple of 128 that divides N=%d",
-                  a->rope_head, a->N);
-    if (!(a->rope_theta >= 0.f) || !isfinite(a->rope_theta))
-      return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: rope_theta must be finite and >= 0");
-  }
-  if (a->w_ready != 0 && a->w_ready != 1) return fail(CSA2_ERR_SHAPE, "csa2_fp8_linear: w_ready=%d must be 0 or 1", a->w_ready);
+  int rc = linear_check(a, "csa2_fp8_linear");
+  if (rc) return rc;
   DeviceCtx ctx;
   cudaError_t e = csa2::device_ctx(&ctx);
   if (e != cudaSuccess) return cuda_fail(e, "csa2_fp8_linear: device");
   const char* why = "csa2_fp8_linear: launch";
   e = csa2::launch_fp8_linear(*a, ctx, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return cuda_fail(e, why);
+  return CSA2_OK;
+}
+
+int csa2_add_norm_fp8(const csa2_add_norm_fp8_args* a, void* stream) {
+  if (!a) return fail(CSA2_ERR_NULL, "csa2_add_norm_fp8: args is NULL");
+  if (!a->x || !a->residual || !a->residual_out || !a->gamma)
+    return fail(CSA2_ERR_NULL, "csa2_add_norm_fp8: x/residual/residual_out/gamma is NULL");
+  if (!a->codes && !a->y) return fail(CSA2_ERR_NULL, "csa2_add_norm_fp8: one of codes, y is required");
+  if (!a->codes != !a->scale) return fail(CSA2_ERR_NULL, "csa2_add_norm_fp8: codes and scale go together");
+  if (a->T < 1) return fail(CSA2_ERR_SHAPE, "csa2_add_norm_fp8: T must be >= 1");
+  if (a->K < 16 || a->K > 16384 || (a->K & 15))
+    return fail(CSA2_ERR_SHAPE, "csa2_add_norm_fp8: K=%d must be a multiple of 16 in 16..16384", a->K);
+  if (a->residual_f32 != 0 && a->residual_f32 != 1)
+    return fail(CSA2_ERR_UNSUPPORTED, "csa2_add_norm_fp8: residual_f32=%d must be 0 or 1", a->residual_f32);
+  if (!(a->eps >= 0.f) || !isfinite(a->eps)) return fail(CSA2_ERR_SHAPE, "csa2_add_norm_fp8: eps must be finite and >= 0");
+  const int nb = (a->K + 127) / 128, size = a->residual_f32 ? 4 : 2;
+  if (a->ld_x < a->K || a->ld_residual < a->K || a->ld_residual_out < a->K || (a->codes && (a->ld_codes < a->K || a->ld_scale < nb)) ||
+      (a->y && a->ld_y < a->K))
+    return fail(CSA2_ERR_SHAPE, "csa2_add_norm_fp8: a row stride is smaller than its row");
+  constexpr int64_t kMost = 1LL << 29;  // T rows of bytes stay inside 63 bits
+  if (a->ld_x >= kMost || a->ld_residual >= kMost || a->ld_residual_out >= kMost || (a->codes && (a->ld_codes >= kMost || a->ld_scale >= kMost)) ||
+      (a->y && a->ld_y >= kMost))
+    return fail(CSA2_ERR_SHAPE, "csa2_add_norm_fp8: row strides must be below 2^29");
+  if (!aligned16(a->x) || !aligned16(a->residual) || !aligned16(a->residual_out) || !aligned16(a->codes) || !aligned16(a->y) ||
+      !aligned16(a->gamma) || (a->ld_x & 7) || (a->ld_residual & (16 / size - 1)) || (a->ld_residual_out & (16 / size - 1)) ||
+      (a->codes && (a->ld_codes & 15)) || (a->y && (a->ld_y & 7)))
+    return fail(CSA2_ERR_ALIGN, "csa2_add_norm_fp8: x, residual, residual_out, codes, y, gamma and their row strides must be 16-B aligned");
+  if (!aligned4(a->scale)) return fail(CSA2_ERR_ALIGN, "csa2_add_norm_fp8: scale must be 4-B aligned");
+  const long long T = a->T, K = a->K;
+  const ByteRows in[] = {{a->residual, K * size, T, a->ld_residual * size}, {a->x, K * 2, T, a->ld_x * 2}, {a->gamma, K * 4, 1, K * 4}};
+  const ByteRows out[] = {{a->residual_out, K * size, T, a->ld_residual_out * size}, {a->codes, K, T, a->ld_codes},
+                          {a->scale, nb * 4LL, T, a->ld_scale * 4}, {a->y, K * 2, T, a->ld_y * 2}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      const bool in_place = o == 0 && i == 0 && a->residual_out == a->residual && a->ld_residual_out == a->ld_residual;
+      if (!in_place && out[o].meets(in[i])) return fail(CSA2_ERR_UNSUPPORTED, "csa2_add_norm_fp8: an output overlaps an input");
+    }
+    for (int i = 0; i < o; ++i)
+      if (out[o].meets(out[i])) return fail(CSA2_ERR_UNSUPPORTED, "csa2_add_norm_fp8: two outputs overlap");
+  }
+  cudaError_t e = csa2::launch_add_norm_fp8(*a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_add_norm_fp8: launch");
+  return CSA2_OK;
+}
+
+int csa2_lora_linear(const csa2_lora_linear_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a) return fail(CSA2_ERR_NULL, "csa2_lora_linear: args is NULL");
+  int rc = lora_check(a, "csa2_lora_linear");
+  if (rc) return rc;
+  if (!ws) return fail(CSA2_ERR_WORKSPACE, "csa2_lora_linear: workspace is NULL");
+  if (!aligned16(ws)) return fail(CSA2_ERR_ALIGN, "csa2_lora_linear: workspace must be 16-B aligned");
+  const size_t need = csa2::lora_workspace_bytes(a->base.T, a->rank);
+  if (ws_bytes < need) return fail(CSA2_ERR_WORKSPACE, "csa2_lora_linear: workspace of %zu bytes, %zu needed", ws_bytes, need);
+  DeviceCtx ctx;
+  cudaError_t e = csa2::device_ctx(&ctx);
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_lora_linear: device");
+  const char* why = "csa2_lora_linear: launch";
+  e = csa2::launch_lora_linear(*a, ws, ctx, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return cuda_fail(e, why);
+  return CSA2_OK;
+}
+
+int csa2_logprobs(const csa2_logprobs_args* a, void* stream) {
+  if (!a) return fail(CSA2_ERR_NULL, "csa2_logprobs: args is NULL");
+  if (!a->logits) return fail(CSA2_ERR_NULL, "csa2_logprobs: logits is NULL");
+  if (!a->logprob && !a->entropy && !a->lse && !a->top_id && !a->top_logprob)
+    return fail(CSA2_ERR_NULL, "csa2_logprobs: no output is given");
+  if (!a->logprob != !a->token) return fail(CSA2_ERR_NULL, "csa2_logprobs: logprob and token go together");
+  if (a->T < 1 || a->T > (1 << 27)) return fail(CSA2_ERR_SHAPE, "csa2_logprobs: T=%d not in 1..2^27", a->T);
+  if (a->V < 1 || a->V > (1 << 30)) return fail(CSA2_ERR_SHAPE, "csa2_logprobs: V=%d not in 1..2^30", a->V);
+  if (a->logits_f32 != 0 && a->logits_f32 != 1)
+    return fail(CSA2_ERR_UNSUPPORTED, "csa2_logprobs: logits_f32=%d must be 0 or 1", a->logits_f32);
+  if (a->n_top < 0 || a->n_top > 32) return fail(CSA2_ERR_SHAPE, "csa2_logprobs: n_top=%d not in 0..32", a->n_top);
+  if ((a->n_top > 0) != (a->top_id || a->top_logprob))
+    return fail(CSA2_ERR_NULL, "csa2_logprobs: n_top goes with top_id or top_logprob");
+  if (a->ld_logits < a->V || (a->n_top && a->ld_top < a->n_top))
+    return fail(CSA2_ERR_SHAPE, "csa2_logprobs: a row stride is smaller than its row");
+  if (a->ld_logits >= (1LL << 32) || a->ld_top >= (1LL << 32))
+    return fail(CSA2_ERR_SHAPE, "csa2_logprobs: row strides must be below 2^32");
+  if ((reinterpret_cast<uintptr_t>(a->logits) & (a->logits_f32 ? 3u : 1u)))
+    return fail(CSA2_ERR_ALIGN, "csa2_logprobs: logits must be aligned to their own size");
+  if (!aligned4(a->token) || !aligned4(a->logprob) || !aligned4(a->entropy) || !aligned4(a->lse) || !aligned4(a->top_id) ||
+      !aligned4(a->top_logprob))
+    return fail(CSA2_ERR_ALIGN, "csa2_logprobs: token and outputs must be 4-B aligned");
+  DeviceCtx ctx;
+  cudaError_t e = csa2::device_ctx(&ctx);
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_logprobs: device");
+  e = csa2::launch_logprobs(*a, ctx, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_logprobs: launch");
   return CSA2_OK;
 }
 
@@ -659,6 +787,13 @@ int csa2_workspace_size(int which, const void* args, size_t* bytes) {
       cudaError_t e = csa2::device_ctx(&ctx);
       if (e != cudaSuccess) return cuda_fail(e, "csa2_workspace_size: device");
       *bytes = csa2::attn_workspace_bytes(a->T, a->n_swa + a->k, ctx.num_sms);
+      return CSA2_OK;
+    }
+    case CSA2_CALL_LORA_LINEAR: {
+      const csa2_lora_linear_args* a = static_cast<const csa2_lora_linear_args*>(args);
+      int rc = lora_check(a, "csa2_workspace_size");
+      if (rc) return rc;
+      *bytes = csa2::lora_workspace_bytes(a->base.T, a->rank);
       return CSA2_OK;
     }
     default:

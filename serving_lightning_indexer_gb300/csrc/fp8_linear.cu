@@ -8,6 +8,11 @@
 // many rows, bound by that chain (2.2 PFLOP/s at 4,096 x 2,048 x 32,768), and one for
 // few rows, bound by the weights' bytes (8 x 2,048 x 32,768: 12.7 us, 5.3 TB/s) or, where
 // they are few, by latency (8 x 7,168 x 512: 4.6 us).
+//
+// LORA: each adapter that a tile's rows use (lora.cu lists them) brings up to two more
+// blocks for every 64 ranks, bf16 products of the rows' inner products with the
+// adapter's b, summed like the others but only to the rows that have the adapter.  The
+// projection's own blocks come first, and only what lora.cu wrote waits for it.
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -38,6 +43,38 @@ struct LinearParams {
   int w_ready;
   uint32_t* err;
   uint64_t turn[32];  // RoPE turn rates of the 32 pairs
+};
+
+// What LORA adds to a launch: nothing without it.
+template <bool LORA>
+struct LoraParams {};
+template <>
+struct LoraParams<true> {
+  CUtensorMap map_v, map_b;  // inner products [2 T, rank], b [adapters N, rank]: 64 ranks by a tile's rows or columns
+  const int* row_adapter;
+  const int* lists;
+  int list_stride;
+  int pieces;  // blocks of an adapter: 64 ranks each, times planes of v
+  int planes;
+};
+// What a launch has to know of its adapters on the host.
+struct NoLora {
+  static constexpr bool kOn = false;
+};
+struct WithLora {
+  static constexpr bool kOn = true;
+  const csa2_lora_linear_args* args;
+  void* workspace;
+};
+// Block i of a tile's adapters: the adapter, and where its ranks and its plane of v start.
+struct LoraBlock {
+  int adapter, rank_byte, v_row;
+  __device__ __forceinline__ LoraBlock(const LoraParams<true>& lo, const int* list, int i, int T) {
+    const int j = i / lo.pieces, k = i - j * lo.pieces;
+    adapter = list[4 + j];
+    rank_byte = k / lo.planes * 128;
+    v_row = k % lo.planes * T;
+  }
 };
 
 // ---------------------------------------------------------------- many rows
@@ -131,14 +168,17 @@ struct Share {
       step = gridDim.x;
     }
   }
+  // The adapters' blocks of a shared tile are the second CTA's, which has the fewer others.
+  __device__ __forceinline__ bool adapters_too() const { return !SPLIT || (blockIdx.x & 1); }
   __device__ __forceinline__ int row(long long tile) const { return static_cast<int>(tile % m_tiles) * kTileM; }
   __device__ __forceinline__ int column(long long tile) const { return static_cast<int>(tile / m_tiles) * BN; }
 };
 
 // The accumulation warps' part: sums each tile in registers and writes it.
 // False when a wait gave up (the same in a warp's lanes).
-template <int BN, int OUT, bool SPLIT>
-__device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out, const LinearParams& p, uint8_t* smem,
+template <int BN, int OUT, bool SPLIT, bool LORA>
+__device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out, const LinearParams& p,
+                                                     const LoraParams<LORA>& lo, uint8_t* smem,
                                                      uint32_t tmem, uint64_t* tfull, uint64_t* tempty, uint64_t* empty,
                                                      uint64_t* sfull, uint64_t* sempty, volatile int* s_abort) {
   using Cfg = WideCfg<BN>;
@@ -193,6 +233,38 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
         }
       }
       if ((b & 3) == 3 || b + 1 == blocks) ++g;
+    }
+    if constexpr (LORA) {
+      if (tile == mine.first) {
+        pdl_wait();
+        pdl_trigger();  // every CTA holds its TMEM
+      }
+      const int* list = lo.lists + static_cast<long long>(t0 / kTileM) * lo.list_stride;
+      const int extra = mine.adapters_too() ? list[0] * lo.pieces : 0;
+      const int own = extra > 0 && row < p.T ? __ldg(lo.row_adapter + row) : -1;
+#pragma unroll 1
+      for (int i = 0; i < extra; ++i, ++it) {
+        const bool add = LoraBlock(lo, list, i, p.T).adapter == own;
+        if (!__all_sync(0xffffffffu, wait(&tfull[it % NA], (it / NA) & 1, s_abort))) return false;
+        tc_fence_after();
+        if (warp == 0 && lane == 0) mbar_arrive(&empty[it % S]);
+        const uint32_t ta = taddr + (it % NA) * BN;
+#pragma unroll
+        for (int c = 0; c < C / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld32x16_async(ta + c * 16, v);
+          tmem_wait_ld16(v);
+          if (c + 1 == C / 16) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[it % NA]);
+          }
+          if (add) {  // another row's products are left alone, whatever they are
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[c * 16 + k] += __uint_as_float(v[k]);
+          }
+        }
+      }
     }
     if (SPLIT) {
       // Rank 0 finishes the left half of the columns, rank 1 the right one: the
@@ -277,10 +349,11 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
   return true;
 }
 
-template <int BN, int OUT, bool SPLIT>
+template <int BN, int OUT, bool SPLIT, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_linear_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                           const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p) {
+                           const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p,
+                           const __grid_constant__ LoraParams<LORA> lo) {
   using Cfg = WideCfg<BN>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAccs, C = Cfg::kCols, SS = Cfg::kScaleSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -320,8 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
-  pdl_trigger();  // every CTA holds its TMEM
+  if constexpr (!LORA) {  // else the previous launch is lora.cu's, behind the launch that wrote x
+    pdl_wait();
+    pdl_trigger();  // every CTA holds its TMEM
+  }
   const uint32_t tmem = *s_tmem;
   const Share<BN, SPLIT> mine(p);
   const int blocks = mine.blocks;
@@ -341,6 +416,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
           tma_load_2d(dst, &map_x, (mine.b0 + b) * kBlockK, t0, &full[s], keep);
           tma_load_2d(dst + kTileM * kBlockK, &map_w, (mine.b0 + b) * kBlockK, n0, &full[s], keep);
+        }
+        if constexpr (LORA) {
+          if (!ok) break;
+          if (tile == mine.first) pdl_wait();
+          const int* list = lo.lists + static_cast<long long>(t0 / kTileM) * lo.list_stride;
+          const int extra = mine.adapters_too() ? list[0] * lo.pieces : 0;
+          for (int i = 0; i < extra; ++i, ++it) {
+            const LoraBlock at(lo, list, i, p.T);
+            const int s = static_cast<int>(it % S);
+            if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
+            uint8_t* dst = smem + s * Cfg::kStageBytes;
+            mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+            tma_load_2d(dst, &lo.map_v, at.rank_byte, at.v_row + t0, &full[s], keep);
+            tma_load_2d(dst + kTileM * kBlockK, &lo.map_b, at.rank_byte, at.adapter * p.N + n0, &full[s], keep);
+          }
         }
       }
       if (!ok) {
@@ -364,7 +454,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d = tmem + a * BN;
       uint32_t s = a, phase = 0, a_phase = 1;
       bool ok = true;
-      for (long long i = a; i < all; i += NA) {
+      if constexpr (LORA) {
+        constexpr uint32_t idesc_b = idesc_bf16_f32(kTileM, BN, 0, 0);
+        long long it = 0;
+        // the products of the tile's next n blocks, those that are this accumulator's
+        auto issue = [&](int n, bool adapters) {
+          for (int b = 0; b < n && ok; ++b) {
+            const long long i = it++;
+            if (i % NA != a) continue;
+            s = static_cast<uint32_t>(i % S);
+            if (!(ok = wait(&full[s], static_cast<uint32_t>(i / S) & 1u, s_abort))) break;
+            if (!(ok = wait(&tempty[a], a_phase, s_abort))) break;
+            tc_fence_after();
+            const uint64_t ad = x_desc + s * kStageDesc, bd = w_desc + s * kStageDesc;
+            if (!adapters) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_e4m3(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) umma_bf16(d, ad + 2 * k, bd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
+            }
+            mma_commit(&tfull[a]);
+            a_phase ^= 1;
+          }
+        };
+        for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
+          issue(blocks, false);
+          if (tile == mine.first) pdl_wait();
+          const int* list = lo.lists + static_cast<long long>(mine.row(tile) / kTileM) * lo.list_stride;
+          if (mine.adapters_too()) issue(list[0] * lo.pieces, true);
+        }
+      }
+      for (long long i = LORA ? all : a; i < all; i += NA) {
         if (!(ok = wait(&full[s], phase, s_abort))) break;
         const uint64_t ad = x_desc + s * kStageDesc, bd = w_desc + s * kStageDesc;
         if (!(ok = wait(&tempty[a], a_phase, s_abort))) break;
@@ -428,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       set_error(p.err, kErrTimeout);
     }
   } else {
-    if (!accumulate_and_store<BN, OUT, SPLIT>(map_out, p, smem, tmem, tfull, tempty, empty, sfull, sempty, s_abort)) {
+    if (!accumulate_and_store<BN, OUT, SPLIT, LORA>(map_out, p, lo, smem, tmem, tfull, tempty, empty, sfull, sempty,
+                                                    s_abort)) {
       *s_abort = 1;
       set_error(p.err, kErrTimeout);
       if (lane == 0) bulk_wait_all();  // the last tile's output still leaves shared memory
@@ -457,9 +579,32 @@ long long wide_tiles(const csa2_fp8_linear_args& a) {
   return ((static_cast<long long>(a.T) + kTileM - 1) / kTileM) * ((static_cast<long long>(a.N) + BN - 1) / BN);
 }
 
-template <int BN, int OUT, bool SPLIT>
-cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, const DeviceCtx& ctx, cudaStream_t st,
-                        const char** why) {
+// With adapters: their inner products and lists are launched first, for tiles of
+// `rows` rows and `columns` columns, and described to the projection.  Nothing without.
+cudaError_t prepare_lora(const NoLora&, LoraParams<false>*, int, int, const DeviceCtx&, cudaStream_t, const char**) {
+  return cudaSuccess;
+}
+cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int columns, const DeviceCtx& ctx, cudaStream_t st,
+                         const char** why) {
+  const csa2_lora_linear_args& a = *l.args;
+  const LoraInner to = lora_inner_at(a, l.workspace, rows);
+  lo->row_adapter = a.row_adapter;
+  lo->lists = to.lists;
+  lo->list_stride = rows + 4;
+  lo->planes = a.base.out_format == CSA2_OUT_BF16 ? 1 : 2;
+  lo->pieces = (a.rank + 63) / 64 * lo->planes;
+  const uint64_t row = 2 * static_cast<uint64_t>(a.rank);
+  if (encode_tmap_2d_u8(&lo->map_v, to.v, row, 2 * static_cast<uint64_t>(a.base.T), row, 128, rows) != CUDA_SUCCESS ||
+      encode_tmap_2d_u8(&lo->map_b, a.b, row, static_cast<uint64_t>(a.n_adapters) * a.base.N, row, 128, columns) != CUDA_SUCCESS) {
+    *why = "csa2_lora_linear: a tensor map could not be encoded";
+    return cudaErrorInvalidValue;
+  }
+  return launch_lora_inner(a, to, ctx, st);
+}
+
+template <int BN, int OUT, bool SPLIT, class L>
+cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, const L& lora, const DeviceCtx& ctx,
+                        cudaStream_t st, const char** why) {
   CUtensorMap map_x, map_w, map_out = {};
   if (encode_tmap_2d_u8(&map_x, a.x, a.K, a.T, a.ld_x, kBlockK, kTileM) != CUDA_SUCCESS ||
       encode_tmap_2d_u8(&map_w, a.w, a.K, a.N, a.ld_w, kBlockK, BN) != CUDA_SUCCESS ||
@@ -468,8 +613,11 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
     *why = "csa2_fp8_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
   }
-  auto kern = fp8_linear_wide_kernel<BN, OUT, SPLIT>;
-  cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT, SPLIT>>(ctx.device, WideCfg<BN>::kSmem);
+  auto kern = fp8_linear_wide_kernel<BN, OUT, SPLIT, L::kOn>;
+  cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT, SPLIT, L::kOn>>(ctx.device, WideCfg<BN>::kSmem);
+  if (e != cudaSuccess) return e;
+  LoraParams<L::kOn> lo;
+  e = prepare_lora(lora, &lo, kTileM, BN, ctx, st, why);
   if (e != cudaSuccess) return e;
   const long long tiles = wide_tiles<BN>(a);
   cudaLaunchConfig_t cfg = {};
@@ -486,7 +634,7 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, map_out, p);
+  return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, map_out, p, lo);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -499,7 +647,10 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
 constexpr int kNarrowThreads = 320;
 constexpr int kScaleSeg = 16;  // blocks whose scales are staged at a time (even)
 
-template <int NT>
+// Of n blocks, those that a cluster's CTA `rank` takes: rank, rank + splits, ..
+__device__ __forceinline__ int shares_of(int n, int rank, int splits) { return n > rank ? (n - rank - 1) / splits + 1 : 0; }
+
+template <int NT, bool LORA>
 struct NarrowCfg {
   static constexpr int kStages = 4;
   static constexpr int kStageBytes = (128 + NT) * kBlockK;
@@ -507,15 +658,15 @@ struct NarrowCfg {
   static constexpr int kCols = kAccs * NT < 32 ? 32 : kAccs * NT;
   static constexpr int kOffScales = kStages * kStageBytes;  // the parts [NT][128] reuse the stages
   static constexpr int kOffBars = kOffScales + kScaleSeg * NT * 4;
-  static constexpr int kSmem = 1024 + kOffBars + 256;
+  static constexpr int kSmem = 1024 + kOffBars + 256 + (LORA ? NT * 4 : 0);
   static_assert(NT * 128 * 4 <= kOffScales, "the parts fit the stages");
 };
 
-template <int NT, int OUT>
+template <int NT, int OUT, bool LORA>
 __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     fp8_linear_narrow_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                             const __grid_constant__ LinearParams p) {
-  using Cfg = NarrowCfg<NT>;
+                             const __grid_constant__ LinearParams p, const __grid_constant__ LoraParams<LORA> lo) {
+  using Cfg = NarrowCfg<NT, LORA>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -545,7 +696,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     fence_mbar_init();
     prefetch_tmap(&map_x);
     prefetch_tmap(&map_w);
-    if (p.w_ready) {  // the first weights do not wait for the previous launch
+    if (LORA || p.w_ready) {  // the first weights do not wait for the previous launch
       for (int b = 0; b < min(S, blocks); ++b) {
         mbar_arrive_expect_tx(&full[b], Cfg::kStageBytes);
         tma_load_2d(smem + b * Cfg::kStageBytes, &map_w, (b0 + b) * kBlockK, n0, &full[b], pol_w);
@@ -559,8 +710,10 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
-  pdl_trigger();  // every CTA holds its TMEM
+  if constexpr (!LORA) {  // else the previous launch is lora.cu's, behind the launch that wrote x
+    pdl_wait();
+    pdl_trigger();  // every CTA holds its TMEM
+  }
   const uint32_t tmem = *s_tmem;
 
   bool ok = true;
@@ -572,11 +725,24 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
         const int s = b % S;
         if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
         uint8_t* dst = smem + s * Cfg::kStageBytes;
-        if (b >= S || !p.w_ready) {
+        if (b >= S || !(LORA || p.w_ready)) {
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
           tma_load_2d(dst, &map_w, (b0 + b) * kBlockK, n0, &full[s], pol_w);
         }
         tma_load_2d(dst + 128 * kBlockK, &map_x, (b0 + b) * kBlockK, t0, &full[s], pol_x);
+      }
+      if constexpr (LORA) {
+        if (ok) pdl_wait();
+        const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
+        for (int i = rank; ok && i < list[0] * lo.pieces; i += splits, ++b) {
+          const LoraBlock at(lo, list, i, p.T);
+          const int s = b % S;
+          if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
+          uint8_t* dst = smem + s * Cfg::kStageBytes;
+          mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+          tma_load_2d(dst, &lo.map_b, at.rank_byte, at.adapter * p.N + n0, &full[s], pol_x);
+          tma_load_2d(dst + 128 * kBlockK, &lo.map_v, at.rank_byte, at.v_row + t0, &full[s], pol_x);
+        }
       }
       if (!ok) {
         *s_abort = 1;
@@ -588,18 +754,34 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(128, NT);
+      constexpr uint32_t idesc = idesc_e4m3_f32(128, NT), idesc_b = idesc_bf16_f32(128, NT, 0, 0);
       int b = 0;
-      for (; b < blocks; ++b) {
-        const int s = b % S, a = b % NA;
-        if (!(ok = mbar_wait(&full[s], static_cast<uint32_t>(b / S) & 1u, s_abort))) break;
-        if (b >= NA && !(ok = mbar_wait(&tempty[a], static_cast<uint32_t>(b / NA - 1) & 1u, s_abort))) break;
-        tc_fence_after();
-        const uint64_t wd = smem_desc_sw128(smem + s * Cfg::kStageBytes);
-        const uint64_t xd = smem_desc_sw128(smem + s * Cfg::kStageBytes + 128 * kBlockK);
+      int end = blocks;
+      for (bool adapters = false;; adapters = true) {
+        for (; b < end; ++b) {
+          const int s = b % S, a = b % NA;
+          if (!(ok = mbar_wait(&full[s], static_cast<uint32_t>(b / S) & 1u, s_abort))) break;
+          if (b >= NA && !(ok = mbar_wait(&tempty[a], static_cast<uint32_t>(b / NA - 1) & 1u, s_abort))) break;
+          tc_fence_after();
+          const uint64_t wd = smem_desc_sw128(smem + s * Cfg::kStageBytes);
+          const uint64_t xd = smem_desc_sw128(smem + s * Cfg::kStageBytes + 128 * kBlockK);
+          if (!LORA || !adapters) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_e4m3(tmem + a * NT, wd + 2 * k, xd + 2 * k, idesc, k > 0 ? 1u : 0u);
-        mma_commit(&tfull[a]);
+            for (int k = 0; k < 4; ++k) mma_e4m3(tmem + a * NT, wd + 2 * k, xd + 2 * k, idesc, k > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(tmem + a * NT, wd + 2 * k, xd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&tfull[a]);
+        }
+        if constexpr (LORA) {
+          if (ok && !adapters) {
+            pdl_wait();
+            end = blocks + shares_of(lo.lists[static_cast<long long>(blockIdx.y) * lo.list_stride] * lo.pieces, rank, splits);
+            continue;
+          }
+        }
+        break;
       }
       if (!ok) {
         *s_abort = 1;
@@ -616,6 +798,10 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     float* s_scale = reinterpret_cast<float*>(smem + Cfg::kOffScales);  // [block][NT]: both scales
     const float* ws = p.w_scale + static_cast<long long>(n0 >> 7) * p.ld_ws + b0;
     const int tid = threadIdx.x - 64;
+    int* s_adapter = reinterpret_cast<int*>(smem + Cfg::kOffBars + 256);  // [NT], LORA only
+    if constexpr (LORA) {
+      if (tid < NT) s_adapter[tid] = t0 + tid < p.T ? __ldg(lo.row_adapter + t0 + tid) : -1;
+    }
     uint64_t acc[NT / 2];
 #pragma unroll
     for (int i = 0; i < NT / 2; ++i) acc[i] = 0;
@@ -651,6 +837,38 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
             uint64_t* s2 = acc + c * 8 + i * 2;
             s2[0] = fma_f32x2(pack_f32x2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), m.x, s2[0]);
             s2[1] = fma_f32x2(pack_f32x2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), m.y, s2[1]);
+          }
+        }
+      }
+    }
+    if constexpr (LORA) {
+      pdl_wait();
+      pdl_trigger();  // every CTA holds its TMEM
+      const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
+      const int extra = shares_of(list[0] * lo.pieces, rank, splits);
+      for (int i = (blocks + group) & 1; i < extra && ok; i += 2) {  // the block's parity is the group, as above
+        const int b = blocks + i, a = b % NA;
+        const int adapter = LoraBlock(lo, list, rank + i * splits, p.T).adapter;
+        ok = __all_sync(0xffffffffu, mbar_wait(&tfull[a], static_cast<uint32_t>(b / NA) & 1u, s_abort));
+        if (!ok) break;
+        tc_fence_after();
+        if (quad == 0 && lane == 0) mbar_arrive(&empty[b % S]);
+#pragma unroll
+        for (int c = 0; c < NT / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld32x16_async(taddr + a * NT + c * 16, v);
+          tmem_wait_ld16(v);
+          if (c + 1 == NT / 16) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[a]);
+          }
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {  // another row's products are left alone, whatever they are
+            float2 f = unpack_f32x2(acc[c * 8 + k / 2]);
+            if (s_adapter[c * 16 + k] == adapter) f.x += __uint_as_float(v[k]);
+            if (s_adapter[c * 16 + k + 1] == adapter) f.y += __uint_as_float(v[k + 1]);
+            acc[c * 8 + k / 2] = pack_f32x2(f.x, f.y);
           }
         }
       }
@@ -759,9 +977,9 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
 // Clusters of `splits` CTAs that run at once on the device, by the runtime's count (an
 // SM holds one CTA of NT = 64, by its registers, and two of the others), which is asked
 // for once a device, kernel and size.
-template <int NT, int OUT>
+template <int NT, int OUT, bool LORA>
 int narrow_clusters(const cudaLaunchConfig_t& cfg, int splits, int device) {
-  constexpr auto kern = fp8_linear_narrow_kernel<NT, OUT>;
+  constexpr auto kern = fp8_linear_narrow_kernel<NT, OUT, LORA>;
   static std::atomic<int> known[64][5];
   int i = 0;
   while ((1 << i) < splits) ++i;
@@ -796,19 +1014,20 @@ long long wide_time(const csa2_fp8_linear_args& a, const DeviceCtx& ctx) {
 // once; with more it has to run at once (one CTA an SM, by its registers) and be the quicker by
 // wide_time's measure, a CTA's blocks and 7 (K = 7168, N = 512: 12.3 us here, 20 us
 // there for 512 rows, 32 and 20 us for 2,048).
-template <int NT, int OUT>
-cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, const DeviceCtx& ctx, cudaStream_t st,
-                          const char** why, bool* taken) {
-  auto kern = fp8_linear_narrow_kernel<NT, OUT>;
+template <int NT, int OUT, class L>
+cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, const L& lora, const DeviceCtx& ctx,
+                          cudaStream_t st, const char** why, bool* taken) {
+  constexpr int kSmem = NarrowCfg<NT, L::kOn>::kSmem;
+  auto kern = fp8_linear_narrow_kernel<NT, OUT, L::kOn>;
   const long long n_tiles = (static_cast<long long>(a.N) + 127) / 128;
   const int t_tiles = (a.T + NT - 1) / NT, blocks = (a.K + 127) / 128;
   *taken = NT < 64 || n_tiles * t_tiles <= ctx.num_sms;
   if (!*taken) return cudaSuccess;
-  cudaError_t e = prefer_max_smem_once<fp8_linear_narrow_kernel<NT, OUT>>(ctx.device, NarrowCfg<NT>::kSmem);
+  cudaError_t e = prefer_max_smem_once<fp8_linear_narrow_kernel<NT, OUT, L::kOn>>(ctx.device, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kNarrowThreads);
-  cfg.dynamicSmemBytes = NarrowCfg<NT>::kSmem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -828,7 +1047,7 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
     cfg.gridDim = dim3(static_cast<unsigned>(n_tiles), t_tiles, splits);
     attr[1].val.clusterDim.z = splits;
     if (2 * splits <= blocks && (NT < 64 && splits <= 8 ? tiles * splits <= 2 * ctx.num_sms
-                                                        : tiles <= narrow_clusters<NT, OUT>(cfg, splits, ctx.device)))
+                                                        : tiles <= narrow_clusters<NT, OUT, L::kOn>(cfg, splits, ctx.device)))
       break;
   }
   *taken = NT < 64 || (blocks + splits - 1) / splits + 7 <= wide_time(a, ctx);
@@ -841,26 +1060,29 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
     *why = "csa2_fp8_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
   }
-  return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, p);
+  LoraParams<L::kOn> lo;
+  e = prepare_lora(lora, &lo, NT, 128, ctx, st, why);
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, p, lo);
 }
 
-template <int OUT>
-cudaError_t launch_out(const csa2_fp8_linear_args& a, const LinearParams& p, const DeviceCtx& ctx, cudaStream_t st,
-                       const char** why) {
+template <int OUT, class L>
+cudaError_t launch_out(const csa2_fp8_linear_args& a, const LinearParams& p, const L& lora, const DeviceCtx& ctx,
+                       cudaStream_t st, const char** why) {
   bool taken = false;
-  cudaError_t e = a.T <= 16   ? launch_narrow<16, OUT>(a, p, ctx, st, why, &taken)
-                  : a.T <= 32 ? launch_narrow<32, OUT>(a, p, ctx, st, why, &taken)
-                              : launch_narrow<64, OUT>(a, p, ctx, st, why, &taken);
+  cudaError_t e = a.T <= 16   ? launch_narrow<16, OUT>(a, p, lora, ctx, st, why, &taken)
+                  : a.T <= 32 ? launch_narrow<32, OUT>(a, p, lora, ctx, st, why, &taken)
+                              : launch_narrow<64, OUT>(a, p, lora, ctx, st, why, &taken);
   if (e != cudaSuccess || taken) return e;
   // Tiles for less than half the SMs share their blocks between two CTAs (4,096 x
   // 7,168 x 512: 28.9 -> 19.9 us).
-  return wide_splits(a, ctx) ? launch_wide<256, OUT, true>(a, p, ctx, st, why)
-                             : launch_wide<256, OUT, false>(a, p, ctx, st, why);
+  return wide_splits(a, ctx) ? launch_wide<256, OUT, true>(a, p, lora, ctx, st, why)
+                             : launch_wide<256, OUT, false>(a, p, lora, ctx, st, why);
 }
 
-}  // namespace
-
-cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ctx, cudaStream_t st, const char** why) {
+template <class L>
+cudaError_t launch_linear(const csa2_fp8_linear_args& a, const L& lora, const DeviceCtx& ctx, cudaStream_t st,
+                          const char** why) {
   LinearParams p;
   p.x_scale = a.x_scale;
   p.w_scale = a.w_scale;
@@ -892,10 +1114,20 @@ cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ct
     memcpy(p.turn, turn, sizeof(turn));
   }
   switch (a.out_format) {
-    case CSA2_OUT_F32: return launch_out<CSA2_OUT_F32>(a, p, ctx, st, why);
-    case CSA2_OUT_BF16: return launch_out<CSA2_OUT_BF16>(a, p, ctx, st, why);
-    default: return launch_out<CSA2_OUT_FP8>(a, p, ctx, st, why);
+    case CSA2_OUT_F32: return launch_out<CSA2_OUT_F32>(a, p, lora, ctx, st, why);
+    case CSA2_OUT_BF16: return launch_out<CSA2_OUT_BF16>(a, p, lora, ctx, st, why);
+    default: return launch_out<CSA2_OUT_FP8>(a, p, lora, ctx, st, why);
   }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ctx, cudaStream_t st, const char** why) {
+  return launch_linear(a, NoLora{}, ctx, st, why);
+}
+cudaError_t launch_lora_linear(const csa2_lora_linear_args& a, void* ws, const DeviceCtx& ctx, cudaStream_t st,
+                               const char** why) {
+  return launch_linear(a.base, WithLora{&a, ws}, ctx, st, why);
 }
 
 }  // namespace csa2

@@ -26,44 +26,6 @@ struct QuantParams {
   long long ld_scale;
 };
 
-// 16 consecutive bf16 values as fp32.
-__device__ __forceinline__ void unpack16(const uint4 (&v)[2], float (&y)[16]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[h * 8 + 2 * i] = __uint_as_float(w[i] << 16);
-      y[h * 8 + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-}
-// Largest finite magnitude; infinities become NaN.
-__device__ __forceinline__ float amax16(float (&y)[16]) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    y[i] = finite_or_nan(y[i]);
-    a = fmaxf(a, fabsf(y[i]));
-  }
-  return a;
-}
-// The same with the finite case apart (a NaN is dropped by fmaxf and coded as
-// such): 14.7 against 15.7 us for rows of 4,096 x 7,168.  The tiles' kernel keeps the
-// one above, at the 80 registers that three CTAs an SM leave it (33.1 against 39.4 us
-// for 32,768 x 2,048).
-__device__ __forceinline__ float amax16_rows(float (&y)[16]) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(y[i]));
-  return a > kLargest ? amax16(y) : a;
-}
-__device__ __forceinline__ uint4 codes16(const float (&y)[16], float f) {
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = e4m3x4(y[4 * i] * f, y[4 * i + 1] * f, y[4 * i + 2] * f, y[4 * i + 3] * f);
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
 // The exact quotients' codes of bf16 values.  PACKED: two values an instruction, for
 // the rows (14.7 us for 4,096 x 7,168, 14.9 without); the tiles have not the registers
 // (32,768 x 2,048: 33.1 us without, 37.5 packed).
@@ -85,13 +47,6 @@ __device__ __forceinline__ uint4 codes16_exact(const float (&y)[16], float f, fl
   }
   return codes16(q, 1.f);
 }
-// Maximum over the 8 lanes that hold one block of 128 columns.
-__device__ __forceinline__ float max8(float a) {
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  return a;
-}
-
 // Rows without a norm: a warp takes U runs of 512 columns, a lane 16 of each (a
 // block of 128 is 8 lanes, its maximum three shuffles); all of them are loaded
 // before the first is used (U = 2: 14.7 us where U = 1 took 15.6).
