@@ -1,8 +1,9 @@
-"""In-tree build of libcsa2.so for sm_103a with nvcc (no cmake).
+"""In-tree build of libcsa2.so for sm_103a with nvcc, and of the Python extension
+_csa2_call.so over it with g++ and torch's headers (no cmake).
 
 Each translation unit compiles in parallel; the objects are linked into
-``serving_lightning_indexer_gb300/_lib/libcsa2.so``.  A rebuild happens only
-when a source or header is newer than the library.
+``serving_lightning_indexer_gb300/_lib/``.  A rebuild happens only when a source
+or header is newer than its library.
 """
 from __future__ import annotations
 
@@ -10,6 +11,9 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libcsa2.so")
+CALL = os.path.join(LIBDIR, "_csa2_call.so")   # Python extension: binding.cpp
 SOURCES = ["csa2_api.cu", "index_score.cu", "select.cu", "sparse_attn.cu", "compress.cu", "topk_noalloc.cu",
            "quant_fp8.cu", "fp8_linear.cu", "batch_plan.cu", "add_norm.cu", "lora.cu", "logprobs.cu"]
 HEADERS = [os.path.join(ROOT, "include", "csa2.h")] + [
@@ -24,6 +29,31 @@ HEADERS = [os.path.join(ROOT, "include", "csa2.h")] + [
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]
+
+
+def _cuda_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+
+
+def _build_call(force: bool, verbose: bool) -> str:
+    """Compile binding.cpp; returns its object."""
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(OBJDIR, "binding.o")
+    if force or _stale(obj, [src, HEADERS[0]]):
+        include = os.path.join(os.path.dirname(torch.__file__), "include")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               *(f"-I{d}" for d in (include, os.path.join(include, "torch", "csrc", "api", "include"),
+                                    os.path.join(_cuda_home(), "include"), sysconfig.get_paths()["include"])),
+               "-c", src, "-o", obj]
+        _run(cmd, src, verbose)
+    return obj
+
+
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {what}:\n{r.stdout}\n{r.stderr}")
 
 
 def nvcc() -> str:
@@ -41,33 +71,35 @@ def _stale(target: str, deps: list[str]) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the CUDA sources and link libcsa2.so; returns its path."""
+    """Compile the sources and link libcsa2.so and _csa2_call.so; returns the former's path."""
     os.makedirs(LIBDIR, exist_ok=True)
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    if not force and not _stale(LIB, srcs + HEADERS):
+    lib_stale = force or _stale(LIB, srcs + HEADERS)
+    call_stale = force or _stale(CALL, [os.path.join(CSRC, "binding.cpp"), HEADERS[0]])
+    if not lib_stale and not call_stale:
         return LIB
     cc = nvcc()
 
     def one(src):
         obj = os.path.join(OBJDIR, os.path.basename(src).replace(".cu", ".o"))
         if force or _stale(obj, [src] + HEADERS):
-            cmd = [cc, *ARCH, *FLAGS, "-c", src, "-o", obj]
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            r = subprocess.run(cmd, capture_output=True, text=True)
-            if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+            _run([cc, *ARCH, *FLAGS, "-c", src, "-o", obj], src, verbose)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = list(ex.map(one, srcs))
-    tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        call = ex.submit(_build_call, force, verbose) if call_stale else None
+        objs = list(ex.map(one, srcs)) if lib_stale else []
+        call_obj = call.result() if call else None
+    if lib_stale:
+        _run([cc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], "libcsa2.so", verbose)
+        os.replace(LIB + ".tmp", LIB)
+    if call_stale:
+        torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+        _run(["g++", "-shared", "-o", CALL + ".tmp", call_obj, f"-L{LIBDIR}", "-lcsa2", "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}",
+              "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{torch_lib}",
+              f"-L{os.path.join(_cuda_home(), 'lib64')}", "-lcudart"], "_csa2_call.so", verbose)
+        os.replace(CALL + ".tmp", CALL)
     return LIB
 
 

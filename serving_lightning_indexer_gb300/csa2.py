@@ -3,11 +3,16 @@
 Argument marshalling only: every step runs in the CUDA kernels of
 ``libcsa2.so``.  Tensors are torch CUDA tensors (their device pointers are
 passed); there is no CPU fallback -- a missing library or a CPU tensor raises.
-Workspace is allocated by torch on first use and cached per device.
+Workspace is allocated by torch on first use and cached per device; lora_linear
+takes its own from torch's allocator for each call.  The calls around the layers
+(add_norm_fp8, lora_linear, logprobs) check and pass their tensors in the
+extension ``_csa2_call.so``.
 """
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
 import os
 import struct
 
@@ -332,16 +337,12 @@ _BF16, _F32, _U8, _INT32 = torch.bfloat16, torch.float32, torch.uint8, torch.int
 def _packer(st):
     """Packs a struct's fields in order into bytes (a fifth of the time of filling the ctypes struct)."""
     code = {_P: "P", _I32: "i", _I64: "q", C.c_float: "f"}
-
-    def form(st):
-        fmt = "".join(form(f[1]) if issubclass(f[1], C.Structure) else code[f[1]] for f in st._fields_)
-        return fmt + "x" * (C.sizeof(st) - struct.calcsize("@" + fmt))
-
-    return struct.Struct("@" + form(st)).pack
+    fmt = "@" + "".join(code[f[1]] for f in st._fields_)
+    pad = C.sizeof(st) - struct.calcsize(fmt)
+    return struct.Struct(fmt + "x" * pad).pack
 
 
 _pack_quant, _pack_linear, _pack_plan = _packer(QuantFp8Args), _packer(Fp8LinearArgs), _packer(BatchPlanArgs)
-_pack_add_norm, _pack_lora, _pack_logprobs = _packer(AddNormFp8Args), _packer(LoraLinearArgs), _packer(LogprobsArgs)
 
 
 def _device(t, name: str) -> int:
@@ -438,12 +439,6 @@ def fp8_linear(x, x_scale, w, w_scale, out, out_scale=None, row_pos=None, rope_h
     [T,ceil(K/128)], w_scale [ceil(N/128),ceil(K/128)].  out fp32, bf16, or uint8 codes with
     out_scale [T,N/128]; rope_head turns the last 64 columns of every head of that many
     columns by row_pos [T] (csa2_fp8_linear)."""
-    dev, fields = _linear_fields(x, x_scale, w, w_scale, out, out_scale, row_pos, rope_head, rope_theta, w_ready)
-    _issue(load().csa2_fp8_linear, _pack_linear(*fields), "csa2_fp8_linear", dev, stream)
-
-
-def _linear_fields(x, x_scale, w, w_scale, out, out_scale, row_pos, rope_head, rope_theta, w_ready):
-    """(device, the fields of csa2_fp8_linear_args) of a projection's checked tensors."""
     dev = _device(x, "x")
     T, K = x_shape = _two_d(x, "x")
     N, _ = w_shape = _two_d(w, "w")
@@ -458,117 +453,10 @@ def _linear_fields(x, x_scale, w, w_scale, out, out_scale, row_pos, rope_head, r
         raise TypeError(f"out: expected float32, bfloat16 or uint8, got {kind}")
     po, ldo = _mat(out, "out", kind, dev, (T, N))
     pos, ldos = (0, 0) if out_scale is None else _mat(out_scale, "out_scale", _F32, dev, (T, N // 128))
-    return dev, (px, ldx, pxs, ldxs, pw, ldw, pws, ldws, T, N, K, fmt, po, ldo, pos, ldos,
-                 _vec(row_pos, "row_pos", _INT32, dev, T), rope_head, rope_theta, 1 if w_ready else 0)
-
-
-def lora_linear(x, x_scale, w, w_scale, a, b, row_adapter, out, adapter_scale=None, out_scale=None, row_pos=None, rope_head=0,
-                rope_theta=0.0, w_ready=False, stream=None, ws=None):
-    """fp8_linear with the low-rank adapters of many requests beside it: a [n,rank,K] and
-    b [n,N,rank] bf16, adapter_scale [n] fp32 (None: 1), row_adapter [T] int32, -1 for a row
-    without one.  Row t of an adapter i gets adapter_scale[i] * (x[t] a[i]^T) b[i]^T added
-    before RoPE and rounding (csa2_lora_linear).  ws: a uint8 tensor of at least
-    lora_workspace_size(T, rank) bytes that nothing else uses until the call's work is
-    done; None takes one from torch's allocator, on the call's stream."""
-    dev, fields = _linear_fields(x, x_scale, w, w_scale, out, out_scale, row_pos, rope_head, rope_theta, w_ready)
-    T, N, K = fields[8:11]
-    for t, name in ((a, "a"), (b, "b")):
-        if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.get_device() != dev:
-            _refuse(t, name, _BF16, dev)
-        if t.dim() != 3 or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous 3-D tensor, got {list(t.shape)}")
-    n, rank, _ = a.shape
-    if a.shape[2] != K or b.shape != (n, N, rank):
-        raise ValueError(f"a, b: expected [n,rank,{K}] and [n,{N},rank], got {list(a.shape)} and {list(b.shape)}")
-    if row_adapter is None:
-        raise TypeError("row_adapter: expected a torch tensor")
-    packed = _pack_lora(*fields, _vec(row_adapter, "row_adapter", _INT32, dev, T), n, rank, a.data_ptr() or _EMPTY,
-                        b.data_ptr() or _EMPTY, _vec(adapter_scale, "adapter_scale", _F32, dev, n))
-    if ws is None:
-        ws = _scratch(_lora_bytes(packed, T, rank), dev, stream)
-    elif not isinstance(ws, _Tensor) or ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError(f"ws: expected a contiguous uint8 tensor on cuda:{dev}")
-    fn, at, size = load().csa2_lora_linear, ws.data_ptr(), ws.numel()
-    _issue(lambda args, st: fn(args, at, size, st), packed, "csa2_lora_linear", dev, stream)
-
-
-_lora_ws_bytes: dict = {}
-
-
-def _lora_bytes(packed: bytes, T: int, rank: int) -> int:
-    need = _lora_ws_bytes.get((T, rank))
-    if need is None:
-        size = C.c_size_t(0)
-        _check(load().csa2_workspace_size(CALL_LORA_LINEAR, packed, C.byref(size)), "csa2_workspace_size")
-        need = _lora_ws_bytes[T, rank] = size.value
-    return need
-
-
-def lora_workspace_size(T: int, rank: int) -> int:
-    """Bytes of workspace that lora_linear takes for T rows and adapters of a rank."""
-    base = Fp8LinearArgs(x=16, ld_x=16, x_scale=16, ld_x_scale=1, w=16, ld_w=16, w_scale=16, ld_w_scale=1, T=T, N=1, K=16,
-                         out=16, ld_out=1)
-    return _lora_bytes(bytes(LoraLinearArgs(base=base, row_adapter=16, n_adapters=1, rank=rank, a=16, b=16)), T, rank)
-
-
-def _scratch(nbytes: int, dev: int, stream) -> torch.Tensor:
-    """A buffer of the call's own, from the stream that the call runs on: it may be
-    handed out again only behind the call's work (in a capture, within its graph)."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=_U8, device=torch.device("cuda", dev))
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)
-        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=_U8, device=torch.device("cuda", dev))
-
-
-def add_norm_fp8(x, residual, residual_out, gamma, codes=None, scale=None, y=None, eps=1e-6, stream=None):
-    """residual_out = x + residual ([T,K]; x bf16, the residual bf16 or fp32, in place if they are
-    one tensor), and its RMSNorm with gamma [K] as e4m3 codes uint8 [T,K] with a scale per
-    128 columns [T,ceil(K/128)], as bf16 y [T,K], or both (csa2_add_norm_fp8)."""
-    dev = _device(x, "x")
-    T, K = shape = _two_d(x, "x")
-    px, ldx = _mat(x, "x", _BF16, dev, shape)
-    kind = getattr(residual, "dtype", None)
-    if kind is not _F32 and kind is not _BF16:
-        raise TypeError(f"residual: expected bfloat16 or float32, got {kind}")
-    pr, ldr = _mat(residual, "residual", kind, dev, shape)
-    po, ldo = _mat(residual_out, "residual_out", kind, dev, shape)
-    pc, ldc = (0, 0) if codes is None else _mat(codes, "codes", _U8, dev, shape)
-    ps, lds = (0, 0) if scale is None else _mat(scale, "scale", _F32, dev, (T, (K + 127) // 128))
-    py, ldy = (0, 0) if y is None else _mat(y, "y", _BF16, dev, shape)
-    if gamma is None:
-        raise TypeError("gamma: expected a torch tensor")
-    _issue(load().csa2_add_norm_fp8, _pack_add_norm(px, ldx, pr, ldr, po, ldo, 1 if kind is _F32 else 0, T, K,
-                                                    _vec(gamma, "gamma", _F32, dev, K), eps, pc, ldc, ps, lds, py, ldy),
-           "csa2_add_norm_fp8", dev, stream)
-
-
-def logprobs(logits, token=None, logprob=None, entropy=None, lse=None, top_id=None, top_logprob=None, stream=None):
-    """Of the rows of logits [T,V] (fp32 or bf16): the log probability [T] of token [T] (int32, -1:
-    none), the entropy [T], the log of the sum of exponentials [T], and the n best tokens'
-    ids [T,n] int32 and log probabilities [T,n], best first, ties to the lower id, n <= 32.
-    Every output is optional (csa2_logprobs)."""
-    dev = _device(logits, "logits")
-    T, V = shape = _two_d(logits, "logits")
-    kind = logits.dtype
-    if kind is not _F32 and kind is not _BF16:
-        raise TypeError(f"logits: expected float32 or bfloat16, got {kind}")
-    pl, ldl = _mat(logits, "logits", kind, dev, shape)
-    n = pi = pt = ld = 0
-    if top_id is not None:
-        n = _two_d(top_id, "top_id")[1]
-        pi, ld = _mat(top_id, "top_id", _INT32, dev, (T, n))
-    if top_logprob is not None:
-        n = n if top_id is not None else _two_d(top_logprob, "top_logprob")[1]
-        pt, ld_t = _mat(top_logprob, "top_logprob", _F32, dev, (T, n))
-        if top_id is not None and ld_t != ld:
-            raise ValueError("top_id, top_logprob: expected one row stride")
-        ld = ld_t
-    _issue(load().csa2_logprobs, _pack_logprobs(pl, ldl, 1 if kind is _F32 else 0, T, V, _vec(token, "token", _INT32, dev, T),
-                                                _vec(logprob, "logprob", _F32, dev, T), _vec(entropy, "entropy", _F32, dev, T),
-                                                _vec(lse, "lse", _F32, dev, T), n, pi, pt, ld), "csa2_logprobs", dev, stream)
+    _issue(load().csa2_fp8_linear,
+           _pack_linear(px, ldx, pxs, ldxs, pw, ldw, pws, ldws, T, N, K, fmt, po, ldo, pos, ldos,
+                        _vec(row_pos, "row_pos", _INT32, dev, T), rope_head, rope_theta, 1 if w_ready else 0),
+           "csa2_fp8_linear", dev, stream)
 
 
 def batch_plan(ctx_len, new_len, ratio_m=1, page_table=None, free_pages=None, free_head=None, free_head_out=None,
@@ -613,6 +501,66 @@ def batch_plan(ctx_len, new_len, ratio_m=1, page_table=None, free_pages=None, fr
         _vec(entry_row, "entry_row", i32, dev, entry_cap),
         swa_ring, _vec(ring_id, "ring_id", i32, dev, B), _vec(swa_new, "swa_new", i32, dev, row_cap), ss, n_swa, lds,
         1 if pad else 0), "csa2_batch_plan", dev, stream)
+
+
+# ---------------------------------------------------------------- around the layers
+_call = None
+
+
+def _load_call():
+    """The extension that checks and passes the tensors of the calls below (raises if it has not been built)."""
+    global _call
+    load()
+    if not os.path.exists(_build.CALL):
+        raise RuntimeError(f"_csa2_call.so is not built ({_build.CALL}); run __graft_entry__.build()")
+    loader = importlib.machinery.ExtensionFileLoader("_csa2_call", _build.CALL)
+    _call = importlib.util.module_from_spec(importlib.util.spec_from_loader("_csa2_call", loader))
+    loader.exec_module(_call)
+    return _call
+
+
+def add_norm_fp8(x, residual, residual_out, gamma, codes=None, scale=None, y=None, eps=1e-6, stream=None):
+    """residual_out = x + residual ([T,K]; x bf16, the residual bf16 or fp32, in place if they are
+    one tensor), and its RMSNorm with gamma [K] fp32 as e4m3 codes uint8 [T,K] with a scale per
+    128 columns [T,ceil(K/128)], as bf16 y [T,K], or both (csa2_add_norm_fp8)."""
+    rc = (_call or _load_call()).add_norm_fp8(x, residual, residual_out, gamma, codes, scale, y, eps,
+                                              None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "csa2_add_norm_fp8")
+
+
+def lora_linear(x, x_scale, w, w_scale, a, b, row_adapter, out, adapter_scale=None, out_scale=None, row_pos=None, rope_head=0,
+                rope_theta=0.0, w_ready=False, stream=None, ws=None):
+    """fp8_linear with the low-rank adapters of many requests beside it: a [n,rank,K] and
+    b [n,N,rank] bf16, adapter_scale [n] fp32 (None: 1), row_adapter [T] int32, -1 for a row
+    without one.  Row t of an adapter i gets adapter_scale[i] * (x[t] a[i]^T) b[i]^T added
+    before RoPE and rounding (csa2_lora_linear).  ws: a uint8 tensor of at least
+    lora_workspace_size(T, rank) bytes that nothing else uses until the call's work is
+    done; None takes one from torch's allocator, on the call's stream."""
+    rc = (_call or _load_call()).lora_linear(x, x_scale, w, w_scale, a, b, row_adapter, out, adapter_scale, out_scale, row_pos,
+                                             rope_head, rope_theta, w_ready, None if stream is None else _stream(stream), ws)
+    if rc:
+        _check(rc, "csa2_lora_linear")
+
+
+def lora_workspace_size(T: int, rank: int) -> int:
+    """Bytes of workspace that lora_linear takes for T rows and adapters of a rank."""
+    base = Fp8LinearArgs(x=16, ld_x=16, x_scale=16, ld_x_scale=1, w=16, ld_w=16, w_scale=16, ld_w_scale=1, T=T, N=1, K=16,
+                         out=16, ld_out=1)
+    a, size = LoraLinearArgs(base=base, row_adapter=16, n_adapters=1, rank=rank, a=16, b=16), C.c_size_t(0)
+    _check(load().csa2_workspace_size(CALL_LORA_LINEAR, C.cast(C.byref(a), _P), C.byref(size)), "csa2_workspace_size")
+    return size.value
+
+
+def logprobs(logits, token=None, logprob=None, entropy=None, lse=None, top_id=None, top_logprob=None, stream=None):
+    """Of the rows of logits [T,V] (fp32 or bf16): the log probability [T] of token [T] (int32, -1:
+    none), the entropy [T], the log of the sum of exponentials [T], and the n best tokens'
+    ids [T,n] int32 and log probabilities [T,n], best first, ties to the lower id, n <= 32.
+    Every output is optional (csa2_logprobs)."""
+    rc = (_call or _load_call()).logprobs(logits, token, logprob, entropy, lse, top_id, top_logprob,
+                                          None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "csa2_logprobs")
 
 
 def check_device_error(stream=None) -> int:

@@ -39,14 +39,6 @@ def test_ctypes_structs_match_c_layout():
     assert got == want
 
 
-def test_packed_bytes_are_the_struct():
-    from serving_lightning_indexer_gb300 import csa2
-    base = csa2.Fp8LinearArgs(x=1, ld_x=2, T=3, N=4, K=5, out_format=2, rope_theta=1.5, w_ready=1)
-    a = csa2.LoraLinearArgs(base=base, row_adapter=6, n_adapters=7, rank=8, a=9, b=10, adapter_scale=11)
-    fields = [getattr(base, f[0]) or 0 for f in base._fields_]
-    assert csa2._pack_lora(*fields, 6, 7, 8, 9, 10, 11) == bytes(a)
-
-
 def _norm(**kw):
     from serving_lightning_indexer_gb300 import csa2
     base = dict(x=FAKE, ld_x=256, residual=FAKE + STEP, ld_residual=256, residual_out=FAKE + 2 * STEP, ld_residual_out=256,

@@ -342,7 +342,7 @@ def test_lora_linear_binding_refuses():
         csa2.lora_linear(x, xs, w, ws, a, b, ids[:3], y)
     with pytest.raises(TypeError, match="row_adapter"):
         csa2.lora_linear(x, xs, w, ws, a, b, None, y)
-    with pytest.raises(ValueError, match="ws: "):
+    with pytest.raises(TypeError, match="ws: "):
         csa2.lora_linear(x, xs, w, ws, a, b, ids, y, ws=torch.empty(8, device=dev))
     with pytest.raises(csa2.Csa2Error, match="needed"):
         csa2.lora_linear(x, xs, w, ws, a, b, ids, y, ws=torch.empty(16, dtype=torch.uint8, device=dev))
