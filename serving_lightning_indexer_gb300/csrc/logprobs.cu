@@ -10,10 +10,11 @@
 // log probability, -ln(1 + R) with R far below 1.  Entropy is a sum of two terms of
 // one sign.  R and W are fp32; a running maximum a warp rescales them.
 //
-// Alternatives: a thread keeps, for each of its runs of 16-byte words, the best word
-// by (largest logit, lower place).  The n best words of all runs name the n runs
-// that hold the n best logits (each of those n words holds a logit that beats all
-// of another run's), and only these runs are read again.
+// Alternatives: a thread keeps the largest logit of each of its runs of 16-byte words.
+// No logit below the n-th largest of the threads' largest ones, tau, is among the n best,
+// as n threads hold one that is not below it; so only the runs with a logit of at least
+// tau are read again, and of those logits, few more than n, the n best by (value, lower
+// token) are sorted out.  Where many runs tie with tau, all of the row is read again.
 //
 // Bound: HBM where there are many rows; a few rows are split over a cluster of CTAs
 // and are bound by latency.
@@ -25,10 +26,28 @@
 namespace csa2 {
 namespace {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kBatch = 4;     // 16-byte words a thread loads at a time
-constexpr int kMaxRuns = 8;   // runs of a thread
-constexpr int kMaxList = 1024;  // candidates that are sorted from a list; more are merged one by one
+constexpr int kLpWarps = 8, kLpThreads = kLpWarps * 32;
+// 16-byte words of a thread at a time, and how many such batches its ring holds
+template <bool F32>
+constexpr int kBatch = F32 ? 4 : 2;
+template <bool F32, bool DEEP>
+constexpr int kStages = F32 && !DEEP ? 2 : 4;
+template <bool F32, bool DEEP>
+constexpr int kRingBytes = kStages<F32, DEEP> * kBatch<F32> * kLpThreads * 16;
+// Runs of a thread, and their batches at least.
+constexpr int kMaxRuns = 4;
+template <int NW>
+constexpr int kRunBatches = NW == 1 ? 1 : 4;
+// Logits are summed as if none were below this: e^(x - M) of one further down is 0 next
+// to any M above it, and x - M stays finite.  A row whose M is not above it is summed
+// as it is.
+constexpr float kLowest = -1.2676506e30f;  // -2^100, exact in bf16
+// Of a row: candidates that are sorted from a list (more are merged as they are read),
+// and runs that are read again (with more, all are).
+template <int NW>
+constexpr int kMaxList = NW == 1 ? 256 : 1024;
+constexpr int kMaxTied = 128;
+constexpr float kLargestFloat = 3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFar = -200.f;  // e^x is 0 in fp32 from -104 on
 
@@ -72,20 +91,38 @@ __device__ __forceinline__ Sums merge(Sums a, Sums b) {
   return a;
 }
 
-// Order of (value, lower place first) as a 64-bit key; 0: nothing.
+// The place of a lane's item, if it has one, at the end of a row's list of *count.  The
+// items of a row's only warp come many at a time and take their places together; of a
+// CTA's warps few lanes have one at a time.
+template <int NW>
+__device__ __forceinline__ int append(int* count, bool is) {
+  if (NW > 1) return is ? atomicAdd(count, 1) : 0;
+  const uint32_t mask = __ballot_sync(0xffffffffu, is);
+  const int lane = threadIdx.x & 31, before = *count;
+  __syncwarp();
+  if (lane == 0) *count = before + __popc(mask);
+  __syncwarp();
+  return before + __popc(mask & ((1u << lane) - 1));
+}
+// Order of a value, and of (value, lower place first) as a 64-bit key; 0: nothing.
+__device__ __forceinline__ uint32_t value_key(float x) { return ord_key(x + 0.f); }  // -0 is 0
+__device__ __forceinline__ uint32_t run_key(float x) { return x > -INFINITY ? value_key(x) : 0u; }
 __device__ __forceinline__ unsigned long long top_key(float x, uint32_t place) {
-  return (static_cast<unsigned long long>(ord_key(x + 0.f)) << 32) | (0xFFFFFFFFu - place);  // -0 is 0
+  return (static_cast<unsigned long long>(value_key(x)) << 32) | (0xFFFFFFFFu - place);
 }
 __device__ __forceinline__ float key_value(unsigned long long k) { return ord_to_float(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ uint32_t key_place(unsigned long long k) { return 0xFFFFFFFFu - static_cast<uint32_t>(k); }
 
 // One step of a bitonic network over the warp's lanes: the pair (lane, lane ^ d).
-__device__ __forceinline__ unsigned long long bitonic_step(unsigned long long k, int d, bool larger) {
-  const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
+// K: the 64-bit keys, or the upper halves alone.
+template <class K>
+__device__ __forceinline__ K bitonic_step(K k, int d, bool larger) {
+  const K o = __shfl_xor_sync(0xffffffffu, k, d);
   return (k > o) == larger ? k : o;
 }
 // Sorts the lanes' keys ascending.
-__device__ __forceinline__ unsigned long long sort_up(unsigned long long k) {
+template <class K>
+__device__ __forceinline__ K sort_up(K k) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int s = 2; s <= 32; s <<= 1)
@@ -95,23 +132,57 @@ __device__ __forceinline__ unsigned long long sort_up(unsigned long long k) {
 }
 // The 32 best of a list (descending over the lanes) and of keys that ascend over
 // the lanes, descending.
-__device__ __forceinline__ unsigned long long merge_best(unsigned long long list, unsigned long long up) {
+template <class K>
+__device__ __forceinline__ K merge_best(K list, K up) {
   const int lane = threadIdx.x & 31;
-  unsigned long long k = list > up ? list : up;
+  K k = list > up ? list : up;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) k = bitonic_step(k, d, (lane & d) == 0);
   return k;
 }
 // Adds the lanes' keys to the warp's list, unless none of them is among its n best.
-__device__ __forceinline__ void add_keys(unsigned long long& list, unsigned long long k, int n) {
-  const unsigned long long least = __shfl_sync(0xffffffffu, list, n - 1);
-  if (__any_sync(0xffffffffu, k > least)) list = merge_best(list, sort_up(k));
+// n == 1: every lane keeps its best.
+template <class K>
+__device__ __forceinline__ void add_keys(K& list, K k, int n) {
+  if (n == 1) {
+    list = list > k ? list : k;
+    return;
+  }
+  const K least = __shfl_sync(0xffffffffu, list, n - 1);
+  if (!__any_sync(0xffffffffu, k > least)) return;
+  const K up = sort_up(k);
+  // a list without keys takes them as they are
+  list = __any_sync(0xffffffffu, list != 0) ? merge_best(list, up) : __shfl_sync(0xffffffffu, up, 31 - (threadIdx.x & 31));
 }
-// The best of the warps' lists, in warp 0.  s: [kLpWarps][32].
-__device__ __forceinline__ unsigned long long join_lists(unsigned long long list, unsigned long long (*s)[32]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <class K>
+__device__ __forceinline__ K warp_best(K k) {
 #pragma unroll
-  for (int h = kLpWarps / 2; h > 0; h >>= 1) {
+  for (int d = 16; d > 0; d >>= 1) k = bitonic_step(k, d, true);
+  return k;
+}
+// Barrier of a row's NW warps: one of the CTA's, or all.
+template <int NW>
+__device__ __forceinline__ void sync_row() {
+  if (NW == 1) __syncwarp();
+  else __syncthreads();
+}
+// The best of the NW warps' lists, in the row's first warp (n == 1: of all lanes' keys, in
+// every lane).  s: [NW][32].
+template <int NW, class K>
+__device__ __forceinline__ K join_lists(K list, K (*s)[32], int n) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (n == 1) list = warp_best(list);
+  if (NW == 1) return list;
+  if (n == 1) {
+    if (lane == 0) s[0][warp] = list;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NW; ++i) list = list > s[0][i] ? list : s[0][i];
+    __syncthreads();
+    return list;
+  }
+#pragma unroll
+  for (int h = NW / 2; h > 0; h >>= 1) {
     if (warp >= h && warp < 2 * h) s[warp][lane] = list;
     __syncthreads();
     if (warp < h) list = merge_best(list, s[warp + h][31 - lane]);
@@ -139,28 +210,28 @@ struct Row {
     V = v;
     n = static_cast<int>((static_cast<long long>(v) + lead + kEl - 1) / kEl);
   }
-  // Logits of word i (-inf where there is none).
-  __device__ __forceinline__ void load(int i, float (&x)[kEl]) const {
-    if (i < n && (i > 0 || lead == 0) && static_cast<long long>(i + 1) * kEl - lead <= V) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(words) + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // The words that are all the row's: from whole0() up to whole1().
+  __device__ __forceinline__ int whole0() const { return lead ? 1 : 0; }
+  __device__ __forceinline__ int whole1() const { return static_cast<int>((static_cast<long long>(V) + lead) / kEl); }
+  // Word i; -inf where there is no logit.
+  __device__ __forceinline__ uint4 load(int i) const {
+    if (i >= whole0() && i < whole1()) return __ldg(reinterpret_cast<const uint4*>(words) + i);
+    uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (F32) {
-          x[j] = __uint_as_float(w[j]);
-        } else {
-          x[2 * j] = __uint_as_float(w[j] << 16);
-          x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kEl; ++j) {
-        const long long e = static_cast<long long>(i) * kEl + j - lead;
-        x[j] = -INFINITY;
-        if (i < n && e >= 0 && e < V) x[j] = at(static_cast<int>(e));
+    for (int j = 0; j < 4; ++j) {
+      const long long e = static_cast<long long>(i) * kEl + (F32 ? j : 2 * j) - lead;
+      if (F32) {
+        w[j] = bits(i, e);
+      } else {
+        w[j] = bits(i, e) | (bits(i, e + 1) << 16);
       }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint32_t bits(int i, long long e) const {
+    if (i >= n || e < 0 || e >= V) return F32 ? 0xFF800000u : 0xFF80u;
+    const uint8_t* p = words + (static_cast<long long>(lead) + e) * kSize;
+    return F32 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : __ldg(reinterpret_cast<const unsigned short*>(p));
   }
   __device__ __forceinline__ float at(int e) const {
     const uint8_t* p = words + (static_cast<long long>(lead) + e) * kSize;
@@ -169,27 +240,178 @@ struct Row {
   }
 };
 
-// A cluster of gridDim.x / rows CTAs takes a row, each a run of its words.
-template <bool F32, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_constant__ LogprobParams p, int splits) {
-  constexpr int kEl = Row<F32>::kEl;
+// A 16-byte copy global -> shared that the thread waits for by group.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // drops a NaN
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// A 16-byte word's logits.
+template <bool F32>
+struct Word {
+  static constexpr int kEl = F32 ? 4 : 8;
+  // The largest of N words; NaN only where all logits are.
+  template <int N>
+  static __device__ __forceinline__ float largest(const uint4 (&v)[N]) {
+    if (F32) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
+                           fmaxf(__uint_as_float(v[u].z), __uint_as_float(v[u].w))));
+      return m;
+    }
+    uint32_t m = 0xFF80FF80u;
+#pragma unroll
+    for (int u = 0; u < N; ++u) m = max_bf16x2(m, max_bf16x2(max_bf16x2(v[u].x, v[u].y), max_bf16x2(v[u].z, v[u].w)));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[kEl]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (F32) {
+        x[j] = __uint_as_float(w[j]);
+      } else {
+        x[2 * j] = bf16_lo(w[j]);
+        x[2 * j + 1] = bf16_hi(w[j]);
+      }
+    }
+  }
+  // Makes one logit equal to top -inf, if the word has one.
+  static __device__ __forceinline__ bool remove(uint4& v, float top) {
+    const uint4 one[1] = {v};
+    if (largest(one) != top) return false;
+    if (!remove(v.x, top) && !remove(v.y, top) && !remove(v.z, top)) remove(v.w, top);
+    return true;
+  }
+  static __device__ __forceinline__ bool remove(uint32_t& w, float top) {
+    if (F32) {
+      if (__uint_as_float(w) != top) return false;
+      w = 0xFF800000u;
+      return true;
+    }
+    if (bf16_lo(w) == top) {
+      w = (w & 0xFFFF0000u) | 0xFF80u;
+      return true;
+    }
+    if (bf16_hi(w) != top) return false;
+    w = (w & 0xFFFFu) | 0xFF800000u;
+    return true;
+  }
+  // +inf made -inf
+  static __device__ __forceinline__ void drop_inf(uint32_t& w) {
+    if (F32) {
+      if (w == 0x7F800000u) w = 0xFF800000u;
+    } else {
+      if ((w & 0xFFFFu) == 0x7F80u) w |= 0x8000u;
+      if ((w >> 16) == 0x7F80u) w |= 0x80000000u;
+    }
+  }
+  // Adds the terms of two logits of the word, both raised to kLowest (which a NaN
+  // becomes as well).
+  static __device__ __forceinline__ void add(float a, float b, uint64_t minus_m, uint64_t& r, uint64_t& w) {
+    const uint64_t d = add_f32x2(pack_f32x2(a, b), minus_m);
+    const float2 e2 = unpack_f32x2(mul_f32x2(d, pack_f32x2(kLog2e, kLog2e)));
+    const uint64_t e = pack_f32x2(exp2_fast(e2.x), exp2_fast(e2.y));
+    r = add_f32x2(r, e);
+    w = fma_f32x2(e, d, w);
+  }
+  static __device__ __forceinline__ void add_word(const uint4& v, uint64_t minus_m, uint64_t& r, uint64_t& w) {
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+    if (F32) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2)
+        add(fmaxf(__uint_as_float(q[j]), kLowest), fmaxf(__uint_as_float(q[j + 1]), kLowest), minus_m, r, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t c = max_bf16x2(q[j], 0xF180F180u);  // kLowest twice
+        add(bf16_lo(c), bf16_hi(c), minus_m, r, w);
+      }
+    }
+  }
+};
+
+// A row is NW warps' work: one warp's, or a CTA's, or that of a cluster of `splits` CTAs,
+// each with a run of its words.  A thread copies its words ahead into places of its own
+// in shared memory, so the pass has no barrier.
+template <bool F32, bool TOP, int NW, bool DEEP>
+__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_constant__ LogprobParams p, int T, int splits) {
+  constexpr int kEl = Row<F32>::kEl, B = kBatch<F32>, S = kStages<F32, DEEP>, kThreads = NW * 32, kRows = kLpWarps / NW;
+  constexpr uint32_t kNone = F32 ? 0xFF800000u : 0xFF80FF80u;
+  constexpr int kRing = S * B * kThreads, kList = kMaxList<NW>;
+  static_assert((NW * 32 + kList) * 8 <= kRing * 16, "the lists fit the row's ring");
   __shared__ Sums s_sums[kLpWarps];
   __shared__ Sums s_part;
-  __shared__ unsigned long long s_keys[TOP ? kLpThreads * kMaxRuns : 1];
-  __shared__ unsigned long long s_cand[TOP ? kMaxList : 1];
-  __shared__ unsigned long long s_lists[TOP ? kLpWarps : 1][32];
+  __shared__ float s_all_runs[kRows][TOP ? kThreads * kMaxRuns : 1];  // the runs' largest logits
+  __shared__ int s_all_tied[kRows][TOP ? kMaxTied : 1];
   __shared__ unsigned long long s_best[32];
-  __shared__ int s_count;
+  __shared__ float s_taus[kRows];
+  __shared__ int s_counts[kRows], s_tied_counts[kRows];
+  extern __shared__ uint4 s_all[];  // [kRows][S][B][kThreads]; behind the pass, lists and candidates
   pdl_wait();
   pdl_trigger();
-  const long long t = blockIdx.x / splits;
-  const int rank = blockIdx.x % splits;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int mine = NW == 1 ? threadIdx.x >> 5 : 0;  // of the CTA's rows
+  const long long t = NW == 1 ? static_cast<long long>(blockIdx.x) * kRows + mine : blockIdx.x / splits;
+  if (NW == 1 && t >= T) return;
+  const int rank = NW == 1 ? 0 : blockIdx.x % splits;
+  const int tid = threadIdx.x % kThreads, warp = tid >> 5, lane = tid & 31;
+  uint4* s_ring = s_all + mine * kRing;
+  unsigned long long(*s_lists)[32] = reinterpret_cast<unsigned long long(*)[32]>(s_ring);
+  unsigned long long* s_cand = reinterpret_cast<unsigned long long*>(s_ring) + NW * 32;
+  float* s_runs = s_all_runs[mine];
+  int* s_tied = s_all_tied[mine];
+  int &s_count = s_counts[mine], &s_tied_count = s_tied_counts[mine];
+  float& s_tau = s_taus[mine];
   const Row<F32> row(p.logits, t * p.ld, p.V);
   const int share = (row.n + splits - 1) / splits;
   const int first = min(row.n, rank * share), words = min(row.n, first + share) - first;
-  const int batches = (words + kLpThreads * kBatch - 1) / (kLpThreads * kBatch);  // of this CTA's threads
-  const int run_batches = max(1, (batches + kMaxRuns - 1) / kMaxRuns);
+  const int batches = (words + kThreads * B - 1) / (kThreads * B);
+  const int run_batches = max(kRunBatches<NW>, (batches + kMaxRuns - 1) / kMaxRuns);
+  const int whole0 = row.whole0(), whole1 = min(row.whole1(), first + words);
+  uint4* place = s_ring + tid;
+  auto fetch = [&](int b) {
+    if (b < batches) {
+      const int w0 = first + b * kThreads * B, st = b % S;
+      if (w0 >= whole0 && w0 + kThreads * B <= whole1) {
+        const uint8_t* src = row.words + (static_cast<long long>(w0) + tid) * 16;
+#pragma unroll
+        for (int u = 0; u < B; ++u) copy16(place + (st * B + u) * kThreads, src + u * kThreads * 16);
+      } else {  // the row's ends, and what is behind them
+#pragma unroll 1
+        for (int u = 0; u < B; ++u) {
+          const int i = w0 + u * kThreads + tid;
+          if (i >= whole0 && i < whole1) copy16(place + (st * B + u) * kThreads, row.words + static_cast<long long>(i) * 16);
+          else place[(st * B + u) * kThreads] = i < first + words ? row.load(i) : make_uint4(kNone, kNone, kNone, kNone);
+        }
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int b = 0; b < S - 1; ++b) fetch(b);
   int token = -1;
   float given = -INFINITY;
   if (rank == 0 && tid == 0 && p.token) {
@@ -204,41 +426,26 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
   // ---- one pass
   float m = -INFINITY;  // the warp's largest logit so far
   float r = 0.f, w = 0.f;
-  float run_max = -INFINITY;
-  uint32_t run_word = 0;
+  float run_max = -INFINITY, thread_max = -INFINITY;
   int run = 0, left = run_batches;
   for (int b = 0; b < batches; ++b) {
-    float x[kBatch][kEl];
-    float best = -INFINITY;
+    copy_wait<S - 2>();
+    uint4 x[B];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = (b * kBatch + u) * kLpThreads + tid;
-      if (i < words) {
-        row.load(first + i, x[u]);
-      } else {
+    for (int u = 0; u < B; ++u) x[u] = place[(b % S * B + u) * kThreads];
+    fetch(b + S - 1);
+    float best = Word<F32>::largest(x);
+    if (best == INFINITY) {
 #pragma unroll
-        for (int j = 0; j < kEl; ++j) x[u][j] = -INFINITY;
+      for (int u = 0; u < B; ++u) {
+        Word<F32>::drop_inf(x[u].x);
+        Word<F32>::drop_inf(x[u].y);
+        Word<F32>::drop_inf(x[u].z);
+        Word<F32>::drop_inf(x[u].w);
       }
+      best = Word<F32>::largest(x);
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      float g = x[u][0];
-#pragma unroll
-      for (int j = 1; j < kEl; ++j) g = fmaxf(g, x[u][j]);  // drops a NaN
-      if (g == INFINITY) {
-        g = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < kEl; ++j) {
-          if (x[u][j] == INFINITY) x[u][j] = -INFINITY;
-          g = fmaxf(g, x[u][j]);
-        }
-      }
-      if (TOP && g > run_max) {
-        run_max = g;
-        run_word = first + (b * kBatch + u) * kLpThreads + tid;
-      }
-      best = fmaxf(best, g);
-    }
+    run_max = fmaxf(run_max, best);
     if (__any_sync(0xffffffffu, best > m)) {
       float top = best;
 #pragma unroll
@@ -252,26 +459,35 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
       if (lane == __ffs(__ballot_sync(0xffffffffu, best == top)) - 1) {
         bool out = false;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-#pragma unroll
-          for (int j = 0; j < kEl; ++j)
-            if (!out && x[u][j] == top) {
-              x[u][j] = -INFINITY;
-              out = true;
-            }
+        for (int u = 0; u < B; ++u)
+          if (!out) out = Word<F32>::remove(x[u], top);
       }
     }
+    if (m > kLowest) {
+      const uint64_t minus_m = pack_f32x2(-m, -m);
+      uint64_t r2 = pack_f32x2(r, 0.f), w2 = pack_f32x2(w, 0.f);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u)
+      for (int u = 0; u < B; ++u) Word<F32>::add_word(x[u], minus_m, r2, w2);
+      const float2 rs = unpack_f32x2(r2), ws = unpack_f32x2(w2);
+      r = rs.x + rs.y;
+      w = ws.x + ws.y;
+    } else {
 #pragma unroll
-      for (int j = 0; j < kEl; ++j) {
-        const float d = fmaxf(x[u][j] - m, kFar);  // masked logits and NaN: e^d is 0
-        const float e = exp_neg(d);
-        r += e;
-        w = fmaf(e, d, w);
+      for (int u = 0; u < B; ++u) {
+        float y[kEl];
+        Word<F32>::unpack(x[u], y);
+#pragma unroll
+        for (int j = 0; j < kEl; ++j) {
+          const float d = fmaxf(y[j] - m, kFar);  // masked logits and NaN: e^d is 0
+          const float e = exp_neg(d);
+          r += e;
+          w = fmaf(e, d, w);
+        }
       }
+    }
     if (TOP && (--left == 0 || b + 1 == batches)) {
-      s_keys[run++ * kLpThreads + tid] = run_max > -INFINITY ? top_key(run_max, run_word) : 0ull;
+      s_runs[run++ * kThreads + tid] = run_max;
+      thread_max = fmaxf(thread_max, run_max);
       run_max = -INFINITY;
       left = run_batches;
     }
@@ -281,83 +497,104 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
     r += __shfl_xor_sync(0xffffffffu, r, o);
     w += __shfl_xor_sync(0xffffffffu, w, o);
   }
-  if (lane == 0) s_sums[warp] = Sums{m, r, w};
-  if (tid == 0) s_count = 0;
-  __syncthreads();
-  Sums all = s_sums[0];
+  Sums all = {m, r, w};
+  if (NW > 1 && lane == 0) s_sums[warp] = all;
+  if (tid == 0) s_count = s_tied_count = 0;
+  sync_row<NW>();
+  if (NW > 1 && warp == 0) {
+    all = Sums{-INFINITY, 0.f, 0.f};
+    if (lane < NW) all = s_sums[lane];
 #pragma unroll
-  for (int i = 1; i < kLpWarps; ++i) all = merge(all, s_sums[i]);
+    for (int o = 1; o < NW; o <<= 1)
+      all = merge(all, Sums{__shfl_down_sync(0xffffffffu, all.m, o), __shfl_down_sync(0xffffffffu, all.r, o),
+                            __shfl_down_sync(0xffffffffu, all.w, o)});
+    all = Sums{__shfl_sync(0xffffffffu, all.m, 0), __shfl_sync(0xffffffffu, all.r, 0), __shfl_sync(0xffffffffu, all.w, 0)};
+  }
 
-  // ---- this CTA's best logits, descending over warp 0's lanes
+  // ---- the best of these logits, descending over the first warp's lanes
   unsigned long long list = 0;
   if (TOP) {
-    for (int i = warp * 32; i < run * kLpThreads; i += kLpThreads) add_keys(list, s_keys[i + lane], p.n);
-    list = join_lists(list, s_lists);
-    if (warp == 0) s_best[lane] = lane < p.n ? list : 0ull;
-    __syncthreads();
-    const unsigned long long least = s_best[p.n - 1];
-    const int run_words = run_batches * kBatch;
-    // logits of the best runs that are no worse than the n-th best word
+    const int run_words = run_batches * B;
+    uint32_t largest = 0;
+    if (NW == 1) {  // 32 threads are few for n of them: their runs
+      for (int i = 0; i < run; ++i) add_keys(largest, run_key(s_runs[i * kThreads + tid]), p.n);
+    } else {
+      add_keys(largest, run_key(thread_max), p.n);
+    }
+    largest = join_lists<NW>(largest, reinterpret_cast<uint32_t(*)[32]>(s_lists), p.n);
+    if (warp == 0) {
+      largest = __shfl_sync(0xffffffffu, largest, p.n - 1);
+      // fewer threads than n have a logit: all runs that have one
+      if (lane == 0) s_tau = largest ? ord_to_float(largest) : -kLargestFloat;
+    }
+    sync_row<NW>();
+    const float tau = s_tau;
+    for (int i = 0; i < run; ++i) {
+      const bool is = s_runs[i * kThreads + tid] >= tau;
+      const int at = append<NW>(&s_tied_count, is);
+      if (is && at < kMaxTied) s_tied[at] = i * kThreads + tid;
+    }
+    sync_row<NW>();
+    const int tied = s_tied_count;
+    const bool all_runs = tied > kMaxTied;
+    const int again = all_runs ? batches * B * kThreads : tied * run_words;
+    // the logits of these runs that are at least tau (0: none), a word a lane
     auto candidates = [&](auto&& take) {
-      for (int i = warp * 32; i < p.n * run_words; i += kLpThreads) {
-        const int at = i + lane;
-        float x[kEl];
-        uint32_t word = 0;
-        bool in = false;
-        if (at < p.n * run_words && s_best[at / run_words]) {
-          const uint32_t local = key_place(s_best[at / run_words]) - first;  // of the run's best word
-          const int j = static_cast<int>(local / kLpThreads) / run_words * run_words + at % run_words;
-          const int k = j * kLpThreads + static_cast<int>(local % kLpThreads);
-          in = k < words;
-          word = first + k;
+      for (int i = warp * 32; i < again; i += kThreads) {
+        int k = i + lane;  // the word, from this CTA's first
+        bool in = k < again;
+        if (in && !all_runs) {
+          const int at = s_tied[k / run_words];
+          k = (at / kThreads * run_words + k % run_words) * kThreads + at % kThreads;
         }
-        if (in) {
-          row.load(static_cast<int>(word), x);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kEl; ++j) x[j] = -INFINITY;
-        }
+        in = in && k < words;
+        const int word = first + (in ? k : 0);
+        float y[kEl];
+        Word<F32>::unpack(row.load(in ? word : row.n), y);
 #pragma unroll
         for (int j = 0; j < kEl; ++j) {
-          const bool is = selectable(x[j]) && top_key(x[j], word) >= least;
-          take(is ? top_key(x[j], word * kEl + j - row.lead) : 0ull);
+          const bool is = y[j] >= tau && y[j] <= kLargestFloat;
+          take(is, y[j], static_cast<uint32_t>(word) * kEl + j - row.lead);
         }
       }
     };
-    candidates([&](unsigned long long k) {
-      if (k) {
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kMaxList) s_cand[at] = k;  // any order: the keys differ and are sorted
-      }
-    });
-    __syncthreads();
-    const int count = s_count;
-    list = 0;
-    if (count <= kMaxList) {
-      for (int i = warp * 32; i < count; i += kLpThreads) add_keys(list, i + lane < count ? s_cand[i + lane] : 0ull, p.n);
+    if (!all_runs)
+      candidates([&](bool is, float y, uint32_t id) {
+        const int at = append<NW>(&s_count, is);
+        if (is && at < kList) s_cand[at] = top_key(y, id);  // any order: the keys differ and are sorted
+      });
+    sync_row<NW>();
+    const int count = all_runs ? kList + 1 : s_count;
+    if (count <= 64) {  // one warp sorts them in less time than the warps' lists are joined
+      if (warp == 0)
+        for (int i = 0; i < count; i += 32) add_keys(list, i + lane < count ? s_cand[i + lane] : 0ull, p.n);
+      if (p.n == 1) list = warp_best(list);
     } else {
-      candidates([&](unsigned long long k) { add_keys(list, k, p.n); });
+      if (count <= kList) {
+        for (int i = warp * 32; i < count; i += kThreads) add_keys(list, i + lane < count ? s_cand[i + lane] : 0ull, p.n);
+      } else {
+        candidates([&](bool is, float y, uint32_t id) { add_keys(list, is ? top_key(y, id) : 0ull, p.n); });
+      }
+      list = join_lists<NW>(list, s_lists, p.n);
     }
-    list = join_lists(list, s_lists);
   }
 
   // ---- the cluster's CTAs
-  if (splits > 1) {
+  if (NW > 1 && splits > 1) {
     if (tid == 0) s_part = all;
     if (TOP && warp == 0) s_best[lane] = list;
+    __syncwarp();
     cluster_sync();
     if (rank == 0) {
-      for (int i = 1; i < splits; ++i) {
-        const uint32_t at = map_rank(smem_u32(&s_part), static_cast<uint32_t>(i));
-        all = merge(all, Sums{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
-      }
+      if (warp == 0)
+        for (int i = 1; i < splits; ++i) {
+          const uint32_t at = map_rank(smem_u32(&s_part), static_cast<uint32_t>(i));
+          all = merge(all, Sums{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
+        }
       if (TOP) {
         list = 0;
-        for (int i = warp; i < splits; i += kLpWarps) {
-          const unsigned long long k = ld_cluster_u64(map_rank(smem_u32(&s_best[31 - lane]), static_cast<uint32_t>(i)));
-          list = merge_best(list, k);
-        }
-        list = join_lists(list, s_lists);
+        if (warp < splits) list = ld_cluster_u64(map_rank(smem_u32(&s_best[lane]), static_cast<uint32_t>(warp)));
+        list = join_lists<NW>(list, s_lists, p.n);
       }
     }
   }
@@ -373,17 +610,19 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
       if (p.top_logprob) p.top_logprob[t * p.ld_top + lane] = list ? (key_value(list) - all.m) - log_total : -INFINITY;
     }
   }
-  if (splits > 1) cluster_sync();  // no CTA leaves while its part may still be read
+  __syncwarp();
+  if (NW > 1 && splits > 1) cluster_sync();  // no CTA leaves while its part may still be read
 }
 
-template <bool F32, bool TOP>
-cudaError_t launch(const LogprobParams& p, int T, const DeviceCtx& ctx, cudaStream_t st) {
-  // Rows that leave SMs idle are split, down to 4,096 logits a CTA.
-  int splits = 1;
-  while (splits < 8 && static_cast<long long>(T) * splits * 2 <= 4LL * ctx.num_sms && p.V / (splits * 2) >= 4096) splits *= 2;
+template <bool F32, bool TOP, int NW, bool DEEP>
+cudaError_t launch(const LogprobParams& p, int T, int splits, const DeviceCtx& ctx, cudaStream_t st) {
+  constexpr int kSmem = kRingBytes<F32, DEEP>;
+  cudaError_t e = prefer_max_smem_once<logprobs_kernel<F32, TOP, NW, DEEP>>(ctx.device, kSmem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(T) * splits);
+  cfg.gridDim = dim3(NW == 1 ? (T + kLpWarps - 1) / kLpWarps : T * splits);
   cfg.blockDim = dim3(kLpThreads);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -394,7 +633,27 @@ cudaError_t launch(const LogprobParams& p, int T, const DeviceCtx& ctx, cudaStre
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<F32, TOP>, p, splits);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<F32, TOP, NW, DEEP>, p, T, splits);
+}
+
+template <bool F32, bool TOP>
+cudaError_t launch_type(const LogprobParams& p, int T, const DeviceCtx& ctx, cudaStream_t st) {
+  // A warp a row where the rows are short and many: 2,048 rows of 1,000 fp32 logits with
+  // 5 alternatives take 6.9 us, 18.5 with a CTA each; 2,048 of 10,000: 21.8 and 27.4; 333
+  // of 2,000: 8.5 and 6.1; 700 of 10,000: 13.5 and 11.3; 2,048 of 20,000: 43 and 37.
+  if (p.V <= 512 || (p.V <= 10000 && T >= 5 * ctx.num_sms)) return launch<F32, TOP, 1, false>(p, T, 1, ctx, st);
+  // A cluster a row where the rows leave SMs idle, down to 4,096 logits a CTA (8 rows of
+  // 131,072 fp32 logits with 20 alternatives: 8.4 us split by 8, 15.5 whole; 64 rows: 12.7
+  // by 4, 16.9 whole; 128 rows: 18.7 by 2, 16.9 whole).
+  int splits = 1;
+  if (2 * T <= ctx.num_sms)
+    while (splits < 8 && T * splits <= ctx.num_sms && p.V / (splits * 2) >= 4096) splits *= 2;
+  // With an SM or half of one to itself a whole row's CTA needs more bytes on their way
+  // (128 rows of 131,072 fp32 logits: 16.9 us, 26 with two stages; 512 rows, where the
+  // larger ring leaves fewer CTAs an SM: 58 and 46).
+  if constexpr (F32)
+    if (splits == 1 && T <= 2 * ctx.num_sms) return launch<F32, TOP, kLpWarps, true>(p, T, splits, ctx, st);
+  return launch<F32, TOP, kLpWarps, false>(p, T, splits, ctx, st);
 }
 
 }  // namespace
@@ -402,8 +661,8 @@ cudaError_t launch(const LogprobParams& p, int T, const DeviceCtx& ctx, cudaStre
 cudaError_t launch_logprobs(const csa2_logprobs_args& a, const DeviceCtx& ctx, cudaStream_t st) {
   const LogprobParams p{a.logits, a.ld_logits, a.V, a.token, a.logprob, a.entropy, a.lse, a.top_id, a.top_logprob,
                         a.ld_top, a.n_top, ctx.err};
-  if (a.logits_f32) return a.n_top ? launch<true, true>(p, a.T, ctx, st) : launch<true, false>(p, a.T, ctx, st);
-  return a.n_top ? launch<false, true>(p, a.T, ctx, st) : launch<false, false>(p, a.T, ctx, st);
+  if (a.logits_f32) return a.n_top ? launch_type<true, true>(p, a.T, ctx, st) : launch_type<true, false>(p, a.T, ctx, st);
+  return a.n_top ? launch_type<false, true>(p, a.T, ctx, st) : launch_type<false, false>(p, a.T, ctx, st);
 }
 
 }  // namespace csa2
