@@ -543,7 +543,8 @@ CSA2_API int csa2_add_norm_fp8(const csa2_add_norm_fp8_args* args, void* stream)
  * e4m3 output.  An infinity or NaN of one adapter stays in its own rows.
  * base: the arguments of csa2_fp8_linear, with its rules; T at most 2^20; w_ready = 1
  * says the same of a, b, adapter_scale and row_adapter as of w and w_scale.  rank is
- * a multiple of 8, at most 128; n_adapters >= 1, n_adapters * N at most 2^30.  An
+ * a multiple of 8, at most 128; n_adapters >= 1, n_adapters * N and n_adapters * rank at
+ * most 2^30.  An
  * adapter of a smaller rank is padded with zeros.  Alignment: a, b 16 B; row_adapter,
  * adapter_scale 4 B; workspace 16 B: csa2_workspace_size(CSA2_CALL_LORA_LINEAR, args,
  * &bytes), read and written until the call's work is done.  Results do not depend on

@@ -147,8 +147,10 @@ int lora_check(const csa2_lora_linear_args* a, const char* who) {
   if (a->base.T > csa2::kLoraMaxRows) return fail(CSA2_ERR_SHAPE, "%s: T=%d is above 2^20", who, a->base.T);
   if (a->rank < 8 || a->rank > 128 || (a->rank & 7))
     return fail(CSA2_ERR_SHAPE, "%s: rank=%d must be a multiple of 8 in 8..128", who, a->rank);
-  if (a->n_adapters < 1 || static_cast<long long>(a->n_adapters) * a->base.N > (1 << 30))
-    return fail(CSA2_ERR_SHAPE, "%s: n_adapters=%d must be >= 1, and n_adapters * N at most 2^30", who, a->n_adapters);
+  if (a->n_adapters < 1 || static_cast<long long>(a->n_adapters) * a->base.N > (1 << 30) ||
+      static_cast<long long>(a->n_adapters) * a->rank > (1 << 30))
+    return fail(CSA2_ERR_SHAPE, "%s: n_adapters=%d must be >= 1, and n_adapters * N and n_adapters * rank at most 2^30", who,
+                a->n_adapters);
   if (!aligned16(a->a) || !aligned16(a->b)) return fail(CSA2_ERR_ALIGN, "%s: a and b must be 16-B aligned", who);
   if (!aligned4(a->row_adapter) || !aligned4(a->adapter_scale))
     return fail(CSA2_ERR_ALIGN, "%s: row_adapter and adapter_scale must be 4-B aligned", who);

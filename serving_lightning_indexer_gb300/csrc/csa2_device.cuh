@@ -162,6 +162,15 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(const void* smem_ptr) {
   return d;
 }
 
+// The same for rows of 32, 64 or 128 bytes (swizzled within as many): groups of 8 rows
+// 8 * row bytes apart; swizzle modes 6, 4 and 2.
+__device__ __forceinline__ uint64_t smem_desc_rows(const void* smem_ptr, uint32_t row_bytes) {
+  const uint64_t mode = row_bytes == 32 ? 6 : row_bytes == 64 ? 4 : 2;
+  uint64_t d = smem_desc_sw128(smem_ptr);
+  d &= ~((0x3FFFull << 32) | (7ull << 61));
+  return d | static_cast<uint64_t>((8 * row_bytes) >> 4) << 32 | mode << 61;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f8f6f4 with e4m3 A and B, fp32
 // accumulation, both operands K-major: D format (bits 4-5) = 1 (f32), A/B
 // formats (7-9, 10-12) = 0 (e4m3), N >> 3 at bits 17-22, M >> 4 at bits 24-28.
@@ -349,6 +358,12 @@ __device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 

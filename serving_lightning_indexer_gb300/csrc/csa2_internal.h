@@ -174,7 +174,7 @@ cudaError_t launch_kv_project(const uint16_t* H, const uint16_t* W, int T, int h
 cudaError_t launch_quant_fp8(const csa2_quant_fp8_args& a, cudaStream_t st);
 // Projection on e4m3 codes with block scales.
 cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ctx, cudaStream_t st, const char** why);
-// Low-rank adapters beside it: where their inner products [2][T][rank] and the lists
+// Low-rank adapters beside it: where their inner products [2][T][pitch] and the lists
 // of adapters of each tile of tile_rows rows ([tile][tile_rows + 4]: how many, then,
 // from the fourth word on, which) are in the workspace, and the launch that writes them.
 struct LoraInner {
@@ -183,9 +183,12 @@ struct LoraInner {
   int tile_rows;
 };
 constexpr int kLoraMaxRows = 1 << 20;
+inline int lora_pitch(int rank) { return (rank + 63) / 64 * 64; }  // rows of whole 128-byte words
 size_t lora_workspace_bytes(int T, int rank);
 LoraInner lora_inner_at(const csa2_lora_linear_args& a, void* ws, int tile_rows);
-cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& to, const DeviceCtx& ctx, cudaStream_t st);
+// ctas: of the projection that follows.
+cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& to, int ctas, const DeviceCtx& ctx,
+                              cudaStream_t st, const char** why);
 cudaError_t launch_lora_linear(const csa2_lora_linear_args& a, void* ws, const DeviceCtx& ctx, cudaStream_t st,
                                const char** why);
 // The residual's addition, RMSNorm and e4m3 codes.

@@ -16,6 +16,8 @@
 #include <cuda_bf16.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "csa2_device.cuh"
 #include "csa2_e4m3.cuh"
 #include "csa2_internal.h"
@@ -50,13 +52,88 @@ template <bool LORA>
 struct LoraParams {};
 template <>
 struct LoraParams<true> {
-  CUtensorMap map_v, map_b;  // inner products [2 T, rank], b [adapters N, rank]: 64 ranks by a tile's rows or columns
+  CUtensorMap map_v, map_b;  // inner products [2 T, pitch], b [adapters N, rank]: row_bytes by a tile's rows or columns
+  const uint16_t* b;
   const int* row_adapter;
   const int* lists;
   int list_stride;
+  int rank;
+  int row_bytes;  // of a block of b in shared memory: 128, or 32 or 64 for all of rank 16 or 32
   int pieces;  // blocks of an adapter: 64 ranks each, times planes of v
   int planes;
 };
+// Block i of a tile's adapters: the adapter, where its ranks start, how many there are,
+// and where its plane of v starts.
+struct LoraBlock {
+  int adapter, rank0, ranks, v_row;
+  __device__ __forceinline__ LoraBlock(const LoraParams<true>& lo, const int* list, int i, int T) {
+    const int j = i / lo.pieces, k = i - j * lo.pieces;
+    adapter = list[4 + j];
+    rank0 = k / lo.planes * 64;
+    ranks = min(64, lo.rank - rank0);
+    v_row = k % lo.planes * T;
+  }
+  __device__ __forceinline__ int steps() const { return (ranks + 15) >> 4; }  // products of 16 ranks
+};
+// The b of a block by plain copies, into the swizzled rows of 128 bytes that tensor copies
+// write, by a whole warp: for runs of ranks that are not a row of 32, 64 or 128 bytes.  A
+// tensor copy of 128-byte rows that end before costs more (64 x 2,048 x 32,768 with 8
+// adapters of rank 8: 43 us, 28 so).  8 ranks without a partner are joined by 8 zeros.
+__device__ __forceinline__ void copy_b_rows(uint8_t* dst, const LoraParams<true>& lo, const LoraBlock& at, int n0, int rows, int N) {
+  const int lane = threadIdx.x & 31;
+  const int words = at.ranks >> 3, all = at.steps() * 2;  // 16-byte words of a row: b's, and with the zeros
+  const int n = min(rows, N - n0);
+  const uint16_t* src = lo.b + (static_cast<long long>(at.adapter) * N + n0) * lo.rank + at.rank0;
+  // lanes of a row side by side; `all` is 2, 4, 6 or 8
+  const int per = all == 6 ? 8 : all, q = lane % per, step = 32 / per;
+  if (q < all)
+    for (int r = lane / per; r < n; r += step)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * 128 + ((q ^ (r & 7)) * 16))),
+                   "l"(src + static_cast<long long>(r) * lo.rank + min(q, words - 1) * 8), "r"(q < words ? 16 : 0)
+                   : "memory");
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// A producing warp's blocks: v by a tensor copy, b by one or, row by row, by plain copies.
+// A stage's barrier takes two arrivals, one with the tensor copies' bytes, one for b.  Plain
+// copies are waited for when those of two more blocks are on their way: with three, all of
+// the ring's stages would be taken before a block's products begin.
+struct LoraCopies {
+  uint64_t* pending[2];  // the barriers of the blocks whose plain copies are on their way, oldest first
+  int count = 0;
+  __device__ __forceinline__ void flush() {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    while (count) arrive();
+  }
+  __device__ __forceinline__ void add(uint8_t* v_dst, uint8_t* b_dst, uint64_t* full, const LoraParams<true>& lo,
+                                      const LoraBlock& at, int t0, int n0, int v_rows, int b_rows, int N, uint64_t policy) {
+    const bool plain = at.ranks * 2 != lo.row_bytes;
+    if ((threadIdx.x & 31) == 0) {
+      mbar_arrive_expect_tx(full, v_rows * kBlockK + (plain ? 0 : b_rows * lo.row_bytes));
+      tma_load_2d(v_dst, &lo.map_v, at.rank0 * 2, at.v_row + t0, full, policy);
+      if (!plain) {
+        tma_load_2d(b_dst, &lo.map_b, at.rank0 * 2, at.adapter * N + n0, full, policy);
+        mbar_arrive(full);
+      }
+    }
+    if (!plain) return;
+    copy_b_rows(b_dst, lo, at, n0, b_rows, N);
+    if (count == 2) {
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      arrive();
+    }
+    pending[count++] = full;
+  }
+
+ private:
+  __device__ __forceinline__ void arrive() {  // the oldest block's plain copies are done
+    fence_proxy_async_smem();                 // each lane's, before the tensor core reads them
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(pending[0]);
+    pending[0] = pending[1];
+    --count;
+  }
+};
+
 // What a launch has to know of its adapters on the host.
 struct NoLora {
   static constexpr bool kOn = false;
@@ -66,17 +143,6 @@ struct WithLora {
   const csa2_lora_linear_args* args;
   void* workspace;
 };
-// Block i of a tile's adapters: the adapter, and where its ranks and its plane of v start.
-struct LoraBlock {
-  int adapter, rank_byte, v_row;
-  __device__ __forceinline__ LoraBlock(const LoraParams<true>& lo, const int* list, int i, int T) {
-    const int j = i / lo.pieces, k = i - j * lo.pieces;
-    adapter = list[4 + j];
-    rank_byte = k / lo.planes * 128;
-    v_row = k % lo.planes * T;
-  }
-};
-
 // ---------------------------------------------------------------- many rows
 // A CTA walks output tiles of 128 rows x 256 columns (persistent grid, the tiles of
 // one column block behind each other so that its weights stay in L2).  Warps 0..7
@@ -85,7 +151,7 @@ struct LoraBlock {
 // 256 because an instruction costs 137 cycles there and 92 at N = 128.  A block
 // takes about 830 cycles: product and commit 566, sums 480, joined by four waits,
 // with two accumulators to overlap them.
-template <int BN>
+template <int BN, bool LORA>
 struct WideCfg {
   static constexpr int kStages = 4;
   static constexpr int kStageBytes = (kTileM + BN) * kBlockK;
@@ -96,7 +162,10 @@ struct WideCfg {
   static constexpr int kScaleBytes = 4 * (kTileM + 2) * 4;  // per block: the rows', the halves'
   static constexpr int kOffScales = kOffOut + kAccWarps * 2048;
   static constexpr int kOffBars = kOffScales + kScaleSlots * kScaleBytes;
-  static constexpr int kSmem = 1024 + kOffBars + 256;
+  // LORA: of two tiles, how many blocks their adapters have, the adapters, the rows' own
+  static constexpr int kOffLists = kOffBars + 256;
+  static constexpr int kListWords = 4 + 2 * kTileM;
+  static constexpr int kSmem = 1024 + kOffLists + (LORA ? 2 * kListWords * 4 : 0);
 };
 
 // mbar_wait with the first look in line: half the time (46 against 92 cycles) where
@@ -174,14 +243,39 @@ struct Share {
   __device__ __forceinline__ int column(long long tile) const { return static_cast<int>(tile / m_tiles) * BN; }
 };
 
+// The adapters' blocks of a tile.  The lists are there when the previous launch is done,
+// which is waited for behind the first tile's other blocks; later tiles' counts are asked
+// for ahead of theirs.
+template <bool SPLIT>
+struct TileAdapters {
+  const LoraParams<true>& lo;
+  const Share<256, SPLIT>& mine;
+  const int* list;
+  int count;
+  __device__ __forceinline__ TileAdapters(const LoraParams<true>& lo, const Share<256, SPLIT>& mine) : lo(lo), mine(mine) {}
+  __device__ __forceinline__ void look(long long tile) {
+    list = lo.lists + static_cast<long long>(mine.row(tile) / kTileM) * lo.list_stride;
+    if (tile != mine.first) count = list[0];
+  }
+  __device__ __forceinline__ int blocks(long long tile) {
+    if (tile == mine.first) {
+      pdl_wait();
+      count = list[0];
+    }
+    return mine.adapters_too() ? count * lo.pieces : 0;
+  }
+  __device__ __forceinline__ LoraBlock at(int i, int T) const { return LoraBlock(lo, list, i, T); }
+};
+
 // The accumulation warps' part: sums each tile in registers and writes it.
 // False when a wait gave up (the same in a warp's lanes).
 template <int BN, int OUT, bool SPLIT, bool LORA>
 __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out, const LinearParams& p,
                                                      const LoraParams<LORA>& lo, uint8_t* smem,
                                                      uint32_t tmem, uint64_t* tfull, uint64_t* tempty, uint64_t* empty,
-                                                     uint64_t* sfull, uint64_t* sempty, volatile int* s_abort) {
-  using Cfg = WideCfg<BN>;
+                                                     uint64_t* sfull, uint64_t* sempty, uint64_t* lfull, uint64_t* lempty,
+                                                     volatile int* s_abort) {
+  using Cfg = WideCfg<BN, LORA>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAccs, C = Cfg::kCols, SS = Cfg::kScaleSlots;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = warp >> 2;            // columns half * C .. of the tile
@@ -193,6 +287,7 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
   const uint32_t row_scales = smem_u32(smem) + Cfg::kOffScales + r * 4;
   const uint32_t half_scales = smem_u32(smem) + Cfg::kOffScales + (kTileM + half) * 4;
   uint32_t it = 0, g = 0;  // blocks and groups of four blocks so far
+  uint32_t n_tile = 0;     // tiles so far, LORA only
   for (long long tile = mine.first; tile < mine.tiles; tile += mine.step) {
     const int n0 = mine.column(tile) + half * C, t0 = mine.row(tile);
     const int row = t0 + r;
@@ -235,20 +330,29 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
       if ((b & 3) == 3 || b + 1 == blocks) ++g;
     }
     if constexpr (LORA) {
-      if (tile == mine.first) {
-        pdl_wait();
-        pdl_trigger();  // every CTA holds its TMEM
-      }
-      const int* list = lo.lists + static_cast<long long>(t0 / kTileM) * lo.list_stride;
-      const int extra = mine.adapters_too() ? list[0] * lo.pieces : 0;
-      const int own = extra > 0 && row < p.T ? __ldg(lo.row_adapter + row) : -1;
+      // from shared memory: what is held through the loop above costs it its registers
+      // (4,096 x 2,048 x 32,768 without an adapter: 290 us, 24x so)
+      const int* list = reinterpret_cast<const int*>(smem + Cfg::kOffLists) + (n_tile & 1) * Cfg::kListWords;
+      if (!__all_sync(0xffffffffu, wait(&lfull[n_tile & 1], (n_tile >> 1) & 1, s_abort))) return false;
+      const int extra = list[0], own = list[4 + kTileM + r];
 #pragma unroll 1
-      for (int i = 0; i < extra; ++i, ++it) {
-        const bool add = LoraBlock(lo, list, i, p.T).adapter == own;
+      for (int i = 0, j = 0, k = 0; i < extra; ++i, ++it) {
+        const bool add = list[4 + j] == own;
+        const uint32_t adds = __ballot_sync(0xffffffffu, add);
+        if (++k == lo.pieces) {
+          k = 0;
+          ++j;
+        }
         if (!__all_sync(0xffffffffu, wait(&tfull[it % NA], (it / NA) & 1, s_abort))) return false;
         tc_fence_after();
         if (warp == 0 && lane == 0) mbar_arrive(&empty[it % S]);
         const uint32_t ta = taddr + (it % NA) * BN;
+        if (adds == 0) {  // none of the warp's rows
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[it % NA]);
+          continue;
+        }
 #pragma unroll
         for (int c = 0; c < C / 16; ++c) {
           uint32_t v[16];
@@ -261,10 +365,18 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
           }
           if (add) {  // another row's products are left alone, whatever they are
 #pragma unroll
-            for (int k = 0; k < 16; ++k) y[c * 16 + k] += __uint_as_float(v[k]);
+            for (int k = 0; k < 16; k += 2) {
+              const float2 sum = unpack_f32x2(add_f32x2(pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                                                        pack_f32x2(y[c * 16 + k], y[c * 16 + k + 1])));
+              y[c * 16 + k] = sum.x;
+              y[c * 16 + k + 1] = sum.y;
+            }
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&lempty[n_tile & 1]);
+      ++n_tile;
     }
     if (SPLIT) {
       // Rank 0 finishes the left half of the columns, rank 1 the right one: the
@@ -354,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fp8_linear_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p,
                            const __grid_constant__ LoraParams<LORA> lo) {
-  using Cfg = WideCfg<BN>;
+  using Cfg = WideCfg<BN, LORA>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAccs, C = Cfg::kCols, SS = Cfg::kScaleSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -364,14 +476,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tempty = tfull + NA;
   uint64_t* sfull = tempty + NA;
   uint64_t* sempty = sfull + SS;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sempty + SS);
+  uint64_t* lfull = sempty + SS;  // LORA: the lists of two tiles
+  uint64_t* lempty = lfull + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(lempty + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     *s_abort = 0;
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], LORA ? 2 : 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < NA; ++i) {
@@ -381,6 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < SS; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&sempty[i], kAccWarps);
+    }
+    for (int i = 0; i < (LORA ? 2 : 0); ++i) {
+      mbar_init(&lfull[i], 1);
+      mbar_init(&lempty[i], kAccWarps);
     }
     fence_mbar_init();
     prefetch_tmap(&map_x);
@@ -403,12 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kAccWarps) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t keep = l2_policy_evict_last();
-      long long it = 0;
-      bool ok = true;
-      for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
-        const int n0 = mine.column(tile), t0 = mine.row(tile);
+    const uint64_t keep = l2_policy_evict_last();
+    long long it = 0;
+    bool ok = true;
+    for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
+      const int n0 = mine.column(tile), t0 = mine.row(tile);
+      if (lane == 0) {
         for (int b = 0; b < blocks; ++b, ++it) {
           const int s = static_cast<int>(it % S);
           if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
@@ -416,23 +534,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
           tma_load_2d(dst, &map_x, (mine.b0 + b) * kBlockK, t0, &full[s], keep);
           tma_load_2d(dst + kTileM * kBlockK, &map_w, (mine.b0 + b) * kBlockK, n0, &full[s], keep);
-        }
-        if constexpr (LORA) {
-          if (!ok) break;
-          if (tile == mine.first) pdl_wait();
-          const int* list = lo.lists + static_cast<long long>(t0 / kTileM) * lo.list_stride;
-          const int extra = mine.adapters_too() ? list[0] * lo.pieces : 0;
-          for (int i = 0; i < extra; ++i, ++it) {
-            const LoraBlock at(lo, list, i, p.T);
-            const int s = static_cast<int>(it % S);
-            if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
-            uint8_t* dst = smem + s * Cfg::kStageBytes;
-            mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
-            tma_load_2d(dst, &lo.map_v, at.rank_byte, at.v_row + t0, &full[s], keep);
-            tma_load_2d(dst + kTileM * kBlockK, &lo.map_b, at.rank_byte, at.adapter * p.N + n0, &full[s], keep);
-          }
+          if (LORA) mbar_arrive(&full[s]);
         }
       }
+      if constexpr (LORA) {  // the adapters' blocks, by the whole warp
+        it = __shfl_sync(0xffffffffu, it, 0);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        TileAdapters<SPLIT> adapters(lo, mine);
+        adapters.look(tile);
+        const int extra = adapters.blocks(tile);
+        LoraCopies copies;
+        for (int i = 0; i < extra; ++i) {
+          const LoraBlock at = adapters.at(i, p.T);
+          const int s = static_cast<int>(it % S);
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort)))) break;
+          uint8_t* dst = smem + s * Cfg::kStageBytes;
+          copies.add(dst, dst + kTileM * kBlockK, &full[s], lo, at, t0, n0, kTileM, BN, p.N, keep);
+          ++it;
+        }
+        copies.flush();
+      }
+    }
+    if (lane == 0) {
       if (!ok) {
         *s_abort = 1;
         set_error(p.err, kErrTimeout);
@@ -454,45 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d = tmem + a * BN;
       uint32_t s = a, phase = 0, a_phase = 1;
       bool ok = true;
-      if constexpr (LORA) {
-        constexpr uint32_t idesc_b = idesc_bf16_f32(kTileM, BN, 0, 0);
-        long long it = 0;
-        // the products of the tile's next n blocks, those that are this accumulator's
-        auto issue = [&](int n, bool adapters) {
-          for (int b = 0; b < n && ok; ++b) {
-            const long long i = it++;
-            if (i % NA != a) continue;
-            s = static_cast<uint32_t>(i % S);
-            if (!(ok = wait(&full[s], static_cast<uint32_t>(i / S) & 1u, s_abort))) break;
-            if (!(ok = wait(&tempty[a], a_phase, s_abort))) break;
-            tc_fence_after();
-            const uint64_t ad = x_desc + s * kStageDesc, bd = w_desc + s * kStageDesc;
-            if (!adapters) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_e4m3(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) umma_bf16(d, ad + 2 * k, bd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
-            }
-            mma_commit(&tfull[a]);
-            a_phase ^= 1;
-          }
-        };
-        for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
-          issue(blocks, false);
-          if (tile == mine.first) pdl_wait();
-          const int* list = lo.lists + static_cast<long long>(mine.row(tile) / kTileM) * lo.list_stride;
-          if (mine.adapters_too()) issue(list[0] * lo.pieces, true);
-        }
-      }
-      for (long long i = LORA ? all : a; i < all; i += NA) {
-        if (!(ok = wait(&full[s], phase, s_abort))) break;
+      // this accumulator's next product: `issue` makes it
+      auto block = [&](auto&& issue) {
+        if (!wait(&full[s], phase, s_abort)) return false;
         const uint64_t ad = x_desc + s * kStageDesc, bd = w_desc + s * kStageDesc;
-        if (!(ok = wait(&tempty[a], a_phase, s_abort))) break;
+        if (!wait(&tempty[a], a_phase, s_abort)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)  // 32 B of the swizzled rows a step
-          mma_e4m3(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+        issue(ad, bd);
         mma_commit(&tfull[a]);
         a_phase ^= 1;
         s += NA;
@@ -500,6 +592,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           s -= S;
           phase ^= 1;
         }
+        return true;
+      };
+      auto codes = [&](uint64_t ad, uint64_t bd) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // 32 B of the swizzled rows a step
+          mma_e4m3(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+      };
+      if constexpr (LORA) {
+        constexpr uint32_t idesc_b = idesc_bf16_f32(kTileM, BN, 0, 0);
+        int next = a;  // blocks until this accumulator's next one
+        TileAdapters<SPLIT> adapters(lo, mine);
+        const uint64_t b_desc = smem_desc_rows(smem + kTileM * kBlockK, lo.row_bytes);
+        for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
+          adapters.look(tile);
+          for (; next < blocks && ok; next += NA) ok = block(codes);
+          next -= blocks;
+          const int extra = adapters.blocks(tile);
+          for (; next < extra && ok; next += NA) {
+            const int steps = adapters.at(next, p.T).steps();
+            ok = block([&](uint64_t ad, uint64_t) {
+              const uint64_t bd = b_desc + s * kStageDesc;
+              for (int k = 0; k < steps; ++k) umma_bf16(d, ad + 2 * k, bd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
+            });
+          }
+          next -= extra;
+        }
+      } else {
+        for (long long i = a; i < all && ok; i += NA) ok = block(codes);
       }
       if (!ok) {
         *s_abort = 1;
@@ -513,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Four blocks' at a time into shared memory: a load of an accumulation warp would
     // be waited for at its next barrier arrival.
     long long g = 0;
+    uint32_t n_tile = 0;
     bool ok = true;
     for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
       const int n0 = mine.column(tile), t0 = mine.row(tile);
@@ -543,6 +664,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sfull[s]);
       }
+      if constexpr (LORA) {  // the tile's adapters and its rows', behind its last scales
+        if (!ok) break;
+        if (tile == mine.first) {
+          pdl_wait();
+          pdl_trigger();  // every CTA holds its TMEM
+        }
+        const int slot = static_cast<int>(n_tile & 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(&lempty[slot], static_cast<uint32_t>((n_tile >> 1) & 1) ^ 1u, s_abort));
+        if (!ok) break;
+        ++n_tile;
+        int* dst = reinterpret_cast<int*>(smem + Cfg::kOffLists) + slot * Cfg::kListWords;
+        const int* src = lo.lists + static_cast<long long>(t0 / kTileM) * lo.list_stride;
+        const int count = mine.adapters_too() ? src[0] : 0;
+        if (lane == 0) dst[0] = count * lo.pieces;
+#pragma unroll
+        for (int i = lane; i < kTileM; i += 32) {
+          if (i < count) dst[4 + i] = src[4 + i];
+          // a row without an adapter has none of the list's
+          dst[4 + kTileM + i] = t0 + i < p.T ? __ldg(lo.row_adapter + t0 + i) : -1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&lfull[slot]);
+      }
     }
     if (!ok) {
       *s_abort = 1;
@@ -550,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     if (!accumulate_and_store<BN, OUT, SPLIT, LORA>(map_out, p, lo, smem, tmem, tfull, tempty, empty, sfull, sempty,
-                                                    s_abort)) {
+                                                    lfull, lempty, s_abort)) {
       *s_abort = 1;
       set_error(p.err, kErrTimeout);
       if (lane == 0) bulk_wait_all();  // the last tile's output still leaves shared memory
@@ -581,25 +725,32 @@ long long wide_tiles(const csa2_fp8_linear_args& a) {
 
 // With adapters: their inner products and lists are launched first, for tiles of
 // `rows` rows and `columns` columns, and described to the projection.  Nothing without.
-cudaError_t prepare_lora(const NoLora&, LoraParams<false>*, int, int, const DeviceCtx&, cudaStream_t, const char**) {
+cudaError_t prepare_lora(const NoLora&, LoraParams<false>*, int, int, long long, const DeviceCtx&, cudaStream_t, const char**) {
   return cudaSuccess;
 }
-cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int columns, const DeviceCtx& ctx, cudaStream_t st,
-                         const char** why) {
+cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int columns, long long ctas, const DeviceCtx& ctx,
+                         cudaStream_t st, const char** why) {
   const csa2_lora_linear_args& a = *l.args;
   const LoraInner to = lora_inner_at(a, l.workspace, rows);
+  lo->b = a.b;
+  lo->rank = a.rank;
   lo->row_adapter = a.row_adapter;
   lo->lists = to.lists;
   lo->list_stride = rows + 4;
   lo->planes = a.base.out_format == CSA2_OUT_BF16 ? 1 : 2;
   lo->pieces = (a.rank + 63) / 64 * lo->planes;
   const uint64_t row = 2 * static_cast<uint64_t>(a.rank);
-  if (encode_tmap_2d_u8(&lo->map_v, to.v, row, 2 * static_cast<uint64_t>(a.base.T), row, 128, rows) != CUDA_SUCCESS ||
-      encode_tmap_2d_u8(&lo->map_b, a.b, row, static_cast<uint64_t>(a.n_adapters) * a.base.N, row, 128, columns) != CUDA_SUCCESS) {
+  lo->row_bytes = a.rank == 16 || a.rank == 32 ? static_cast<int>(row) : 128;
+  const uint64_t v_row = 2 * static_cast<uint64_t>(lora_pitch(a.rank));
+  if (encode_tmap_2d_u8(&lo->map_v, to.v, v_row, 2 * static_cast<uint64_t>(a.base.T), v_row, 128, rows) != CUDA_SUCCESS ||
+      encode_tmap_2d_u8(&lo->map_b, a.b, row, static_cast<uint64_t>(a.n_adapters) * a.base.N, row, lo->row_bytes, columns,
+                        lo->row_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                        : lo->row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                              : CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS) {
     *why = "csa2_lora_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
   }
-  return launch_lora_inner(a, to, ctx, st);
+  return launch_lora_inner(a, to, static_cast<int>(ctas < ctx.num_sms ? ctas : ctx.num_sms), ctx, st, why);
 }
 
 template <int BN, int OUT, bool SPLIT, class L>
@@ -614,16 +765,16 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
     return cudaErrorInvalidValue;
   }
   auto kern = fp8_linear_wide_kernel<BN, OUT, SPLIT, L::kOn>;
-  cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT, SPLIT, L::kOn>>(ctx.device, WideCfg<BN>::kSmem);
+  cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT, SPLIT, L::kOn>>(ctx.device, WideCfg<BN, L::kOn>::kSmem);
   if (e != cudaSuccess) return e;
   LoraParams<L::kOn> lo;
-  e = prepare_lora(lora, &lo, kTileM, BN, ctx, st, why);
+  e = prepare_lora(lora, &lo, kTileM, BN, SPLIT ? 2 * wide_tiles<BN>(a) : wide_tiles<BN>(a), ctx, st, why);
   if (e != cudaSuccess) return e;
   const long long tiles = wide_tiles<BN>(a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? 2 * tiles : (tiles < ctx.num_sms ? tiles : ctx.num_sms)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = WideCfg<BN>::kSmem;
+  cfg.dynamicSmemBytes = WideCfg<BN, L::kOn>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -686,7 +837,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   if (threadIdx.x == 0) {
     *s_abort = 0;
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], LORA ? 2 : 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < NA; ++i) {
@@ -699,6 +850,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     if (LORA || p.w_ready) {  // the first weights do not wait for the previous launch
       for (int b = 0; b < min(S, blocks); ++b) {
         mbar_arrive_expect_tx(&full[b], Cfg::kStageBytes);
+        if (LORA) mbar_arrive(&full[b]);
         tma_load_2d(smem + b * Cfg::kStageBytes, &map_w, (b0 + b) * kBlockK, n0, &full[b], pol_w);
       }
     }
@@ -719,31 +871,41 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   bool ok = true;
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    int b = 0;
     if (lane == 0) {
-      int b = 0;
       for (; b < blocks; ++b) {
         const int s = b % S;
         if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
         uint8_t* dst = smem + s * Cfg::kStageBytes;
         if (b >= S || !(LORA || p.w_ready)) {
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+          if (LORA) mbar_arrive(&full[s]);
           tma_load_2d(dst, &map_w, (b0 + b) * kBlockK, n0, &full[s], pol_w);
         }
         tma_load_2d(dst + 128 * kBlockK, &map_x, (b0 + b) * kBlockK, t0, &full[s], pol_x);
       }
-      if constexpr (LORA) {
-        if (ok) pdl_wait();
+    }
+    if constexpr (LORA) {  // the adapters' blocks, by the whole warp
+      b = __shfl_sync(0xffffffffu, b, 0);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok) {
+        pdl_wait();
         const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
-        for (int i = rank; ok && i < list[0] * lo.pieces; i += splits, ++b) {
+        const int extra = list[0] * lo.pieces;
+        LoraCopies copies;
+        for (int i = rank; i < extra; i += splits, ++b) {
           const LoraBlock at(lo, list, i, p.T);
           const int s = b % S;
-          if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
+          if (b >= S &&
+              !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))))
+            break;
           uint8_t* dst = smem + s * Cfg::kStageBytes;
-          mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
-          tma_load_2d(dst, &lo.map_b, at.rank_byte, at.adapter * p.N + n0, &full[s], pol_x);
-          tma_load_2d(dst + 128 * kBlockK, &lo.map_v, at.rank_byte, at.v_row + t0, &full[s], pol_x);
+          copies.add(dst + 128 * kBlockK, dst, &full[s], lo, at, t0, n0, NT, 128, p.N, pol_x);
         }
+        copies.flush();
       }
+    }
+    if (lane == 0) {
       if (!ok) {
         *s_abort = 1;
         set_error(p.err, kErrTimeout);
@@ -754,34 +916,35 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(128, NT), idesc_b = idesc_bf16_f32(128, NT, 0, 0);
+      constexpr uint32_t idesc = idesc_e4m3_f32(128, NT);
       int b = 0;
-      int end = blocks;
-      for (bool adapters = false;; adapters = true) {
-        for (; b < end; ++b) {
-          const int s = b % S, a = b % NA;
-          if (!(ok = mbar_wait(&full[s], static_cast<uint32_t>(b / S) & 1u, s_abort))) break;
-          if (b >= NA && !(ok = mbar_wait(&tempty[a], static_cast<uint32_t>(b / NA - 1) & 1u, s_abort))) break;
-          tc_fence_after();
-          const uint64_t wd = smem_desc_sw128(smem + s * Cfg::kStageBytes);
-          const uint64_t xd = smem_desc_sw128(smem + s * Cfg::kStageBytes + 128 * kBlockK);
-          if (!LORA || !adapters) {
+      auto block = [&](auto&& issue) {  // block b's products: `issue` makes them
+        const int s = b % S, a = b % NA;
+        if (!mbar_wait(&full[s], static_cast<uint32_t>(b / S) & 1u, s_abort)) return false;
+        if (b >= NA && !mbar_wait(&tempty[a], static_cast<uint32_t>(b / NA - 1) & 1u, s_abort)) return false;
+        tc_fence_after();
+        issue(tmem + a * NT, smem_desc_sw128(smem + s * Cfg::kStageBytes),
+              smem_desc_sw128(smem + s * Cfg::kStageBytes + 128 * kBlockK));
+        mma_commit(&tfull[a]);
+        ++b;
+        return true;
+      };
+      while (b < blocks && ok)
+        ok = block([&](uint32_t d, uint64_t wd, uint64_t xd) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_e4m3(tmem + a * NT, wd + 2 * k, xd + 2 * k, idesc, k > 0 ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(tmem + a * NT, wd + 2 * k, xd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
-          }
-          mma_commit(&tfull[a]);
+          for (int k = 0; k < 4; ++k) mma_e4m3(d, wd + 2 * k, xd + 2 * k, idesc, k > 0 ? 1u : 0u);
+        });
+      if constexpr (LORA) {
+        constexpr uint32_t idesc_b = idesc_bf16_f32(128, NT, 0, 0);
+        if (ok) pdl_wait();
+        const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
+        for (int i = rank; ok && i < list[0] * lo.pieces; i += splits) {
+          const int steps = LoraBlock(lo, list, i, p.T).steps();
+          ok = block([&](uint32_t d, uint64_t, uint64_t xd) {
+            const uint64_t wd = smem_desc_rows(smem + (b % S) * Cfg::kStageBytes, lo.row_bytes);
+            for (int k = 0; k < steps; ++k) umma_bf16(d, wd + 2 * k, xd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
+          });
         }
-        if constexpr (LORA) {
-          if (ok && !adapters) {
-            pdl_wait();
-            end = blocks + shares_of(lo.lists[static_cast<long long>(blockIdx.y) * lo.list_stride] * lo.pieces, rank, splits);
-            continue;
-          }
-        }
-        break;
       }
       if (!ok) {
         *s_abort = 1;
@@ -1061,7 +1224,7 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
     return cudaErrorInvalidValue;
   }
   LoraParams<L::kOn> lo;
-  e = prepare_lora(lora, &lo, NT, 128, ctx, st, why);
+  e = prepare_lora(lora, &lo, NT, 128, tiles * splits, ctx, st, why);
   if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, p, lo);
 }

@@ -8,8 +8,10 @@
 // result is written as the bf16 nearest to it and, for outputs that can tell (fp32,
 // and the fp32 scales of e4m3), the bf16 nearest to what that leaves: 2^-17 together.
 //
-// A CTA takes 16 rows, one of the adapters among them and 8 of its ranks; its 16
-// warps take the blocks of 128 input dims in turn and are added in warp order.
+// Two kernels.  Up to 16 rows: a CTA takes one of their adapters and 8 of its ranks, its
+// 16 warps the blocks of 128 input dims in turn, added in warp order.  More rows: a CTA
+// takes 128 of them, 64 ranks and a share of the input dims, and goes through the tile's
+// adapters with a in a ring in shared memory; a cluster adds the shares in rank order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -19,7 +21,6 @@
 namespace csa2 {
 namespace {
 
-constexpr int kInnerWarps = 16;
 
 struct InnerParams {
   const uint8_t* x;
@@ -27,10 +28,10 @@ struct InnerParams {
   const uint16_t* a;
   const float* adapter_scale;
   const int* row_adapter;
-  uint16_t* v;  // [2][T][rank]: the bf16 values, and what they leave
+  uint16_t* v;  // [2][T][pitch]: the bf16 values, and what they leave
   int* lists;
   long long ld_x, ld_xs;
-  int T, K, rank, n_adapters;
+  int T, K, rank, pitch, n_adapters;
   int tile_rows;  // rows of the projection's tiles
   int low;        // the second plane is wanted
   int ready;      // a and row_adapter may be read before the previous launch completes
@@ -68,8 +69,15 @@ __device__ __forceinline__ void write_list(const InnerParams& p, long long t0, i
   }
   if (i < n) s_id[i] = id;
   __syncthreads();
-  bool first = id >= 0;
-  for (int j = 0; j < i && j < n; ++j) first = first && s_id[j] != id;
+  // the first of its warp with this adapter, and none of an earlier warp has it
+  const uint32_t same = __match_any_sync(0xffffffffu, id);
+  bool first = id >= 0 && __ffs(same) - 1 == lane;
+  const int before = min(i & ~31, n);
+#pragma unroll 8
+  for (int j = 0; j < before; j += 4) {
+    const int4 v = *reinterpret_cast<const int4*>(s_id + j);
+    first = first & (v.x != id) & (v.y != id) & (v.z != id) & (v.w != id);
+  }
   const uint32_t mask = __ballot_sync(0xffffffffu, first);
   if (lane == 0) s_base[i >> 5] = __popc(mask);
   __syncthreads();
@@ -80,9 +88,42 @@ __device__ __forceinline__ void write_list(const InnerParams& p, long long t0, i
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kInnerWarps * 32) lora_inner_kernel(const __grid_constant__ InnerParams p) {
-  __shared__ float part[kInnerWarps][16][8];
-  __shared__ int s_id[128], s_base[kInnerWarps];
+// Writes v of a row and rank.
+__device__ __forceinline__ void store_v(const InnerParams& p, long long row, int rank, float v) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  const long long at = row * p.pitch + rank;
+  p.v[at] = *reinterpret_cast<const uint16_t*>(&hi);
+  if (p.low) {
+    // an infinite or NaN value is all in the first plane
+    const float rest = v - __bfloat162float(hi);
+    const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+    p.v[at + static_cast<long long>(p.T) * p.pitch] = *reinterpret_cast<const uint16_t*>(&lo);
+  }
+}
+
+// The same of four ranks from a multiple of four on.
+__device__ __forceinline__ void store_v4(const InnerParams& p, long long row, int rank, const float (&v)[4]) {
+  uint32_t hi[2], lo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
+    const float2 f = __bfloat1622float2(a);
+    const float x = v[2 * h] - f.x, y = v[2 * h + 1] - f.y;
+    const __nv_bfloat162 b = __floats2bfloat162_rn(isfinite(x) ? x : 0.f, isfinite(y) ? y : 0.f);
+    hi[h] = *reinterpret_cast<const uint32_t*>(&a);
+    lo[h] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  const long long at = row * p.pitch + rank;
+  *reinterpret_cast<uint2*>(p.v + at) = make_uint2(hi[0], hi[1]);
+  if (p.low) *reinterpret_cast<uint2*>(p.v + at + static_cast<long long>(p.T) * p.pitch) = make_uint2(lo[0], lo[1]);
+}
+
+// W warps: 16, or 32 where there are more than 16 blocks of input dims.
+template <int W>
+__global__ void __launch_bounds__(W * 32) lora_inner_kernel(const __grid_constant__ InnerParams p) {
+  __shared__ float part[W][16][8];
+  __shared__ __align__(16) int s_id[128];
+  __shared__ int s_base[W];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (!p.ready) pdl_wait();
   const int t0 = blockIdx.x * 16;
@@ -94,29 +135,51 @@ __global__ void __launch_bounds__(kInnerWarps * 32) lora_inner_kernel(const __gr
   uint32_t firsts = __ballot_sync(0xffffffffu, id >= 0 && __ffs(same) - 1 == lane);
   for (int j = blockIdx.z; j > 0; --j) firsts &= firsts - 1;
   const int adapter = __shfl_sync(0xffffffffu, id, firsts ? __ffs(firsts) - 1 : 0);
-  if (p.ready) pdl_wait();
-  pdl_trigger();
-  if (blockIdx.y == 0 && blockIdx.z == 0 && t0 % p.tile_rows == 0)
+  if (!p.ready) pdl_trigger();
+  if (blockIdx.y == 0 && blockIdx.z == 0 && t0 % p.tile_rows == 0) {
+    if (p.ready) {  // the last call's projection may still read its lists
+      pdl_wait();
+      pdl_trigger();
+    }
     write_list(p, t0, p.tile_rows, p.lists + static_cast<long long>(t0 / p.tile_rows) * (p.tile_rows + 4), s_id, s_base);
-  if (!firsts) return;
+  }
+  if (!firsts) {
+    if (p.ready) {
+      pdl_wait();
+      pdl_trigger();
+    }
+    return;
+  }
 
   const int g = lane >> 2, q = lane & 3, r0 = blockIdx.y * 8;
-  const int blocks = (p.K + 127) / 128;
+  const int blocks = r0 < p.rank ? (p.K + 127) / 128 : 0;
   const uint16_t* a = p.a + (static_cast<long long>(adapter) * p.rank + r0 + g) * p.K + q * 8;
   const int ra = min(t0 + g, p.T - 1), rb = min(t0 + g + 8, p.T - 1);
   const uint8_t* xa = p.x + ra * p.ld_x + q * 8;
   const uint8_t* xb = p.x + rb * p.ld_x + q * 8;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int b = warp; b < blocks; b += kInnerWarps) {
-    // The order of the products of a block is free: a lane holds 8 dims in a row of
-    // each 32, which the fragments of two steps take as their four pairs.
-    uint4 av[4];
+  // The order of the products of a block is free: a lane holds 8 dims in a row of each
+  // 32, which the fragments of two steps take as their four pairs.
+  uint4 av[4];
+  auto load_a = [&](int b) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int k = b * 128 + c * 32;
+      av[c] = k + q * 8 < p.K ? __ldg(reinterpret_cast<const uint4*>(a + k)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (p.ready) {  // the first block of a does not wait for the previous launch
+    if (warp < blocks) load_a(warp);
+    pdl_wait();
+    pdl_trigger();
+  }
+  for (int b = warp; b < blocks; b += W) {
+    if (!p.ready || b != warp) load_a(b);
     uint2 xv[4], yv[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int k = b * 128 + c * 32;
       const bool in = k + q * 8 < p.K;
-      av[c] = in ? __ldg(reinterpret_cast<const uint4*>(a + k)) : make_uint4(0, 0, 0, 0);
       xv[c] = in ? __ldg(reinterpret_cast<const uint2*>(xa + k)) : make_uint2(0, 0);
       yv[c] = in ? __ldg(reinterpret_cast<const uint2*>(xb + k)) : make_uint2(0, 0);
     }
@@ -144,26 +207,356 @@ __global__ void __launch_bounds__(kInnerWarps * 32) lora_inner_kernel(const __gr
     if (t0 + i < p.T && __ldg(p.row_adapter + t0 + i) == adapter) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kInnerWarps; ++w) v += part[w][i][r];
+      for (int w = 0; w < W; ++w) v += part[w][i][r];
       if (p.adapter_scale) v *= __ldg(p.adapter_scale + adapter);
-      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-      const long long at = static_cast<long long>(t0 + i) * p.rank + r0 + r;
-      p.v[at] = *reinterpret_cast<const uint16_t*>(&hi);
-      if (p.low) {
-        // an infinite or NaN value is all in the first plane
-        const float rest = v - __bfloat162float(hi);
-        const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-        p.v[at + static_cast<long long>(p.T) * p.rank] = *reinterpret_cast<const uint16_t*>(&lo);
-      }
+      store_v(p, t0 + i, r0 + r, v);
     }
   }
+}
+
+// The projection's lists of 128 rows from theirs, by a warp: of each tile, the adapters
+// that one of its rows has, in the order of the whole list.
+__device__ __forceinline__ void write_sub_lists(const InnerParams& p, long long t0, const int* s_list, const int* s_place) {
+  const int lane = threadIdx.x & 31;
+  int* to = p.lists + t0 / p.tile_rows * (p.tile_rows + 4);
+  for (int sub = 0; sub < 128 && t0 + sub < p.T; sub += p.tile_rows, to += p.tile_rows + 4) {
+    uint32_t has[4] = {0, 0, 0, 0};  // a bit for each place in the whole list
+    for (int i = lane; i < p.tile_rows; i += 32) {
+      const int at = s_place[sub + i];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) has[w] |= at >= 0 && at >> 5 == w ? 1u << (at & 31) : 0u;
+    }
+    int count = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t mask = __reduce_or_sync(0xffffffffu, has[w]);
+      if (mask >> lane & 1u) to[4 + count + __popc(mask & ((1u << lane) - 1))] = s_list[4 + w * 32 + lane];
+      count += __popc(mask);
+    }
+    if (lane == 0) to[0] = count;
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+// Products on tcgen05 (mma.sync reaches a twentieth of its rate here: 4,096 x 2,048 with
+// rank 64 took 19 us on it).  Each block of 128 input dims of the CTA's rows becomes bf16
+// in a ring in shared memory; each adapter's block of a comes by tensor copies; each of
+// these pairs is a product of its own, which eight warps (a lane is a row, four warps
+// half the ranks) add, times the row's scale, to the sums of the rows that have the
+// adapter.  So a row's sums stay in registers throughout.
+constexpr int kTileRows = 128, kTileRanks = 64, kTileStages = 12, kTileXStages = 3, kTileRaw = 4, kTileAccs = 4;
+constexpr int kSumWarps = 8, kConvertWarps = 8, kCopyWarp = kSumWarps + kConvertWarps, kIssueWarp = kCopyWarp + 1;
+constexpr int kTileWarps = kIssueWarp + 1;
+constexpr int kTileXBytes = kTileRows * 256;  // a block of x: two halves of 64 dims, rows of 128 bytes
+constexpr int kTileOffRaw = kTileXStages * kTileXBytes;  // blocks of codes, a lane's own words side by side; then the sums
+static_assert(kTileRows * kTileRanks * 4 <= kTileRaw * kTileRows * 128, "the sums fit where the codes were");
+constexpr int kTileOffA = kTileOffRaw + kTileRaw * kTileRows * 128;
+constexpr int kTileABytes = 3 * kTileRanks * 256;  // the ring of blocks of a: three of 64 ranks, twelve of 16
+// Rows' scales of the blocks between the farthest copied one, kTileRaw - 1 ahead of the
+// converting warps, and the one whose sums are added, kTileXStages behind them.
+constexpr int kTileScales = 8, kTileOffScales = kTileOffA + kTileABytes;
+static_assert(kTileRaw + kTileXStages <= kTileScales, "a scale stays until it is used");
+constexpr int kTileSmem = 1024 + kTileOffScales + kTileScales * kTileRows * 4;
+
+// Grid: row tiles, shares of the input dims (a cluster), runs of 64 ranks times slots;
+// slot z takes the tile's adapters z, z + slots, ..  map_a: a as rows of K, boxes of 64
+// dims by `box` ranks (a run's, in sixteens).
+__global__ void __launch_bounds__(kTileWarps * 32, 1)
+    lora_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ InnerParams p, int slots, int box,
+                     int stages) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* part = reinterpret_cast<float*>(smem + kTileOffRaw);  // [rows][ranks]: a row's own adapter's sums
+  uint8_t* x_ring = smem;
+  uint8_t* a_ring = smem + kTileOffA;
+  const int a_bytes = box * 256;
+  __shared__ __align__(16) int s_id[kTileRows], s_list[kTileRows + 4];
+  __shared__ int s_place[kTileRows];  // a row's adapter's place in the list, or -1
+  __shared__ int s_base[kTileWarps];
+  __shared__ uint64_t s_full[kTileStages], s_empty[kTileStages], s_xfull[kTileXStages], s_xempty[kTileXStages];
+  __shared__ uint64_t s_tfull[kTileAccs], s_tempty[kTileAccs];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long t0 = static_cast<long long>(blockIdx.x) * kTileRows;
+  const int splits = gridDim.y, rank = blockIdx.y;
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 1);
+    }
+    for (int i = 0; i < kTileXStages; ++i) {
+      mbar_init(&s_xfull[i], kConvertWarps);
+      mbar_init(&s_xempty[i], 1);
+    }
+    for (int i = 0; i < kTileAccs; ++i) {
+      mbar_init(&s_tfull[i], 1);
+      mbar_init(&s_tempty[i], kSumWarps);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&map_a);
+  }
+  if (warp == kIssueWarp) {
+    tmem_alloc(&s_tmem, kTileAccs * kTileRanks);
+    tmem_relinquish();
+  }
+  if (tid < kTileRows) s_list[4 + tid] = -1;
+  if (!p.ready) pdl_wait();
+  const int slot = blockIdx.z % slots, r0 = blockIdx.z / slots * kTileRanks;
+  const int ranks = min(kTileRanks, p.rank - r0), columns = (ranks + 15) & ~15;
+  const int all = (p.K + 127) / 128;
+  const int b0 = all * rank / splits, nb = all * (rank + 1) / splits - b0;
+  tc_fence_before();
+  write_list(p, t0, kTileRows, s_list, s_id, s_base);
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int n = s_list[0];
+  if (tid < kTileRows) {
+    const int id = s_id[tid];
+    int at = -1;
+#pragma unroll 1
+    for (int j = 0; j < n; j += 4) {  // -1 behind the list's end
+      const int4 v = *reinterpret_cast<const int4*>(s_list + 4 + j);
+      at = v.x == id ? j : v.y == id ? j + 1 : v.z == id ? j + 2 : v.w == id ? j + 3 : at;
+    }
+    s_place[tid] = id >= 0 ? at : -1;
+  }
+  const int mine = n > slot ? (n - slot - 1) / slots + 1 : 0;  // adapters of this slot
+  __syncthreads();                                             // s_place
+  // a is asked for first; what else is read waits for the previous launch
+  if (warp != kCopyWarp) {
+    if (p.ready) pdl_wait();
+    pdl_trigger();  // every CTA holds its TMEM
+  }
+  bool ok = true;
+  if (mine == 0) {
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------ a
+    if (lane == 0) {
+      const uint64_t keep = l2_policy_evict_last();
+      int s = 0, sent = 0;
+      uint32_t phase = 0;
+      for (int b = 0; b < nb && ok; ++b)
+        for (int j = 0; j < mine; ++j, ++sent) {
+          if (sent >= stages && !(ok = mbar_wait(&s_empty[s], phase ^ 1u, &s_abort))) break;
+          mbar_arrive_expect_tx(&s_full[s], a_bytes);
+          const int y = s_list[4 + slot + j * slots] * p.rank + r0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d(a_ring + s * a_bytes + h * (a_bytes / 2), &map_a, ((b0 + b) * 128 + h * 64) * 2, y, &s_full[s], keep);
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      if (!ok) {
+        s_abort = 1;
+        set_error(p.err, kErrTimeout);
+      }
+      // copies in flight must land before the CTA may exit
+      for (int i = 0; i < min(stages, sent); ++i) {
+        if (--s < 0) {
+          s = stages - 1;
+          phase ^= 1u;
+        }
+        mbar_wait(&s_full[s], phase, nullptr);
+      }
+    }
+  } else if (warp == kIssueWarp) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kTileRows, columns, 0, 0);
+      const uint64_t xd = smem_desc_sw128(x_ring), ad = smem_desc_sw128(a_ring);
+      int s = 0;
+      uint32_t phase = 0, at = 0;
+      for (int b = 0; b < nb && ok; ++b) {
+        const int xs = b % kTileXStages;
+        if (!(ok = mbar_wait(&s_xfull[xs], static_cast<uint32_t>(b / kTileXStages) & 1u, &s_abort))) break;
+        for (int j = 0; j < mine; ++j, ++at) {
+          const int acc = static_cast<int>(at % kTileAccs);
+          if (!(ok = mbar_wait(&s_full[s], phase, &s_abort))) break;
+          if (at >= kTileAccs && !(ok = mbar_wait(&s_tempty[acc], (at / kTileAccs - 1) & 1u, &s_abort))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 16 dims each: four to a half
+            umma_bf16(tmem + acc * kTileRanks, xd + ((xs * kTileXBytes + (k >> 2) * (kTileXBytes / 2)) >> 4) + (k & 3) * 2,
+                      ad + ((s * a_bytes + (k >> 2) * (a_bytes / 2)) >> 4) + (k & 3) * 2, idesc, k > 0 ? 1u : 0u);
+          mma_commit(&s_tfull[acc]);
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        s_abort = 1;
+        set_error(p.err, kErrTimeout);
+        // the last products still read shared memory and write TMEM
+        for (uint32_t i = at > kTileAccs ? at - kTileAccs : 0; i < at; ++i)
+          mbar_wait(&s_tfull[i % kTileAccs], (i / kTileAccs) & 1u, nullptr);
+      }
+    }
+  } else if (warp >= kSumWarps) {
+    // ------------------------------------------------------------ x
+    // A lane's 16 codes are two words of the swizzled rows; eight lanes have a row's
+    // block, a warp four rows of it at a time.  Codes are copied kTileRaw - 1 blocks ahead
+    // to places of the lane's own.  Loops stay rolled: a launch runs this code once, and
+    // fetching it takes longer than running it.
+    constexpr int kSteps = kTileRows / kConvertWarps / 4;
+    const int q = lane & 7, first = (warp - kSumWarps) * (kSteps * 4) + (lane >> 3);
+    uint8_t* raw = smem + kTileOffRaw + ((warp - kSumWarps) * 32 + lane) * 16;
+    const uint8_t* x = p.x + (t0 + first) * p.ld_x + q * 16;
+    auto fetch = [&](int b) {
+      const int k = (b0 + b) * 128;
+#pragma unroll 1
+      for (int j = 0; j < kSteps; ++j) {
+        const bool in = b < nb && t0 + first + j * 4 < p.T && k + q * 16 < p.K;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         smem_u32(raw + ((b % kTileRaw) * kSteps + j) * kConvertWarps * 512)),
+                     "l"(in ? x + j * 4 * p.ld_x + k : p.x), "r"(in ? 16 : 0)
+                     : "memory");
+      }
+      const int r = (warp - kSumWarps) * (kSteps * 4) + lane;
+      if (lane < kSteps * 4 && b < nb && t0 + r < p.T)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                         smem_u32(smem + kTileOffScales + ((b % kTileScales) * kTileRows + r) * 4)),
+                     "l"(p.x_scale + (t0 + r) * p.ld_xs + b0 + b)
+                     : "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int b = 0; b < kTileRaw - 1; ++b) fetch(b);
+#pragma unroll 1
+    for (int b = 0; b < nb; ++b) {
+      const int xs = b % kTileXStages;
+      fetch(b + kTileRaw - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kTileRaw - 1) : "memory");
+      if (b >= kTileXStages) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_xempty[xs], static_cast<uint32_t>(b / kTileXStages - 1) & 1u, &s_abort));
+        if (!ok) break;
+      }
+      uint8_t* dst = x_ring + xs * kTileXBytes + (q >> 2) * (kTileXBytes / 2);
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const int r = first + j * 4;
+        const uint4 v = *reinterpret_cast<const uint4*>(raw + ((b % kTileRaw) * kSteps + j) * kConvertWarps * 512);
+        *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * (q & 3)) ^ (r & 7)) * 16)) =
+            make_uint4(bf16_of_e4m3x2(v.x), bf16_of_e4m3x2(v.x >> 16), bf16_of_e4m3x2(v.y), bf16_of_e4m3x2(v.y >> 16));
+        *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * (q & 3) + 1) ^ (r & 7)) * 16)) =
+            make_uint4(bf16_of_e4m3x2(v.z), bf16_of_e4m3x2(v.z >> 16), bf16_of_e4m3x2(v.w), bf16_of_e4m3x2(v.w >> 16));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_xfull[xs]);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      set_error(p.err, kErrTimeout);
+    }
+  } else {
+    // ------------------------------------------------------------ sums
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const int place = s_place[row];
+    const float* scales = reinterpret_cast<const float*>(smem + kTileOffScales) + row;
+    const float factor = p.adapter_scale && place >= 0 ? __ldg(p.adapter_scale + s_id[row]) : 1.f;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 32;
+    const bool idle = half * 32 >= columns;
+    float y[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) y[k] = 0.f;
+    int s = 0;
+    uint32_t at = 0;
+    for (int b = 0; b < nb && ok; ++b) {
+      for (int j = 0; j < mine; ++j, ++at) {
+        const int acc = static_cast<int>(at % kTileAccs);
+        const bool own = place == slot + j * slots;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_tfull[acc], (at / kTileAccs) & 1u, &s_abort));
+        if (!ok) break;
+        tc_fence_after();
+        if (warp == 0 && lane == 0) {  // the products have read the stages
+          mbar_arrive(&s_empty[s]);
+          if (j + 1 == mine) mbar_arrive(&s_xempty[b % kTileXStages]);
+        }
+        if (++s == stages) s = 0;
+        if (__any_sync(0xffffffffu, own) && !idle) {
+          uint32_t v[2][16];
+          tmem_ld32x16_async(taddr + acc * kTileRanks, v[0]);
+          tmem_ld32x16_async(taddr + acc * kTileRanks + 16, v[1]);
+          tmem_wait_ld16(v[0]);
+          tmem_wait_ld16(v[1]);
+          if (own) {
+            const float scale = scales[(b % kTileScales) * kTileRows];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) y[k] = fmaf(scale, __uint_as_float(v[k >> 4][k & 15]), y[k]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_tempty[acc]);
+      }
+    }
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      set_error(p.err, kErrTimeout);
+    }
+    // every block has been converted: its products are done
+    if (!idle) {  // the pieces of a row turned by its number: lanes do not collide
+      float4* dst = reinterpret_cast<float4*>(part + row * kTileRanks);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        dst[(half * 8 + k) ^ (row & 15)] = make_float4(y[4 * k] * factor, y[4 * k + 1] * factor, y[4 * k + 2] * factor,
+                                                         y[4 * k + 3] * factor);
+    }
+  }
+  if (warp == kCopyWarp) {
+    __syncwarp();
+    if (p.ready) pdl_wait();
+    pdl_trigger();
+    if (rank == 0 && blockIdx.z == 0) write_sub_lists(p, t0, s_list, s_place);
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == kIssueWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTileAccs * kTileRanks);
+  }
+  if (mine == 0) return;  // the same in a cluster's CTAs
+  if (splits > 1) cluster_sync();
+  // a share of the rows for each CTA: 16 threads a row, 4 ranks each
+  const int row0 = kTileRows * rank / splits, row1 = kTileRows * (rank + 1) / splits;
+#pragma unroll 1
+  for (int i = row0 + (tid >> 4); s_abort == 0 && i < row1; i += kTileWarps * 2) {
+    const int r = (tid & 15) * 4;
+    if (s_place[i] < 0 || s_place[i] % slots != slot || r >= columns) continue;
+    const uint32_t at = smem_u32(part + i * kTileRanks + (((tid & 15) ^ (i & 15)) * 4));
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int c = 0; c < splits; ++c) {  // in rank order
+      float4 w;
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+                   : "r"(splits > 1 ? map_rank(at, static_cast<uint32_t>(c)) : at));
+      v[0] += w.x;
+      v[1] += w.y;
+      v[2] += w.z;
+      v[3] += w.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = r + k < ranks ? v[k] : 0.f;
+    store_v4(p, t0 + i, r0 + r, v);
+  }
+  __syncwarp();
+  if (splits > 1) cluster_sync();  // no CTA leaves while its part may still be read
 }
 
 }  // namespace
 
 // The lists for any tile height: (rows + 4) words a tile of 16, 32, 64 or 128 rows.
 static size_t lists_offset(int T, int rank) {
-  return (4 * static_cast<size_t>(T) * rank + 255) & ~static_cast<size_t>(255);
+  return (4 * static_cast<size_t>(T) * lora_pitch(rank) + 255) & ~static_cast<size_t>(255);
 }
 size_t lora_workspace_bytes(int T, int rank) {
   return lists_offset(T, rank) + (static_cast<size_t>(T) + 15) / 16 * 80 + 528;
@@ -174,12 +567,54 @@ LoraInner lora_inner_at(const csa2_lora_linear_args& a, void* ws, int tile_rows)
   return LoraInner{reinterpret_cast<uint16_t*>(base), reinterpret_cast<int*>(base + lists_offset(a.base.T, a.rank)), tile_rows};
 }
 
-cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& to, const DeviceCtx& ctx, cudaStream_t st) {
+cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& to, int ctas, const DeviceCtx& ctx,
+                              cudaStream_t st, const char** why) {
   const csa2_fp8_linear_args& l = a.base;
   const InnerParams p{l.x, l.x_scale, a.a, a.adapter_scale, a.row_adapter, to.v, to.lists, l.ld_x, l.ld_x_scale, l.T, l.K,
-                      a.rank, a.n_adapters, to.tile_rows, l.out_format != CSA2_OUT_BF16, l.w_ready, ctx.err};
-  const dim3 grid((l.T + 15) / 16, a.rank / 8, a.n_adapters < 16 ? a.n_adapters : 16);
-  return launch_pdl(lora_inner_kernel, grid, dim3(kInnerWarps * 32), 0, st, p);
+                      a.rank, lora_pitch(a.rank), a.n_adapters, to.tile_rows, l.out_format != CSA2_OUT_BF16, l.w_ready,
+                      ctx.err};
+  const int tiles = (l.T + kTileRows - 1) / kTileRows, runs = (a.rank + kTileRanks - 1) / kTileRanks, blocks = (l.K + 127) / 128;
+  // 8 ranks without a partner get 8 zeros beside them: products are of 16
+  const dim3 grid((l.T + 15) / 16, (a.rank + 15) / 16 * 2, a.n_adapters < 16 ? a.n_adapters : 16);
+  // The small CTAs while they run in a wave or two (an SM holds two), by the most adapters
+  // that 16 rows can have: 333 x 1,360 x 1,001 with 5 of rank 24 take 13.9 us, 17 with the
+  // tiles; 64 x 2,048 x 32,768 with 16 of rank 64: 31.9 and 30.7.
+  if (static_cast<long long>(grid.x) * grid.y * grid.z <= 3LL * ctx.num_sms)
+    return blocks > 16 ? launch_pdl(lora_inner_kernel<32>, grid, dim3(1024), 0, st, p)
+                       : launch_pdl(lora_inner_kernel<16>, grid, dim3(512), 0, st, p);
+  // one CTA an SM: shares of the input dims, then of the adapters
+  int splits = ctx.num_sms / (tiles * runs);
+  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  if (splits > blocks) splits = blocks;
+  const int room = ctx.num_sms - ctas >= 16 ? ctx.num_sms - ctas : ctx.num_sms;
+  int slots = room / (tiles * runs * splits);
+  slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
+  if (slots > a.n_adapters) slots = a.n_adapters;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles, splits, runs * slots);
+  cfg.blockDim = dim3(kTileWarps * 32);
+  cfg.dynamicSmemBytes = kTileSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = splits;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = splits > 1 ? 2 : 1;
+  CUtensorMap map_a;
+  const uint64_t row = 2 * static_cast<uint64_t>(l.K);
+  const int box = a.rank > 48 ? kTileRanks : (a.rank + 15) & ~15;
+  if (encode_tmap_2d_u8(&map_a, a.a, row, static_cast<uint64_t>(a.n_adapters) * a.rank, row, 128, box) != CUDA_SUCCESS) {
+    *why = "csa2_lora_linear: a tensor map could not be encoded";
+    return cudaErrorInvalidValue;
+  }
+  cudaError_t e = prefer_max_smem_once<lora_tile_kernel>(ctx.device, kTileSmem);
+  if (e != cudaSuccess) return e;
+  const int stages = kTileABytes / (box * 256) < kTileStages ? kTileABytes / (box * 256) : kTileStages;
+  return cudaLaunchKernelEx(&cfg, lora_tile_kernel, map_a, p, slots, box, stages);
 }
 
 }  // namespace csa2

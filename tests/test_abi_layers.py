@@ -91,7 +91,7 @@ def _lora(base=None, **kw):
     ({"T": (1 << 20) + 1}, {}, 2, b"2^20"), ({}, {"row_adapter": None}, 1, b"row_adapter"), ({}, {"a": None}, 1, b"row_adapter/a/b"),
     ({}, {"b": None}, 1, b"row_adapter/a/b"), ({}, {"rank": 0}, 2, b"rank=0"), ({}, {"rank": 12}, 2, b"rank=12"),
     ({}, {"rank": 136}, 2, b"rank=136"), ({}, {"rank": -8}, 2, b"rank=-8"), ({}, {"n_adapters": 0}, 2, b"n_adapters=0"),
-    ({}, {"n_adapters": (1 << 21) + 1}, 2, b"n_adapters"), ({}, {"a": FAKE + 8}, 3, b"16-B"), ({}, {"b": FAKE + 8}, 3, b"16-B"),
+    ({}, {"n_adapters": (1 << 21) + 1}, 2, b"n_adapters"), ({"N": 1}, {"n_adapters": (1 << 23) + 1, "rank": 128}, 2, b"rank at most"), ({}, {"a": FAKE + 8}, 3, b"16-B"), ({}, {"b": FAKE + 8}, 3, b"16-B"),
     ({}, {"row_adapter": FAKE + 2}, 3, b"4-B"), ({}, {"adapter_scale": FAKE + 2}, 3, b"4-B"),
 ])
 def test_lora_linear_refusals(lib, base, kw, code, word):
@@ -118,9 +118,9 @@ def test_lora_linear_workspace(lib):
 @pytest.mark.parametrize("T", [1, 15, 16, 17, 64, 127, 128, 129, 1000, 1 << 20])
 @pytest.mark.parametrize("rank", [8, 24, 128])
 def test_lora_workspace_holds_every_tile_height(lib, T, rank):
-    """Inner products [2][T][rank] in bf16, then (rows + 4) words for each tile of 16, 32, 64 or 128 rows."""
+    """Inner products [2][T][rank, to a multiple of 64] in bf16, then (rows + 4) words for each tile of 16, 32, 64 or 128 rows."""
     from serving_lightning_indexer_gb300 import csa2
-    v = -(-4 * T * rank // 256) * 256
+    v = -(-4 * T * (-(-rank // 64) * 64) // 256) * 256
     assert csa2.lora_workspace_size(T, rank) >= v + max(-(-T // rows) * (rows + 4) * 4 for rows in (16, 32, 64, 128))
 
 
