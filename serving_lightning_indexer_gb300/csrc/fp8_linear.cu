@@ -9,7 +9,7 @@
 // few rows, bound by the weights' bytes (8 x 2,048 x 32,768: 12.7 us, 5.3 TB/s) or, where
 // they are few, by latency (8 x 7,168 x 512: 4.6 us).
 //
-// LORA: each adapter that a tile's rows use (lora.cu lists them) brings up to two more
+// LORA: each adapter that a tile's rows use (lora.cu lists them) brings one to three more
 // blocks for every 64 ranks, bf16 products of the rows' inner products with the
 // adapter's b, summed like the others but only to the rows that have the adapter.  The
 // projection's own blocks come first, and only what lora.cu wrote waits for it.
@@ -52,7 +52,7 @@ template <bool LORA>
 struct LoraParams {};
 template <>
 struct LoraParams<true> {
-  CUtensorMap map_v, map_b;  // inner products [2 T, pitch], b [adapters N, rank]: row_bytes by a tile's rows or columns
+  CUtensorMap map_v, map_b;  // inner products [planes T, pitch], b [adapters N, rank]: row_bytes by a tile's rows or columns
   const uint16_t* b;
   const int* row_adapter;
   const int* lists;
@@ -737,12 +737,12 @@ cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int 
   lo->row_adapter = a.row_adapter;
   lo->lists = to.lists;
   lo->list_stride = rows + 4;
-  lo->planes = a.base.out_format == CSA2_OUT_BF16 ? 1 : 2;
+  lo->planes = lora_planes(a.base.out_format);
   lo->pieces = (a.rank + 63) / 64 * lo->planes;
   const uint64_t row = 2 * static_cast<uint64_t>(a.rank);
   lo->row_bytes = a.rank == 16 || a.rank == 32 ? static_cast<int>(row) : 128;
   const uint64_t v_row = 2 * static_cast<uint64_t>(lora_pitch(a.rank));
-  if (encode_tmap_2d_u8(&lo->map_v, to.v, v_row, 2 * static_cast<uint64_t>(a.base.T), v_row, 128, rows) != CUDA_SUCCESS ||
+  if (encode_tmap_2d_u8(&lo->map_v, to.v, v_row, lo->planes * static_cast<uint64_t>(a.base.T), v_row, 128, rows) != CUDA_SUCCESS ||
       encode_tmap_2d_u8(&lo->map_b, a.b, row, static_cast<uint64_t>(a.n_adapters) * a.base.N, row, lo->row_bytes, columns,
                         lo->row_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
                         : lo->row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B

@@ -4,9 +4,11 @@
 // projection (fp8_linear.cu) adds v[t] b[i]^T to its sums before RoPE and rounding.
 //
 // The codes are exact in bf16 and a is bf16, so a block's 128 products are summed by
-// the tensor core (mma.sync, fp32) and the block's scale is applied to the sum.  The
-// result is written as the bf16 nearest to it and, for outputs that can tell (fp32,
-// and the fp32 scales of e4m3), the bf16 nearest to what that leaves: 2^-17 together.
+// the tensor core in fp32 and the block's scale is applied to the sum.  The result is
+// written as the bf16 nearest to it and, for fp32 output, the bf16 nearest to what that
+// leaves (2^-17 together); for e4m3 output a third (2^-25), as a code on the other side of
+// its border is 2^-3 off however near the border was (two leave three times the codes on
+// the other side that fp32's own roundings do).
 //
 // Two kernels.  Up to 16 rows: a CTA takes one of their adapters and 8 of its ranks, its
 // 16 warps the blocks of 128 input dims in turn, added in warp order.  More rows: a CTA
@@ -28,12 +30,12 @@ struct InnerParams {
   const uint16_t* a;
   const float* adapter_scale;
   const int* row_adapter;
-  uint16_t* v;  // [2][T][pitch]: the bf16 values, and what they leave
+  uint16_t* v;  // [planes][T][pitch]: the bf16 values, what they leave, and what that leaves
   int* lists;
   long long ld_x, ld_xs;
   int T, K, rank, pitch, n_adapters;
   int tile_rows;  // rows of the projection's tiles
-  int low;        // the second plane is wanted
+  int planes;     // 1, 2 or 3
   int ready;      // a and row_adapter may be read before the previous launch completes
   uint32_t* err;
 };
@@ -88,34 +90,23 @@ __device__ __forceinline__ void write_list(const InnerParams& p, long long t0, i
   __syncthreads();
 }
 
-// Writes v of a row and rank.
-__device__ __forceinline__ void store_v(const InnerParams& p, long long row, int rank, float v) {
-  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-  const long long at = row * p.pitch + rank;
-  p.v[at] = *reinterpret_cast<const uint16_t*>(&hi);
-  if (p.low) {
-    // an infinite or NaN value is all in the first plane
-    const float rest = v - __bfloat162float(hi);
-    const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-    p.v[at + static_cast<long long>(p.T) * p.pitch] = *reinterpret_cast<const uint16_t*>(&lo);
-  }
-}
-
-// The same of four ranks from a multiple of four on.
-__device__ __forceinline__ void store_v4(const InnerParams& p, long long row, int rank, const float (&v)[4]) {
-  uint32_t hi[2], lo[2];
+// Writes v of a row and N ranks from `rank` on, in as many bf16 as there are planes.  An
+// infinite or NaN value is all in the first.
+template <int N>
+__device__ __forceinline__ void store_v(const InnerParams& p, long long row, int rank, float (&v)[N]) {
+  uint16_t* to = p.v + row * p.pitch + rank;
+  for (int plane = 0; plane < p.planes; ++plane, to += static_cast<long long>(p.T) * p.pitch) {
+    alignas(8) uint16_t h[N];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
-    const float2 f = __bfloat1622float2(a);
-    const float x = v[2 * h] - f.x, y = v[2 * h + 1] - f.y;
-    const __nv_bfloat162 b = __floats2bfloat162_rn(isfinite(x) ? x : 0.f, isfinite(y) ? y : 0.f);
-    hi[h] = *reinterpret_cast<const uint32_t*>(&a);
-    lo[h] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int k = 0; k < N; ++k) {
+      const __nv_bfloat16 b = __float2bfloat16_rn(v[k]);
+      const float rest = v[k] - __bfloat162float(b);
+      v[k] = isfinite(rest) ? rest : 0.f;
+      h[k] = *reinterpret_cast<const uint16_t*>(&b);
+    }
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(h);
+    else to[0] = h[0];
   }
-  const long long at = row * p.pitch + rank;
-  *reinterpret_cast<uint2*>(p.v + at) = make_uint2(hi[0], hi[1]);
-  if (p.low) *reinterpret_cast<uint2*>(p.v + at + static_cast<long long>(p.T) * p.pitch) = make_uint2(lo[0], lo[1]);
 }
 
 // W warps: 16, or 32 where there are more than 16 blocks of input dims.
@@ -209,7 +200,8 @@ __global__ void __launch_bounds__(W * 32) lora_inner_kernel(const __grid_constan
 #pragma unroll
       for (int w = 0; w < W; ++w) v += part[w][i][r];
       if (p.adapter_scale) v *= __ldg(p.adapter_scale + adapter);
-      store_v(p, t0 + i, r0 + r, v);
+      float one[1] = {v};
+      store_v(p, t0 + i, r0 + r, one);
     }
   }
 }
@@ -546,7 +538,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = r + k < ranks ? v[k] : 0.f;
-    store_v4(p, t0 + i, r0 + r, v);
+    store_v(p, t0 + i, r0 + r, v);
   }
   __syncwarp();
   if (splits > 1) cluster_sync();  // no CTA leaves while its part may still be read
@@ -556,7 +548,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
 
 // The lists for any tile height: (rows + 4) words a tile of 16, 32, 64 or 128 rows.
 static size_t lists_offset(int T, int rank) {
-  return (4 * static_cast<size_t>(T) * lora_pitch(rank) + 255) & ~static_cast<size_t>(255);
+  return (2 * kLoraPlanes * static_cast<size_t>(T) * lora_pitch(rank) + 255) & ~static_cast<size_t>(255);
 }
 size_t lora_workspace_bytes(int T, int rank) {
   return lists_offset(T, rank) + (static_cast<size_t>(T) + 15) / 16 * 80 + 528;
@@ -571,7 +563,7 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
                               cudaStream_t st, const char** why) {
   const csa2_fp8_linear_args& l = a.base;
   const InnerParams p{l.x, l.x_scale, a.a, a.adapter_scale, a.row_adapter, to.v, to.lists, l.ld_x, l.ld_x_scale, l.T, l.K,
-                      a.rank, lora_pitch(a.rank), a.n_adapters, to.tile_rows, l.out_format != CSA2_OUT_BF16, l.w_ready,
+                      a.rank, lora_pitch(a.rank), a.n_adapters, to.tile_rows, lora_planes(l.out_format), l.w_ready,
                       ctx.err};
   const int tiles = (l.T + kTileRows - 1) / kTileRows, runs = (a.rank + kTileRanks - 1) / kTileRanks, blocks = (l.K + 127) / 128;
   // 8 ranks without a partner get 8 zeros beside them: products are of 16

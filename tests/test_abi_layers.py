@@ -118,9 +118,9 @@ def test_lora_linear_workspace(lib):
 @pytest.mark.parametrize("T", [1, 15, 16, 17, 64, 127, 128, 129, 1000, 1 << 20])
 @pytest.mark.parametrize("rank", [8, 24, 128])
 def test_lora_workspace_holds_every_tile_height(lib, T, rank):
-    """Inner products [2][T][rank, to a multiple of 64] in bf16, then (rows + 4) words for each tile of 16, 32, 64 or 128 rows."""
+    """Inner products [3][T][rank, to a multiple of 64] in bf16, then (rows + 4) words for each tile of 16, 32, 64 or 128 rows."""
     from serving_lightning_indexer_gb300 import csa2
-    v = -(-4 * T * (-(-rank // 64) * 64) // 256) * 256
+    v = -(-6 * T * (-(-rank // 64) * 64) // 256) * 256
     assert csa2.lora_workspace_size(T, rank) >= v + max(-(-T // rows) * (rows + 4) * 4 for rows in (16, 32, 64, 128))
 
 

@@ -10,7 +10,8 @@ Tolerances, from the arithmetic (u = 2^-24, half a step of fp32):
     after the root; root, reciprocal and two products 4 more: e = (8 V + 12) u.  A
     code's value adds its block's maximum (e) and factor and product (2 u).
   * an inner product v: 128 products of a block, exact in fp32, and blocks in at most
-    150 + blocks / 16 roundings; then its bf16 value, 2^-8 of it, or two, 2^-16.
+    150 + blocks / 16 roundings; then its bf16 value, 2^-8 of it, or two, 2^-16, or
+    three, 2^-24.
   * an adapter's addition: exact products, at most 2 rank + 8 roundings; the whole sum
     those of csa2_fp8_linear and one for each of the parts that are added (at most 40
     here).  RoPE and the output's step as for csa2_fp8_linear.
@@ -152,7 +153,7 @@ def _lora_ref(x, xs, w, ws, a, b, ids, s, pos, head, theta, planes):
         if i >= 0:
             out_mag[t] = np.abs(bf[i]) @ np.abs(sf[i] * (af[i] @ xr[t]))
     tol = (170 + 2 * nb) * U * (mag + out_mag) + (150 + nb / 16) * U * add_mag
-    tol += (2.0 ** (-16 if planes == 2 else -8) + (2 * R + 8) * U) * out_mag
+    tol += (2.0 ** (-8 * planes) + (2 * R + 8) * U) * out_mag
     y = y + add
     if head:
         N = y.shape[1]
@@ -212,7 +213,7 @@ def _check_lora(T, N, K, out, R, n, run=1, head=0, seed=0, w_ready=False, extra=
     pick = torch.arange(T, device=dev) if T * N * K < 1 << 31 else torch.unique(torch.cat([
         torch.tensor([0, 1, T // 2, T - 1], device=dev), torch.randint(0, T, (12,), generator=g, device=dev)]))
     y, tol = _lora_ref(x[pick], xs[pick], w, ws, a, b, ids[pick], s if factor else torch.ones_like(s),
-                       pos[pick] if head else None, head, 10000.0, 1 if out == "bf16" else 2)
+                       pos[pick] if head else None, head, 10000.0, {"bf16": 1, "fp32": 2, "fp8": 3}[out])
     _check_out(big[:T, :N][pick], osc[:T, :N // 128][pick] if out == "fp8" else None, y, tol, out, len(pick), N)
 
 
