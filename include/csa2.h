@@ -516,7 +516,7 @@ CSA2_API int csa2_batch_plan(const csa2_batch_plan_args* args, void* stream);
  * written and nothing else.  The row's sum of squares is held in fp32; where it
  * passes that range (from magnitudes of 2^57 on) y is zeros.  K is a multiple of 16,
  * at most 16384.  Alignment: x, residual, residual_out, codes, y, gamma 16 B; row
- * strides multiples of 16 B; scale 4 B.  No workspace. */
+ * strides multiples of 16 B and below 2^29; scale 4 B.  No workspace. */
 typedef struct {
   const uint16_t* x; int64_t ld_x;             /* [T, K] bf16, row stride ld_x >= K */
   const void* residual; int64_t ld_residual;   /* [T, K] bf16 or fp32 */
@@ -540,14 +540,15 @@ CSA2_API int csa2_add_norm_fp8(const csa2_add_norm_fp8_args* args, void* stream)
  * counts as none and is recorded (CSA2_ERR_DEVICE_BOUNDS).  Rows of one adapter may
  * be anywhere; side by side they take the least time.  v is held as the bf16 nearest
  * to its fp32 sum for bf16 output, as the sum of two bf16 (2^-17 of it) for fp32 output
- * and of three (2^-25) for e4m3 output.  An infinity or NaN of one adapter stays in its own rows.
+ * and of three (2^-25) for e4m3 output.  An infinity or NaN of one adapter stays in its
+ * own rows.
  * base: the arguments of csa2_fp8_linear, with its rules; T at most 2^20; w_ready = 1
  * says the same of a, b, adapter_scale and row_adapter as of w and w_scale.  rank is
  * a multiple of 8, at most 128; n_adapters >= 1, n_adapters * N and n_adapters * rank at
- * most 2^30.  An
- * adapter of a smaller rank is padded with zeros.  Alignment: a, b 16 B; row_adapter,
- * adapter_scale 4 B; workspace 16 B: csa2_workspace_size(CSA2_CALL_LORA_LINEAR, args,
- * &bytes), read and written until the call's work is done.  Results do not depend on
+ * most 2^30.  An adapter of a smaller rank is padded with zeros.  Alignment: a, b 16 B;
+ * row_adapter, adapter_scale 4 B; workspace 16 B: csa2_workspace_size(
+ * CSA2_CALL_LORA_LINEAR, args, &bytes), read and written until the call's work is done,
+ * so calls that may run at the same time need one each.  Results do not depend on
  * the launch's timing (no atomics); the order in which a row's parts are added, and so
  * its last bits, can depend on which adapters the rows around it have. */
 typedef struct {
@@ -569,9 +570,9 @@ CSA2_API int csa2_lora_linear(const csa2_lora_linear_args* args, void* workspace
  *   their log probabilities; -1 and -inf where fewer are finite.
  * An infinity or NaN among the logits has no part in a row (a masked token's -inf;
  * the type's lowest value is a logit like any other).  A row without a finite logit
- * has lse -inf and entropy 0; a log probability past fp32's range is -inf.  token[t] = -1: no token, logprob 0; an id outside
- * [-1, V) counts as none and is recorded (CSA2_ERR_DEVICE_BOUNDS).  Every output is
- * optional, but one has to be there; logprob goes with token.  Sums are held in fp32,
+ * has lse -inf and entropy 0; a log probability past fp32's range is -inf.  token[t] =
+ * -1: no token, logprob 0; an id outside [-1, V) counts as none and is recorded
+ * (CSA2_ERR_DEVICE_BOUNDS).  Every output is optional, but one has to be there; logprob goes with token.  Sums are held in fp32,
  * the largest term apart, so that a likely token's log probability keeps its digits.
  * T * V is not limited; V at most 2^30, T at most 2^27, n_top at most 32.
  * Alignment: logits their own size (rows may start anywhere; 16-B aligned rows are

@@ -59,7 +59,7 @@ struct LoraParams<true> {
   int list_stride;
   int rank;
   int row_bytes;  // of a block of b in shared memory: 128, or 32 or 64 for all of rank 16 or 32
-  int pieces;  // blocks of an adapter: 64 ranks each, times planes of v
+  int pieces;     // blocks of an adapter: 64 ranks each, times planes of v
   int planes;
 };
 // Block i of a tile's adapters: the adapter, where its ranks start, how many there are,
@@ -94,9 +94,9 @@ __device__ __forceinline__ void copy_b_rows(uint8_t* dst, const LoraParams<true>
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 // A producing warp's blocks: v by a tensor copy, b by one or, row by row, by plain copies.
-// A stage's barrier takes two arrivals, one with the tensor copies' bytes, one for b.  Plain
-// copies are waited for when those of two more blocks are on their way: with three, all of
-// the ring's stages would be taken before a block's products begin.
+// A stage's barrier takes two arrivals, one with the tensor copies' bytes, one for b.  A
+// block's plain copies are waited for two blocks later, whatever kind those are: with
+// three, all of the ring's stages would be taken before its products begin.
 struct LoraCopies {
   uint64_t* pending[2];  // the barriers of the blocks whose plain copies are on their way, oldest first
   int count = 0;
@@ -115,7 +115,15 @@ struct LoraCopies {
         mbar_arrive(full);
       }
     }
-    if (!plain) return;
+    if (!plain) {
+      if (count == 2) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        arrive();
+      } else {
+        flush();
+      }
+      return;
+    }
     copy_b_rows(b_dst, lo, at, n0, b_rows, N);
     if (count == 2) {
       asm volatile("cp.async.wait_group 2;" ::: "memory");

@@ -23,7 +23,6 @@
 namespace csa2 {
 namespace {
 
-
 struct InnerParams {
   const uint8_t* x;
   const float* x_scale;
@@ -230,8 +229,8 @@ __device__ __forceinline__ void write_sub_lists(const InnerParams& p, long long 
 }
 
 // ---------------------------------------------------------------- many rows
-// Products on tcgen05 (mma.sync reaches a twentieth of its rate here: 4,096 x 2,048 with
-// rank 64 took 19 us on it).  Each block of 128 input dims of the CTA's rows becomes bf16
+// Products on tcgen05: with many adapters in a tile each of them is a product with all 128
+// rows, 16 times what the rows need, which its rate hides.  Each block of 128 input dims of the CTA's rows becomes bf16
 // in a ring in shared memory; each adapter's block of a comes by tensor copies; each of
 // these pairs is a product of its own, which eight warps (a lane is a row, four warps
 // half the ranks) add, times the row's scale, to the sums of the rows that have the
@@ -401,9 +400,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
     const uint8_t* x = p.x + (t0 + first) * p.ld_x + q * 16;
     auto fetch = [&](int b) {
       const int k = (b0 + b) * 128;
+      // nothing, not even zeros, behind the last block: the sums go where the codes were
 #pragma unroll 1
-      for (int j = 0; j < kSteps; ++j) {
-        const bool in = b < nb && t0 + first + j * 4 < p.T && k + q * 16 < p.K;
+      for (int j = 0; b < nb && j < kSteps; ++j) {
+        const bool in = t0 + first + j * 4 < p.T && k + q * 16 < p.K;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                          smem_u32(raw + ((b % kTileRaw) * kSteps + j) * kConvertWarps * 512)),
                      "l"(in ? x + j * 4 * p.ld_x + k : p.x), "r"(in ? 16 : 0)

@@ -326,6 +326,107 @@ def test_lora_linear_repeats_and_takes_strides_streams_and_graphs(T, K, N):
             assert torch.equal(y, ref)
 
 
+@pytest.mark.parametrize("T,N,K,R,n,run,out", [
+    (5, 128, 65536, 16, 2, 1, "fp8"), (200, 128, 32768, 64, 3, 50, "fp8"), (16, 128, 16, 96, 16, 1, "fp8"),
+    (64, 8192, 128, 104, 9, 1, "bf16"), (48, 20000, 144, 8, 48, 1, "fp32"), (1500, 1024, 528, 8, 4, 90, "fp8"),
+    (1500, 1024, 528, 40, 4, 90, "bf16"), (1500, 4097, 528, 120, 3, 500, "fp32"), (1400, 640, 272, 128, 1400, 1, "fp8"),
+    (1400, 640, 272, 96, 1, 1400, "fp32"), (20000, 257, 144, 32, 11, 333, "bf16"), (2305, 512, 7168, 64, 8, 100, "fp8")])
+def test_lora_linear_at_the_edges_of_its_kernels(T, N, K, R, n, run, out):
+    """The longest and shortest rows, each way that a block of b is copied beside each kind of
+    tile, a tile in which every row has an adapter of its own, one adapter for all."""
+    _check_lora(T, N, K, out, R, n, run, seed=T + N + R, extra=16, w_ready=T % 3 == 0)
+
+
+@pytest.mark.parametrize("T,N,K,R", [(8, 512, 2048, 24), (70, 2048, 528, 64), (300, 512, 1040, 16), (1400, 700, 272, 72)])
+def test_lora_linear_leaves_an_old_workspace_unread(T, N, K, R):
+    """What an earlier call left, NaN in every place, has no part in the result."""
+    dev = need_gpu()
+    g = _gen(dev, 31)
+    x, xs = _codes((T, K), g, dev, 1)
+    w, ws = _codes((N, K), g, dev, 128)
+    a, b, s = _adapters(4, N, K, R, g, dev)
+    ids = _ids(T, 4, 3, g, dev)
+    want, got = torch.empty(T, N, device=dev), torch.empty(T, N, device=dev)
+    need = csa2.lora_workspace_size(T, R)
+    space = torch.zeros(need + 64, dtype=torch.uint8, device=dev)
+    csa2.lora_linear(x, xs, w, ws, a, b, ids, want, adapter_scale=s, ws=space[:need])
+    space.fill_(0xFF)
+    csa2.lora_linear(x, xs, w, ws, a, b, ids, got, adapter_scale=s, ws=space[:need])
+    _sync_ok()
+    assert torch.equal(got, want) and (space[need:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("T", [8, 300, 1400])
+def test_lora_linear_graphs_may_share_a_workspace(T):
+    """Two captured calls with one workspace, replayed in turn, and an eager one between."""
+    dev = need_gpu()
+    g = _gen(dev, 33)
+    K, N, R = 1040, 512, 64
+    sets, want, graphs, outs = [], [], [], []
+    space = torch.empty(csa2.lora_workspace_size(T, R), dtype=torch.uint8, device=dev)
+    for k in range(2):
+        x, xs = _codes((T, K), g, dev, 1)
+        w, ws = _codes((N, K), g, dev, 128)
+        a, b, s = _adapters(5, N, K, R, g, dev)
+        sets.append((x, xs, w, ws, a, b, _ids(T, 5, 2, g, dev)))
+        want.append(torch.empty(T, N, device=dev))
+        csa2.lora_linear(*sets[k], want[k])
+        torch.cuda.synchronize()
+        outs.append(torch.empty(T, N, device=dev))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[k]):
+            for _ in range(3):
+                csa2.lora_linear(*sets[k], outs[k], ws=space)
+    eager = torch.empty(T, N, device=dev)
+    for _ in range(5):
+        for k in (0, 1):
+            graphs[k].replay()
+            csa2.lora_linear(*sets[1 - k], eager, ws=space)
+            assert torch.equal(outs[k], want[k]) and torch.equal(eager, want[1 - k])
+    _sync_ok()
+
+
+def test_rows_further_apart_than_32_bits():
+    """Row strides that put the last row past 2^32 bytes and 2^31 elements."""
+    dev = need_gpu()
+    g = _gen(dev, 35)
+    T, K, far = 6, 2048, (1 << 29) - 64
+    room = torch.empty(2 * ((T - 1) * far + K), dtype=torch.uint8, device=dev)
+    wide = torch.as_strided(room.view(torch.bfloat16), (T, K), (far, 1))
+    x = (0.5 * torch.randn(T, K, generator=g, device=dev)).to(torch.bfloat16)
+    # residual and log probabilities
+    wide.copy_(x)
+    res, gamma = torch.randn(T, K, generator=g, device=dev), torch.ones(K, device=dev)
+    r_out, y = torch.empty_like(res), torch.empty_like(x)
+    csa2.add_norm_fp8(wide, res, r_out, gamma, y=y)
+    _sync_ok()
+    _check_norm(x, res, gamma, 1e-6, r_out, None, None, y)
+    wide.zero_()
+    csa2.add_norm_fp8(x, x, wide, gamma, y=y)      # x and the residual may be one tensor
+    _sync_ok()
+    assert torch.equal(wide, 2 * x)
+    csa2.add_norm_fp8(x, res, r_out, gamma, y=wide)
+    _sync_ok()
+    _check_norm(x, res, gamma, 1e-6, r_out, None, None, wide)
+    _check_logprobs(wide, torch.tensor([1, 2047, 5, -1, 7, 9], dtype=torch.int32, device=dev), 4)
+    # the adapters' projection
+    codes, xs = _codes((T, K), g, dev, 1)
+    w, ws = _codes((256, K), g, dev, 128)
+    a, b, s = _adapters(2, 256, K, 16, g, dev)
+    ids = torch.tensor([1, 0, 1, -1, 0, 1], dtype=torch.int32, device=dev)
+    apart = torch.as_strided(room, (T, K), (2 * far, 1))
+    apart.copy_(codes)
+    want, got = torch.empty(T, 256, device=dev), torch.empty(T, 256, device=dev)
+    csa2.lora_linear(codes, xs, w, ws, a, b, ids, want, adapter_scale=s)
+    csa2.lora_linear(apart, xs, w, ws, a, b, ids, got, adapter_scale=s)
+    _sync_ok()
+    assert torch.equal(got, want)
+    out = torch.as_strided(room.view(torch.float32), (T, 256), (far // 2, 1))
+    csa2.lora_linear(codes, xs, w, ws, a, b, ids, out, adapter_scale=s)
+    _sync_ok()
+    assert torch.equal(out, want)
+
+
 def test_lora_linear_binding_refuses():
     dev = need_gpu()
     g = _gen(dev, 1)
@@ -412,6 +513,17 @@ def test_logprobs_match_oracle(T, V, n, kind):
     token = torch.randint(-1, V, (T,), generator=g, device=dev, dtype=torch.int32)
     token[0] = int(x[0].float().argmax())
     _check_logprobs(x, token, n, ids_stride=3)
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,V,n", [(3, 512, 9), (3, 513, 9), (759, 1500, 3), (760, 1500, 3), (760, 10000, 0), (760, 10001, 2),
+                                   (76, 8192, 4), (77, 8192, 4), (304, 4000, 5), (305, 4000, 5), (153, 4000, 0), (5, 4095, 6),
+                                   (19, 65536, 6), (38, 65536, 32)])
+def test_logprobs_at_the_edges_of_their_kernels(T, V, n, kind):
+    dev = need_gpu()
+    g = _gen(dev, T + V)
+    x = _logits(T, V, kind, g, dev, mask=0.3)
+    _check_logprobs(x, torch.randint(-1, V, (T,), generator=g, device=dev, dtype=torch.int32), n)
 
 
 @pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
