@@ -52,16 +52,20 @@ template <bool LORA>
 struct LoraParams {};
 template <>
 struct LoraParams<true> {
-  CUtensorMap map_v, map_b;  // inner products [planes T, pitch], b [adapters N, rank]: row_bytes by a tile's rows or columns
-  const uint16_t* b;
+  // Inner products [planes T, pitch] and b [adapters N, rank], as boxes of a block's row by
+  // a tile's rows or columns: of the runs of 64 ranks, and of the last one if it is shorter.
+  CUtensorMap map_v, map_b, map_v_last, map_b_last;
   const int* row_adapter;
   const int* lists;
   int list_stride;
   int rank;
-  int row_bytes;  // of a block of b in shared memory: 128, or 32 or 64 for all of rank 16 or 32
-  int pieces;     // blocks of an adapter: 64 ranks each, times planes of v
+  int pieces;  // blocks of an adapter: 64 ranks each, times planes of v
   int planes;
 };
+// Bytes of a row of v or b of some ranks in shared memory.  The least that hold them: a box
+// whose rows end far past the matrix's costs time (64 x 2,048 x 32,768 with 8 adapters of
+// rank 8: 43 us with 128, 26 with 32), though less than plain copies of the rows (50 us).
+__host__ __device__ __forceinline__ int lora_row_bytes(int ranks) { return ranks <= 16 ? 32 : ranks <= 32 ? 64 : 128; }
 // Block i of a tile's adapters: the adapter, where its ranks start, how many there are,
 // and where its plane of v starts.
 struct LoraBlock {
@@ -74,71 +78,13 @@ struct LoraBlock {
     v_row = k % lo.planes * T;
   }
   __device__ __forceinline__ int steps() const { return (ranks + 15) >> 4; }  // products of 16 ranks
-};
-// The b of a block by plain copies, into the swizzled rows of 128 bytes that tensor copies
-// write, by a whole warp: for runs of ranks that are not a row of 32, 64 or 128 bytes.  A
-// tensor copy of 128-byte rows that end before costs more (64 x 2,048 x 32,768 with 8
-// adapters of rank 8: 43 us, 28 so).  8 ranks without a partner are joined by 8 zeros.
-__device__ __forceinline__ void copy_b_rows(uint8_t* dst, const LoraParams<true>& lo, const LoraBlock& at, int n0, int rows, int N) {
-  const int lane = threadIdx.x & 31;
-  const int words = at.ranks >> 3, all = at.steps() * 2;  // 16-byte words of a row: b's, and with the zeros
-  const int n = min(rows, N - n0);
-  const uint16_t* src = lo.b + (static_cast<long long>(at.adapter) * N + n0) * lo.rank + at.rank0;
-  // lanes of a row side by side; `all` is 2, 4, 6 or 8
-  const int per = all == 6 ? 8 : all, q = lane % per, step = 32 / per;
-  if (q < all)
-    for (int r = lane / per; r < n; r += step)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * 128 + ((q ^ (r & 7)) * 16))),
-                   "l"(src + static_cast<long long>(r) * lo.rank + min(q, words - 1) * 8), "r"(q < words ? 16 : 0)
-                   : "memory");
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// A producing warp's blocks: v by a tensor copy, b by one or, row by row, by plain copies.
-// A stage's barrier takes two arrivals, one with the tensor copies' bytes, one for b.  A
-// block's plain copies are waited for two blocks later, whatever kind those are: with
-// three, all of the ring's stages would be taken before its products begin.
-struct LoraCopies {
-  uint64_t* pending[2];  // the barriers of the blocks whose plain copies are on their way, oldest first
-  int count = 0;
-  __device__ __forceinline__ void flush() {
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    while (count) arrive();
-  }
-  __device__ __forceinline__ void add(uint8_t* v_dst, uint8_t* b_dst, uint64_t* full, const LoraParams<true>& lo,
-                                      const LoraBlock& at, int t0, int n0, int v_rows, int b_rows, int N, uint64_t policy) {
-    const bool plain = at.ranks * 2 != lo.row_bytes;
-    if ((threadIdx.x & 31) == 0) {
-      mbar_arrive_expect_tx(full, v_rows * kBlockK + (plain ? 0 : b_rows * lo.row_bytes));
-      tma_load_2d(v_dst, &lo.map_v, at.rank0 * 2, at.v_row + t0, full, policy);
-      if (!plain) {
-        tma_load_2d(b_dst, &lo.map_b, at.rank0 * 2, at.adapter * N + n0, full, policy);
-        mbar_arrive(full);
-      }
-    }
-    if (!plain) {
-      if (count == 2) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        arrive();
-      } else {
-        flush();
-      }
-      return;
-    }
-    copy_b_rows(b_dst, lo, at, n0, b_rows, N);
-    if (count == 2) {
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-      arrive();
-    }
-    pending[count++] = full;
-  }
-
- private:
-  __device__ __forceinline__ void arrive() {  // the oldest block's plain copies are done
-    fence_proxy_async_smem();                 // each lane's, before the tensor core reads them
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(pending[0]);
-    pending[0] = pending[1];
-    --count;
+  // Behind the matrix's columns, and in the columns of 8 ranks without a partner, are zeros.
+  __device__ __forceinline__ void copy(const LoraParams<true>& lo, uint8_t* v_dst, uint8_t* b_dst, uint64_t* full, int t0,
+                                       int n0, int v_rows, int b_rows, int N, uint64_t policy) const {
+    const bool last = ranks < 64;
+    mbar_arrive_expect_tx(full, (v_rows + b_rows) * lora_row_bytes(ranks));
+    tma_load_2d(v_dst, last ? &lo.map_v_last : &lo.map_v, rank0 * 2, v_row + t0, full, policy);
+    tma_load_2d(b_dst, last ? &lo.map_b_last : &lo.map_b, rank0 * 2, adapter * N + n0, full, policy);
   }
 };
 
@@ -339,7 +285,7 @@ __device__ __forceinline__ bool accumulate_and_store(const CUtensorMap& map_out,
     }
     if constexpr (LORA) {
       // from shared memory: what is held through the loop above costs it its registers
-      // (4,096 x 2,048 x 32,768 without an adapter: 290 us, 24x so)
+      // (4,096 x 2,048 x 32,768 without an adapter: 290 us, 246 so)
       const int* list = reinterpret_cast<const int*>(smem + Cfg::kOffLists) + (n_tile & 1) * Cfg::kListWords;
       if (!__all_sync(0xffffffffu, wait(&lfull[n_tile & 1], (n_tile >> 1) & 1, s_abort))) return false;
       const int extra = list[0], own = list[4 + kTileM + r];
@@ -493,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *s_abort = 0;
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], LORA ? 2 : 1);
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < NA; ++i) {
@@ -529,12 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kAccWarps) {
     // ------------------------------------------------------------ producer
-    const uint64_t keep = l2_policy_evict_last();
-    long long it = 0;
-    bool ok = true;
-    for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
-      const int n0 = mine.column(tile), t0 = mine.row(tile);
-      if (lane == 0) {
+    if (lane == 0) {
+      const uint64_t keep = l2_policy_evict_last();
+      long long it = 0;
+      bool ok = true;
+      for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
+        const int n0 = mine.column(tile), t0 = mine.row(tile);
         for (int b = 0; b < blocks; ++b, ++it) {
           const int s = static_cast<int>(it % S);
           if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
@@ -542,29 +488,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
           tma_load_2d(dst, &map_x, (mine.b0 + b) * kBlockK, t0, &full[s], keep);
           tma_load_2d(dst + kTileM * kBlockK, &map_w, (mine.b0 + b) * kBlockK, n0, &full[s], keep);
-          if (LORA) mbar_arrive(&full[s]);
+        }
+        if constexpr (LORA) {  // the adapters' blocks
+          if (!ok) break;
+          TileAdapters<SPLIT> adapters(lo, mine);
+          adapters.look(tile);
+          const int extra = adapters.blocks(tile);
+          for (int i = 0; i < extra; ++i, ++it) {
+            const LoraBlock at = adapters.at(i, p.T);
+            const int s = static_cast<int>(it % S);
+            if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
+            uint8_t* dst = smem + s * Cfg::kStageBytes;
+            at.copy(lo, dst, dst + kTileM * kBlockK, &full[s], t0, n0, kTileM, BN, p.N, keep);
+          }
         }
       }
-      if constexpr (LORA) {  // the adapters' blocks, by the whole warp
-        it = __shfl_sync(0xffffffffu, it, 0);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        TileAdapters<SPLIT> adapters(lo, mine);
-        adapters.look(tile);
-        const int extra = adapters.blocks(tile);
-        LoraCopies copies;
-        for (int i = 0; i < extra; ++i) {
-          const LoraBlock at = adapters.at(i, p.T);
-          const int s = static_cast<int>(it % S);
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort)))) break;
-          uint8_t* dst = smem + s * Cfg::kStageBytes;
-          copies.add(dst, dst + kTileM * kBlockK, &full[s], lo, at, t0, n0, kTileM, BN, p.N, keep);
-          ++it;
-        }
-        copies.flush();
-      }
-    }
-    if (lane == 0) {
       if (!ok) {
         *s_abort = 1;
         set_error(p.err, kErrTimeout);
@@ -611,16 +549,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_b = idesc_bf16_f32(kTileM, BN, 0, 0);
         int next = a;  // blocks until this accumulator's next one
         TileAdapters<SPLIT> adapters(lo, mine);
-        const uint64_t b_desc = smem_desc_rows(smem + kTileM * kBlockK, lo.row_bytes);
         for (long long tile = mine.first; tile < mine.tiles && ok; tile += mine.step) {
           adapters.look(tile);
           for (; next < blocks && ok; next += NA) ok = block(codes);
           next -= blocks;
           const int extra = adapters.blocks(tile);
           for (; next < extra && ok; next += NA) {
-            const int steps = adapters.at(next, p.T).steps();
-            ok = block([&](uint64_t ad, uint64_t) {
-              const uint64_t bd = b_desc + s * kStageDesc;
+            const LoraBlock at = adapters.at(next, p.T);
+            const int steps = at.steps(), row = lora_row_bytes(at.ranks);
+            ok = block([&](uint64_t, uint64_t) {
+              const uint64_t ad = smem_desc_rows(smem, row) + s * kStageDesc;
+              const uint64_t bd = smem_desc_rows(smem + kTileM * kBlockK, row) + s * kStageDesc;
               for (int k = 0; k < steps; ++k) umma_bf16(d, ad + 2 * k, bd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
             });
           }
@@ -740,7 +679,6 @@ cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int 
                          cudaStream_t st, const char** why) {
   const csa2_lora_linear_args& a = *l.args;
   const LoraInner to = lora_inner_at(a, l.workspace, rows);
-  lo->b = a.b;
   lo->rank = a.rank;
   lo->row_adapter = a.row_adapter;
   lo->lists = to.lists;
@@ -748,13 +686,18 @@ cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int 
   lo->planes = lora_planes(a.base.out_format);
   lo->pieces = (a.rank + 63) / 64 * lo->planes;
   const uint64_t row = 2 * static_cast<uint64_t>(a.rank);
-  lo->row_bytes = a.rank == 16 || a.rank == 32 ? static_cast<int>(row) : 128;
   const uint64_t v_row = 2 * static_cast<uint64_t>(lora_pitch(a.rank));
-  if (encode_tmap_2d_u8(&lo->map_v, to.v, v_row, lo->planes * static_cast<uint64_t>(a.base.T), v_row, 128, rows) != CUDA_SUCCESS ||
-      encode_tmap_2d_u8(&lo->map_b, a.b, row, static_cast<uint64_t>(a.n_adapters) * a.base.N, row, lo->row_bytes, columns,
-                        lo->row_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
-                        : lo->row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                              : CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS) {
+  const uint64_t v_rows = lo->planes * static_cast<uint64_t>(a.base.T), b_rows = static_cast<uint64_t>(a.n_adapters) * a.base.N;
+  auto encode = [&](int bytes, CUtensorMap* v, CUtensorMap* b) {
+    const CUtensorMapSwizzle swizzle = bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                       : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                     : CU_TENSOR_MAP_SWIZZLE_128B;
+    return encode_tmap_2d_u8(v, to.v, v_row, v_rows, v_row, bytes, rows, swizzle) == CUDA_SUCCESS &&
+           encode_tmap_2d_u8(b, a.b, row, b_rows, row, bytes, columns, swizzle) == CUDA_SUCCESS;
+  };
+  const int last = a.rank & 63;
+  if ((a.rank >= 64 && !encode(128, &lo->map_v, &lo->map_b)) ||
+      (last && !encode(lora_row_bytes(last), &lo->map_v_last, &lo->map_b_last))) {
     *why = "csa2_lora_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
   }
@@ -775,7 +718,7 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
   auto kern = fp8_linear_wide_kernel<BN, OUT, SPLIT, L::kOn>;
   cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT, SPLIT, L::kOn>>(ctx.device, WideCfg<BN, L::kOn>::kSmem);
   if (e != cudaSuccess) return e;
-  LoraParams<L::kOn> lo;
+  LoraParams<L::kOn> lo{};
   e = prepare_lora(lora, &lo, kTileM, BN, SPLIT ? 2 * wide_tiles<BN>(a) : wide_tiles<BN>(a), ctx, st, why);
   if (e != cudaSuccess) return e;
   const long long tiles = wide_tiles<BN>(a);
@@ -845,7 +788,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   if (threadIdx.x == 0) {
     *s_abort = 0;
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], LORA ? 2 : 1);
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < NA; ++i) {
@@ -858,7 +801,6 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     if (LORA || p.w_ready) {  // the first weights do not wait for the previous launch
       for (int b = 0; b < min(S, blocks); ++b) {
         mbar_arrive_expect_tx(&full[b], Cfg::kStageBytes);
-        if (LORA) mbar_arrive(&full[b]);
         tma_load_2d(smem + b * Cfg::kStageBytes, &map_w, (b0 + b) * kBlockK, n0, &full[b], pol_w);
       }
     }
@@ -879,41 +821,30 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   bool ok = true;
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    int b = 0;
     if (lane == 0) {
+      int b = 0;
       for (; b < blocks; ++b) {
         const int s = b % S;
         if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
         uint8_t* dst = smem + s * Cfg::kStageBytes;
         if (b >= S || !(LORA || p.w_ready)) {
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
-          if (LORA) mbar_arrive(&full[s]);
           tma_load_2d(dst, &map_w, (b0 + b) * kBlockK, n0, &full[s], pol_w);
         }
         tma_load_2d(dst + 128 * kBlockK, &map_x, (b0 + b) * kBlockK, t0, &full[s], pol_x);
       }
-    }
-    if constexpr (LORA) {  // the adapters' blocks, by the whole warp
-      b = __shfl_sync(0xffffffffu, b, 0);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (ok) {
-        pdl_wait();
+      if constexpr (LORA) {  // the adapters' blocks
+        if (ok) pdl_wait();
         const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
-        const int extra = list[0] * lo.pieces;
-        LoraCopies copies;
+        const int extra = ok ? list[0] * lo.pieces : 0;
         for (int i = rank; i < extra; i += splits, ++b) {
           const LoraBlock at(lo, list, i, p.T);
           const int s = b % S;
-          if (b >= S &&
-              !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))))
-            break;
+          if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
           uint8_t* dst = smem + s * Cfg::kStageBytes;
-          copies.add(dst + 128 * kBlockK, dst, &full[s], lo, at, t0, n0, NT, 128, p.N, pol_x);
+          at.copy(lo, dst + 128 * kBlockK, dst, &full[s], t0, n0, NT, 128, p.N, pol_x);
         }
-        copies.flush();
       }
-    }
-    if (lane == 0) {
       if (!ok) {
         *s_abort = 1;
         set_error(p.err, kErrTimeout);
@@ -947,9 +878,11 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
         if (ok) pdl_wait();
         const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
         for (int i = rank; ok && i < list[0] * lo.pieces; i += splits) {
-          const int steps = LoraBlock(lo, list, i, p.T).steps();
-          ok = block([&](uint32_t d, uint64_t, uint64_t xd) {
-            const uint64_t wd = smem_desc_rows(smem + (b % S) * Cfg::kStageBytes, lo.row_bytes);
+          const LoraBlock at(lo, list, i, p.T);
+          const int steps = at.steps(), row = lora_row_bytes(at.ranks);
+          ok = block([&](uint32_t d, uint64_t, uint64_t) {
+            const uint64_t wd = smem_desc_rows(smem + (b % S) * Cfg::kStageBytes, row);
+            const uint64_t xd = smem_desc_rows(smem + (b % S) * Cfg::kStageBytes + 128 * kBlockK, row);
             for (int k = 0; k < steps; ++k) umma_bf16(d, wd + 2 * k, xd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
           });
         }
@@ -1231,7 +1164,7 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
     *why = "csa2_fp8_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
   }
-  LoraParams<L::kOn> lo;
+  LoraParams<L::kOn> lo{};
   e = prepare_lora(lora, &lo, NT, 128, tiles * splits, ctx, st, why);
   if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, p, lo);
