@@ -953,28 +953,32 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
       for (int i = (blocks + group) & 1; i < extra && ok; i += 2) {  // the block's parity is the group, as above
         const int b = blocks + i, a = b % NA;
         const int adapter = LoraBlock(lo, list, rank + i * splits, p.T).adapter;
+        uint32_t rows[(NT + 31) / 32];  // a bit for each row that has the adapter
+#pragma unroll
+        for (int h = 0; h < (NT + 31) / 32; ++h)
+          rows[h] = __ballot_sync(0xffffffffu, h * 32 + lane < NT && s_adapter[h * 32 + lane] == adapter);
         ok = __all_sync(0xffffffffu, mbar_wait(&tfull[a], static_cast<uint32_t>(b / NA) & 1u, s_abort));
         if (!ok) break;
         tc_fence_after();
         if (quad == 0 && lane == 0) mbar_arrive(&empty[b % S]);
 #pragma unroll
         for (int c = 0; c < NT / 16; ++c) {
+          const uint32_t mine = rows[c / 2] >> (c % 2 * 16);
+          if (!(mine & 0xFFFFu)) continue;
           uint32_t v[16];
           tmem_ld32x16_async(taddr + a * NT + c * 16, v);
           tmem_wait_ld16(v);
-          if (c + 1 == NT / 16) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[a]);
-          }
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {  // another row's products are left alone, whatever they are
             float2 f = unpack_f32x2(acc[c * 8 + k / 2]);
-            if (s_adapter[c * 16 + k] == adapter) f.x += __uint_as_float(v[k]);
-            if (s_adapter[c * 16 + k + 1] == adapter) f.y += __uint_as_float(v[k + 1]);
+            if (mine >> k & 1u) f.x += __uint_as_float(v[k]);
+            if (mine >> (k + 1) & 1u) f.y += __uint_as_float(v[k + 1]);
             acc[c * 8 + k / 2] = pack_f32x2(f.x, f.y);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[a]);
       }
     }
     if (!ok) {
