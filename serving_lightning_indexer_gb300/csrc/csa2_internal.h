@@ -175,19 +175,19 @@ cudaError_t launch_quant_fp8(const csa2_quant_fp8_args& a, cudaStream_t st);
 // Projection on e4m3 codes with block scales.
 cudaError_t launch_fp8_linear(const csa2_fp8_linear_args& a, const DeviceCtx& ctx, cudaStream_t st, const char** why);
 // Low-rank adapters beside it: where their inner products [planes][T][pitch] and the lists
-// of adapters of each tile of tile_rows rows ([tile][tile_rows + 4]: how many, then,
-// from the fourth word on, which) are in the workspace, and the launch that writes them.
+// of adapters of each 128 rows (kLoraListWords: how many, then, from the fifth on, which;
+// NULL for none) are in the workspace, and the launch that writes them.
 struct LoraInner {
   uint16_t* v;
   int* lists;
-  int tile_rows;
 };
 constexpr int kLoraMaxRows = 1 << 20;
+constexpr int kLoraListWords = 132;
 constexpr int kLoraPlanes = 3;  // at most; the inner products' bf16 parts by the output's format
 inline int lora_planes(int out_format) { return out_format == CSA2_OUT_BF16 ? 1 : out_format == CSA2_OUT_F32 ? 2 : kLoraPlanes; }
 inline int lora_pitch(int rank) { return (rank + 63) / 64 * 64; }  // rows of whole 128-byte words
 size_t lora_workspace_bytes(int T, int rank);
-LoraInner lora_inner_at(const csa2_lora_linear_args& a, void* ws, int tile_rows);
+LoraInner lora_inner_at(const csa2_lora_linear_args& a, void* ws, bool lists);
 // ctas: of the projection that follows.
 cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& to, int ctas, const DeviceCtx& ctx,
                               cudaStream_t st, const char** why);

@@ -56,9 +56,8 @@ struct LoraParams<true> {
   // a tile's rows or columns: of the runs of 64 ranks, and of the last one if it is shorter.
   CUtensorMap map_v, map_b, map_v_last, map_b_last;
   const int* row_adapter;
-  const int* lists;
-  int list_stride;
-  int rank;
+  const int* lists;  // of tiles of 128 rows, kLoraListWords each; a tile of fewer makes its own
+  int n_adapters, rank;
   int pieces;  // blocks of an adapter: 64 ranks each, times planes of v
   int planes;
 };
@@ -78,15 +77,44 @@ struct LoraBlock {
     v_row = k % lo.planes * T;
   }
   __device__ __forceinline__ int steps() const { return (ranks + 15) >> 4; }  // products of 16 ranks
-  // Behind the matrix's columns, and in the columns of 8 ranks without a partner, are zeros.
-  __device__ __forceinline__ void copy(const LoraParams<true>& lo, uint8_t* v_dst, uint8_t* b_dst, uint64_t* full, int t0,
-                                       int n0, int v_rows, int b_rows, int N, uint64_t policy) const {
-    const bool last = ranks < 64;
+  __device__ __forceinline__ void expect(uint64_t* full, int v_rows, int b_rows) const {
     mbar_arrive_expect_tx(full, (v_rows + b_rows) * lora_row_bytes(ranks));
-    tma_load_2d(v_dst, last ? &lo.map_v_last : &lo.map_v, rank0 * 2, v_row + t0, full, policy);
-    tma_load_2d(b_dst, last ? &lo.map_b_last : &lo.map_b, rank0 * 2, adapter * N + n0, full, policy);
+  }
+  __device__ __forceinline__ void copy_v(const LoraParams<true>& lo, uint8_t* dst, uint64_t* full, int t0, uint64_t policy) const {
+    tma_load_2d(dst, ranks < 64 ? &lo.map_v_last : &lo.map_v, rank0 * 2, v_row + t0, full, policy);
+  }
+  // Behind b's columns, and in the columns of 8 ranks without a partner, are zeros.
+  __device__ __forceinline__ void copy_b(const LoraParams<true>& lo, uint8_t* dst, uint64_t* full, int n0, int N,
+                                         uint64_t policy) const {
+    tma_load_2d(dst, ranks < 64 ? &lo.map_b_last : &lo.map_b, rank0 * 2, adapter * N + n0, full, policy);
   }
 };
+// The adapters among a tile's NT rows, each once, in the order of their first rows, and the
+// rows' own, by a warp: list[0] how many, list[4 ..] which; own: -1 for none or no row.
+template <int NT>
+__device__ __forceinline__ void tile_adapters(const LoraParams<true>& lo, int t0, int T, int* list, int* own) {
+  const int lane = threadIdx.x & 31;
+  int count = 0;
+#pragma unroll
+  for (int h = 0; h < (NT + 31) / 32; ++h) {
+    const int row = h * 32 + lane;
+    int id = row < NT && t0 + row < T ? __ldg(lo.row_adapter + t0 + row) : -1;
+    if (id < 0 || id >= lo.n_adapters) id = -1;
+    if (row < NT) own[row] = id;
+    const uint32_t same = __match_any_sync(0xffffffffu, id);  // all lanes take part
+    bool first = id >= 0 && __ffs(same) - 1 == lane;
+    for (int j = 0; j < h * 32; j += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(own + j);
+      first = first & (v.x != id) & (v.y != id) & (v.z != id) & (v.w != id);
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, first);
+    if (first) list[4 + count + __popc(mask & ((1u << lane) - 1))] = id;
+    count += __popc(mask);
+    __syncwarp();
+  }
+  if (lane == 0) list[0] = count;
+  __syncwarp();
+}
 
 // What a launch has to know of its adapters on the host.
 struct NoLora {
@@ -208,7 +236,7 @@ struct TileAdapters {
   int count;
   __device__ __forceinline__ TileAdapters(const LoraParams<true>& lo, const Share<256, SPLIT>& mine) : lo(lo), mine(mine) {}
   __device__ __forceinline__ void look(long long tile) {
-    list = lo.lists + static_cast<long long>(mine.row(tile) / kTileM) * lo.list_stride;
+    list = lo.lists + static_cast<long long>(mine.row(tile) / kTileM) * kLoraListWords;
     if (tile != mine.first) count = list[0];
   }
   __device__ __forceinline__ int blocks(long long tile) {
@@ -499,7 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = static_cast<int>(it % S);
             if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
             uint8_t* dst = smem + s * Cfg::kStageBytes;
-            at.copy(lo, dst, dst + kTileM * kBlockK, &full[s], t0, n0, kTileM, BN, p.N, keep);
+            at.expect(&full[s], kTileM, BN);
+            at.copy_v(lo, dst, &full[s], t0, keep);
+            at.copy_b(lo, dst + kTileM * kBlockK, &full[s], n0, p.N, keep);
           }
         }
       }
@@ -622,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++n_tile;
         int* dst = reinterpret_cast<int*>(smem + Cfg::kOffLists) + slot * Cfg::kListWords;
-        const int* src = lo.lists + static_cast<long long>(t0 / kTileM) * lo.list_stride;
+        const int* src = lo.lists + static_cast<long long>(t0 / kTileM) * kLoraListWords;
         const int count = mine.adapters_too() ? src[0] : 0;
         if (lane == 0) dst[0] = count * lo.pieces;
 #pragma unroll
@@ -670,19 +700,20 @@ long long wide_tiles(const csa2_fp8_linear_args& a) {
   return ((static_cast<long long>(a.T) + kTileM - 1) / kTileM) * ((static_cast<long long>(a.N) + BN - 1) / BN);
 }
 
-// With adapters: their inner products and lists are launched first, for tiles of
-// `rows` rows and `columns` columns, and described to the projection.  Nothing without.
+// With adapters: their inner products, and the lists of tiles of 128 rows, are launched
+// first and described to the projection with tiles of `rows` rows and `columns` columns.
+// Nothing without.
 cudaError_t prepare_lora(const NoLora&, LoraParams<false>*, int, int, long long, const DeviceCtx&, cudaStream_t, const char**) {
   return cudaSuccess;
 }
 cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int columns, long long ctas, const DeviceCtx& ctx,
                          cudaStream_t st, const char** why) {
   const csa2_lora_linear_args& a = *l.args;
-  const LoraInner to = lora_inner_at(a, l.workspace, rows);
+  const LoraInner to = lora_inner_at(a, l.workspace, rows == kTileM);
+  lo->n_adapters = a.n_adapters;
   lo->rank = a.rank;
   lo->row_adapter = a.row_adapter;
   lo->lists = to.lists;
-  lo->list_stride = rows + 4;
   lo->planes = lora_planes(a.base.out_format);
   lo->pieces = (a.rank + 63) / 64 * lo->planes;
   const uint64_t row = 2 * static_cast<uint64_t>(a.rank);
@@ -760,7 +791,9 @@ struct NarrowCfg {
   static constexpr int kCols = kAccs * NT < 32 ? 32 : kAccs * NT;
   static constexpr int kOffScales = kStages * kStageBytes;  // the parts [NT][128] reuse the stages
   static constexpr int kOffBars = kOffScales + kScaleSeg * NT * 4;
-  static constexpr int kSmem = 1024 + kOffBars + 256 + (LORA ? NT * 4 : 0);
+  // LORA: the tile's adapters and its rows' own
+  static constexpr int kOffLists = kOffBars + 256;
+  static constexpr int kSmem = 1024 + kOffLists + (LORA ? (4 + 2 * NT) * 4 : 0);
   static_assert(NT * 128 * 4 <= kOffScales, "the parts fit the stages");
 };
 
@@ -776,8 +809,11 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
   uint64_t* tempty = tfull + NA;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + NA);
+  uint64_t* lready = tempty + NA;  // LORA: the tile's adapters
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(lready + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_list = reinterpret_cast<int*>(smem + Cfg::kOffLists);  // [4 + NT], then [NT], LORA only
+  int* s_own = s_list + 4 + NT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * 128, t0 = blockIdx.y * NT;
   const int splits = gridDim.z, rank = blockIdx.z;
@@ -795,6 +831,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 4);
     }
+    if (LORA) mbar_init(lready, 1);
     fence_mbar_init();
     prefetch_tmap(&map_x);
     prefetch_tmap(&map_w);
@@ -833,16 +870,29 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
         }
         tma_load_2d(dst + 128 * kBlockK, &map_x, (b0 + b) * kBlockK, t0, &full[s], pol_x);
       }
-      if constexpr (LORA) {  // the adapters' blocks
-        if (ok) pdl_wait();
-        const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
-        const int extra = ok ? list[0] * lo.pieces : 0;
-        for (int i = rank; i < extra; i += splits, ++b) {
-          const LoraBlock at(lo, list, i, p.T);
+      if constexpr (LORA) {  // the adapters' blocks: only v waits for the previous launch
+        ok = ok && mbar_wait(lready, 0u, s_abort);
+        const int extra = ok ? shares_of(s_list[0] * lo.pieces, rank, splits) : 0;
+        const int ahead = min(extra, S);
+        for (int i = 0; i < ahead; ++i, ++b) {
           const int s = b % S;
           if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
-          uint8_t* dst = smem + s * Cfg::kStageBytes;
-          at.copy(lo, dst + 128 * kBlockK, dst, &full[s], t0, n0, NT, 128, p.N, pol_x);
+          const LoraBlock at(lo, s_list, rank + i * splits, p.T);
+          at.expect(&full[s], NT, 128);
+          at.copy_b(lo, smem + s * Cfg::kStageBytes, &full[s], n0, p.N, pol_x);
+        }
+        if (b > blocks) pdl_wait();
+        for (int i = 0; blocks + i < b; ++i) {
+          const int s = (blocks + i) % S;
+          LoraBlock(lo, s_list, rank + i * splits, p.T).copy_v(lo, smem + s * Cfg::kStageBytes + 128 * kBlockK, &full[s], t0, pol_x);
+        }
+        for (int i = ahead; ok && i < extra; ++i, ++b) {
+          const int s = b % S;
+          if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
+          const LoraBlock at(lo, s_list, rank + i * splits, p.T);
+          at.expect(&full[s], NT, 128);
+          at.copy_b(lo, smem + s * Cfg::kStageBytes, &full[s], n0, p.N, pol_x);
+          at.copy_v(lo, smem + s * Cfg::kStageBytes + 128 * kBlockK, &full[s], t0, pol_x);
         }
       }
       if (!ok) {
@@ -875,10 +925,10 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
         });
       if constexpr (LORA) {
         constexpr uint32_t idesc_b = idesc_bf16_f32(128, NT, 0, 0);
-        if (ok) pdl_wait();
-        const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
-        for (int i = rank; ok && i < list[0] * lo.pieces; i += splits) {
-          const LoraBlock at(lo, list, i, p.T);
+        ok = ok && mbar_wait(lready, 0u, s_abort);
+        const int extra = ok ? shares_of(s_list[0] * lo.pieces, rank, splits) : 0;
+        for (int i = 0; ok && i < extra; ++i) {
+          const LoraBlock at(lo, s_list, rank + i * splits, p.T);
           const int steps = at.steps(), row = lora_row_bytes(at.ranks);
           ok = block([&](uint32_t d, uint64_t, uint64_t) {
             const uint64_t wd = smem_desc_rows(smem + (b % S) * Cfg::kStageBytes, row);
@@ -902,9 +952,11 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     float* s_scale = reinterpret_cast<float*>(smem + Cfg::kOffScales);  // [block][NT]: both scales
     const float* ws = p.w_scale + static_cast<long long>(n0 >> 7) * p.ld_ws + b0;
     const int tid = threadIdx.x - 64;
-    int* s_adapter = reinterpret_cast<int*>(smem + Cfg::kOffBars + 256);  // [NT], LORA only
     if constexpr (LORA) {
-      if (tid < NT) s_adapter[tid] = t0 + tid < p.T ? __ldg(lo.row_adapter + t0 + tid) : -1;
+      if (warp == 2) {
+        tile_adapters<NT>(lo, t0, p.T, s_list, s_own);
+        if (lane == 0) mbar_arrive(lready);
+      }
     }
     uint64_t acc[NT / 2];
 #pragma unroll
@@ -948,15 +1000,15 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     if constexpr (LORA) {
       pdl_wait();
       pdl_trigger();  // every CTA holds its TMEM
-      const int* list = lo.lists + static_cast<long long>(blockIdx.y) * lo.list_stride;
-      const int extra = shares_of(list[0] * lo.pieces, rank, splits);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(lready, 0u, s_abort));
+      const int extra = ok ? shares_of(s_list[0] * lo.pieces, rank, splits) : 0;
       for (int i = (blocks + group) & 1; i < extra && ok; i += 2) {  // the block's parity is the group, as above
         const int b = blocks + i, a = b % NA;
-        const int adapter = LoraBlock(lo, list, rank + i * splits, p.T).adapter;
+        const int adapter = s_list[4 + (rank + i * splits) / lo.pieces];
         uint32_t rows[(NT + 31) / 32];  // a bit for each row that has the adapter
 #pragma unroll
         for (int h = 0; h < (NT + 31) / 32; ++h)
-          rows[h] = __ballot_sync(0xffffffffu, h * 32 + lane < NT && s_adapter[h * 32 + lane] == adapter);
+          rows[h] = __ballot_sync(0xffffffffu, h * 32 + lane < NT && s_own[h * 32 + lane] == adapter);
         ok = __all_sync(0xffffffffu, mbar_wait(&tfull[a], static_cast<uint32_t>(b / NA) & 1u, s_abort));
         if (!ok) break;
         tc_fence_after();

@@ -1,6 +1,6 @@
 // Inner products of low-rank adapters with the rows that use them,
 //   v[t][r] = s[i] * sum_b x_scale[t][b] * sum_{k in b} x[t][k] a[i][r][k],  i = row_adapter[t],
-// and the list of adapters that each of the projection's row tiles needs.  The
+// and the list of adapters that each 128 rows of the projection need.  The
 // projection (fp8_linear.cu) adds v[t] b[i]^T to its sums before RoPE and rounding.
 //
 // The codes are exact in bf16 and a is bf16, so a block's 128 products are summed by
@@ -30,12 +30,11 @@ struct InnerParams {
   const float* adapter_scale;
   const int* row_adapter;
   uint16_t* v;  // [planes][T][pitch]: the bf16 values, what they leave, and what that leaves
-  int* lists;
+  int* lists;  // NULL: the projection's tiles are smaller and make their own
   long long ld_x, ld_xs;
   int T, K, rank, pitch, n_adapters;
-  int tile_rows;  // rows of the projection's tiles
-  int planes;     // 1, 2 or 3
-  int ready;      // a and row_adapter may be read before the previous launch completes
+  int planes;  // 1, 2 or 3
+  int ready;   // a and row_adapter may be read before the previous launch completes
   uint32_t* err;
 };
 
@@ -56,9 +55,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The adapters among a tile's rows, each once, in the order of their first rows:
-// list[0] how many, list[4 ..] which.  n <= 128 threads of whole warps, all of them.
-__device__ __forceinline__ void write_list(const InnerParams& p, long long t0, int n, int* list, int* s_id, int* s_base) {
+// The adapters among 128 rows, each once, in the order of their first rows: list[0] how
+// many, list[4 ..] which.  All threads, 128 or more.
+__device__ __forceinline__ void write_list(const InnerParams& p, long long t0, int* list, int* s_id, int* s_base) {
+  constexpr int n = 128;
   const int i = threadIdx.x, lane = i & 31;
   int id = -1;
   if (i < n && t0 + i < p.T) {
@@ -120,18 +120,21 @@ __global__ void __launch_bounds__(W * 32) lora_inner_kernel(const __grid_constan
   // the blockIdx.z-th adapter among the 16 rows
   int id = -1;
   if (lane < 16 && t0 + lane < p.T) id = __ldg(p.row_adapter + t0 + lane);
-  if (id >= p.n_adapters) id = -1;
+  if (id < -1 || id >= p.n_adapters) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) set_error(p.err, kErrBounds);
+    id = -1;
+  }
   const uint32_t same = __match_any_sync(0xffffffffu, id);
   uint32_t firsts = __ballot_sync(0xffffffffu, id >= 0 && __ffs(same) - 1 == lane);
   for (int j = blockIdx.z; j > 0; --j) firsts &= firsts - 1;
   const int adapter = __shfl_sync(0xffffffffu, id, firsts ? __ffs(firsts) - 1 : 0);
   if (!p.ready) pdl_trigger();
-  if (blockIdx.y == 0 && blockIdx.z == 0 && t0 % p.tile_rows == 0) {
+  if (p.lists && blockIdx.y == 0 && blockIdx.z == 0 && t0 % 128 == 0) {
     if (p.ready) {  // the last call's projection may still read its lists
       pdl_wait();
       pdl_trigger();
     }
-    write_list(p, t0, p.tile_rows, p.lists + static_cast<long long>(t0 / p.tile_rows) * (p.tile_rows + 4), s_id, s_base);
+    write_list(p, t0, p.lists + static_cast<long long>(t0 / 128) * kLoraListWords, s_id, s_base);
   }
   if (!firsts) {
     if (p.ready) {
@@ -202,29 +205,6 @@ __global__ void __launch_bounds__(W * 32) lora_inner_kernel(const __grid_constan
       float one[1] = {v};
       store_v(p, t0 + i, r0 + r, one);
     }
-  }
-}
-
-// The projection's lists of 128 rows from theirs, by a warp: of each tile, the adapters
-// that one of its rows has, in the order of the whole list.
-__device__ __forceinline__ void write_sub_lists(const InnerParams& p, long long t0, const int* s_list, const int* s_place) {
-  const int lane = threadIdx.x & 31;
-  int* to = p.lists + t0 / p.tile_rows * (p.tile_rows + 4);
-  for (int sub = 0; sub < 128 && t0 + sub < p.T; sub += p.tile_rows, to += p.tile_rows + 4) {
-    uint32_t has[4] = {0, 0, 0, 0};  // a bit for each place in the whole list
-    for (int i = lane; i < p.tile_rows; i += 32) {
-      const int at = s_place[sub + i];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) has[w] |= at >= 0 && at >> 5 == w ? 1u << (at & 31) : 0u;
-    }
-    int count = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t mask = __reduce_or_sync(0xffffffffu, has[w]);
-      if (mask >> lane & 1u) to[4 + count + __popc(mask & ((1u << lane) - 1))] = s_list[4 + w * 32 + lane];
-      count += __popc(mask);
-    }
-    if (lane == 0) to[0] = count;
   }
 }
 
@@ -299,7 +279,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
   const int all = (p.K + 127) / 128;
   const int b0 = all * rank / splits, nb = all * (rank + 1) / splits - b0;
   tc_fence_before();
-  write_list(p, t0, kTileRows, s_list, s_id, s_base);
+  write_list(p, t0, s_list, s_id, s_base);
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int n = s_list[0];
@@ -506,7 +486,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
     __syncwarp();
     if (p.ready) pdl_wait();
     pdl_trigger();
-    if (rank == 0 && blockIdx.z == 0) write_sub_lists(p, t0, s_list, s_place);
+    if (p.lists && rank == 0 && blockIdx.z == 0)
+      for (int i = lane; i < 4 + n; i += 32) p.lists[t0 / kTileRows * kLoraListWords + i] = s_list[i];
   }
   tc_fence_before();
   __syncwarp();
@@ -546,7 +527,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
 
 }  // namespace
 
-// The lists for any tile height: (rows + 4) words a tile of 16, 32, 64 or 128 rows.
+// The lists, kLoraListWords for each 128 rows, in 80 bytes for each 16.
 static size_t lists_offset(int T, int rank) {
   return (2 * kLoraPlanes * static_cast<size_t>(T) * lora_pitch(rank) + 255) & ~static_cast<size_t>(255);
 }
@@ -554,16 +535,17 @@ size_t lora_workspace_bytes(int T, int rank) {
   return lists_offset(T, rank) + (static_cast<size_t>(T) + 15) / 16 * 80 + 528;
 }
 
-LoraInner lora_inner_at(const csa2_lora_linear_args& a, void* ws, int tile_rows) {
+LoraInner lora_inner_at(const csa2_lora_linear_args& a, void* ws, bool lists) {
   uint8_t* base = static_cast<uint8_t*>(ws);
-  return LoraInner{reinterpret_cast<uint16_t*>(base), reinterpret_cast<int*>(base + lists_offset(a.base.T, a.rank)), tile_rows};
+  return LoraInner{reinterpret_cast<uint16_t*>(base),
+                   lists ? reinterpret_cast<int*>(base + lists_offset(a.base.T, a.rank)) : nullptr};
 }
 
 cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& to, int ctas, const DeviceCtx& ctx,
                               cudaStream_t st, const char** why) {
   const csa2_fp8_linear_args& l = a.base;
   const InnerParams p{l.x, l.x_scale, a.a, a.adapter_scale, a.row_adapter, to.v, to.lists, l.ld_x, l.ld_x_scale, l.T, l.K,
-                      a.rank, lora_pitch(a.rank), a.n_adapters, to.tile_rows, lora_planes(l.out_format), l.w_ready,
+                      a.rank, lora_pitch(a.rank), a.n_adapters, lora_planes(l.out_format), l.w_ready,
                       ctx.err};
   const int tiles = (l.T + kTileRows - 1) / kTileRows, runs = (a.rank + kTileRanks - 1) / kTileRanks, blocks = (l.K + 127) / 128;
   // 8 ranks without a partner get 8 zeros beside them: products are of 16
