@@ -12,7 +12,9 @@
 // LORA: each adapter that a tile's rows use (lora.cu lists them) brings one to three more
 // blocks for every 64 ranks, bf16 products of the rows' inner products with the
 // adapter's b, summed like the others but only to the rows that have the adapter.  The
-// projection's own blocks come first, and only what lora.cu wrote waits for it.
+// projection's own blocks come first, and only what lora.cu wrote waits for it.  4,096 x
+// 2,048 x 32,768 with 4 adapters of rank 64: 268 us, 249 without adapters; 64 rows with 16
+// of rank 32: 25.3 us, 16.2 without, of which b's bytes are 5.
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -62,7 +64,7 @@ struct LoraParams<true> {
   int planes;
 };
 // Bytes of a row of v or b of some ranks in shared memory.  The least that hold them: a box
-// whose rows end far past the matrix's costs time (64 x 2,048 x 32,768 with 8 adapters of
+// whose rows end far past the matrix's costs time (64 x 2,048 x 32,768 with 16 adapters of
 // rank 8: 43 us with 128, 26 with 32), though less than plain copies of the rows (50 us).
 __host__ __device__ __forceinline__ int lora_row_bytes(int ranks) { return ranks <= 16 ? 32 : ranks <= 32 ? 64 : 128; }
 // Block i of a tile's adapters: the adapter, where its ranks start, how many there are,

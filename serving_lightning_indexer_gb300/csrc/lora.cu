@@ -10,10 +10,13 @@
 // its border is 2^-3 off however near the border was (two leave three times the codes on
 // the other side that fp32's own roundings do).
 //
-// Two kernels.  Up to 16 rows: a CTA takes one of their adapters and 8 of its ranks, its
-// 16 warps the blocks of 128 input dims in turn, added in warp order.  More rows: a CTA
-// takes 128 of them, 64 ranks and a share of the input dims, and goes through the tile's
-// adapters with a in a ring in shared memory; a cluster adds the shares in rank order.
+// Two kernels, both bound by latency: launch, ids, operands, products, sums.  For few rows
+// a CTA takes 16 of them, one of their adapters and 8 of its ranks, its 16 or 32 warps the
+// blocks of 128 input dims in turn, added in warp order: 8 x 7,168 x 512 with 8 adapters
+// takes 8.4 us with its projection, 4.7 without adapters.  For many a CTA takes 128 rows,
+// 64 ranks and a share of the input dims, and goes through the tile's adapters with a in a
+// ring in shared memory; a cluster adds the shares in rank order: about 12 us of the 268 of
+// 4,096 x 2,048 x 32,768 at rank 64.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -551,8 +554,8 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
   // 8 ranks without a partner get 8 zeros beside them: products are of 16
   const dim3 grid((l.T + 15) / 16, (a.rank + 15) / 16 * 2, a.n_adapters < 16 ? a.n_adapters : 16);
   // The small CTAs while they run in a wave or two (an SM holds two), by the most adapters
-  // that 16 rows can have: 333 x 1,360 x 1,001 with 5 of rank 24 take 13.9 us, 17 with the
-  // tiles; 64 x 2,048 x 32,768 with 16 of rank 64: 31.9 and 30.7.
+  // that 16 rows can have: 333 x 1,360 x 1,001 with 5 of rank 24 take 11.8 us, 13.4 with the
+  // tiles; 64 x 2,048 x 32,768 with 16 of rank 64: 31.6 and 29.5.
   if (static_cast<long long>(grid.x) * grid.y * grid.z <= 3LL * ctx.num_sms)
     return blocks > 16 ? launch_pdl(lora_inner_kernel<32>, grid, dim3(1024), 0, st, p)
                        : launch_pdl(lora_inner_kernel<16>, grid, dim3(512), 0, st, p);
