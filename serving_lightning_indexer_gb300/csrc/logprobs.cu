@@ -49,6 +49,7 @@ constexpr float kLowest = -1.2676506e30f;  // -2^100, exact in bf16
 template <int NW>
 constexpr int kMaxList = NW == 1 ? 256 : 1024;
 constexpr int kMaxTied = 128;
+constexpr int kMaxSplits = 16;  // CTAs of a row
 constexpr float kLargestFloat = 3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFar = -200.f;  // e^x is 0 in fp32 from -104 on
@@ -91,6 +92,16 @@ __device__ __forceinline__ Sums merge(Sums a, Sums b) {
   a.r += s * f;
   a.w += (b.w + s * d) * f;
   return a;
+}
+
+// The N first lanes' sums merged, in every lane.
+template <int N>
+__device__ __forceinline__ Sums merge_lanes(Sums a) {
+#pragma unroll
+  for (int o = 1; o < N; o <<= 1)
+    a = merge(a, Sums{__shfl_down_sync(0xffffffffu, a.m, o), __shfl_down_sync(0xffffffffu, a.r, o),
+                      __shfl_down_sync(0xffffffffu, a.w, o)});
+  return Sums{__shfl_sync(0xffffffffu, a.m, 0), __shfl_sync(0xffffffffu, a.r, 0), __shfl_sync(0xffffffffu, a.w, 0)};
 }
 
 // The place of a lane's item, if it has one, at the end of a row's list of *count.  The
@@ -354,7 +365,7 @@ struct Word {
 // A row is NW warps' work: one warp's, or a CTA's, or that of a cluster of `splits` CTAs,
 // each with a run of its words.  A thread copies its words ahead into places of its own
 // in shared memory, so the pass has no barrier.
-template <bool F32, bool TOP, int NW, bool DEEP>
+template <bool F32, bool TOP, int NW, bool DEEP, bool SPLIT>
 __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_constant__ LogprobParams p, int T, int splits) {
   constexpr int kEl = Row<F32>::kEl, B = kBatch<F32>, S = kStages<F32, DEEP>, kThreads = NW * 32, kRows = kLpWarps / NW;
   constexpr uint32_t kNone = F32 ? 0xFF800000u : 0xFF80FF80u;
@@ -371,9 +382,9 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
   pdl_wait();
   pdl_trigger();
   const int mine = NW == 1 ? threadIdx.x >> 5 : 0;  // of the CTA's rows
-  const long long t = NW == 1 ? static_cast<long long>(blockIdx.x) * kRows + mine : blockIdx.x / splits;
+  const long long t = NW == 1 ? static_cast<long long>(blockIdx.x) * kRows + mine : SPLIT ? blockIdx.x / splits : blockIdx.x;
   if (NW == 1 && t >= T) return;
-  const int rank = NW == 1 ? 0 : blockIdx.x % splits;
+  const int rank = SPLIT ? blockIdx.x % splits : 0;
   const int tid = threadIdx.x % kThreads, warp = tid >> 5, lane = tid & 31;
   uint4* s_ring = s_all + mine * kRing;
   unsigned long long(*s_lists)[32] = reinterpret_cast<unsigned long long(*)[32]>(s_ring);
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
   int &s_count = s_counts[mine], &s_tied_count = s_tied_counts[mine];
   float& s_tau = s_taus[mine];
   const Row<F32> row(p.logits, t * p.ld, p.V);
-  const int share = (row.n + splits - 1) / splits;
+  const int share = SPLIT ? (row.n + splits - 1) / splits : row.n;
   const int first = min(row.n, rank * share), words = min(row.n, first + share) - first;
   const int batches = (words + kThreads * B - 1) / (kThreads * B);
   const int run_batches = max(kRunBatches<NW>, (batches + kMaxRuns - 1) / kMaxRuns);
@@ -498,15 +509,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
   if (NW > 1 && lane == 0) s_sums[warp] = all;
   if (tid == 0) s_count = s_tied_count = 0;
   sync_row<NW>();
-  if (NW > 1 && warp == 0) {
-    all = Sums{-INFINITY, 0.f, 0.f};
-    if (lane < NW) all = s_sums[lane];
-#pragma unroll
-    for (int o = 1; o < NW; o <<= 1)
-      all = merge(all, Sums{__shfl_down_sync(0xffffffffu, all.m, o), __shfl_down_sync(0xffffffffu, all.r, o),
-                            __shfl_down_sync(0xffffffffu, all.w, o)});
-    all = Sums{__shfl_sync(0xffffffffu, all.m, 0), __shfl_sync(0xffffffffu, all.r, 0), __shfl_sync(0xffffffffu, all.w, 0)};
-  }
+  if (NW > 1 && warp == 0) all = merge_lanes<NW>(lane < NW ? s_sums[lane] : Sums{-INFINITY, 0.f, 0.f});
 
   // ---- the best of these logits, descending over the first warp's lanes
   unsigned long long list = 0;
@@ -577,20 +580,26 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
   }
 
   // ---- the cluster's CTAs
-  if (NW > 1 && splits > 1) {
+  if constexpr (SPLIT) {
+    static_assert(kMaxSplits <= 2 * NW, "a warp joins two CTAs' lists");
     if (tid == 0) s_part = all;
     if (TOP && warp == 0) s_best[lane] = list;
     __syncwarp();
     cluster_sync();
     if (rank == 0) {
-      if (warp == 0)
-        for (int i = 1; i < splits; ++i) {
-          const uint32_t at = map_rank(smem_u32(&s_part), static_cast<uint32_t>(i));
-          all = merge(all, Sums{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
+      if (warp == 0) {
+        all = Sums{-INFINITY, 0.f, 0.f};
+        if (lane < splits) {
+          const uint32_t at = map_rank(smem_u32(&s_part), static_cast<uint32_t>(lane));
+          all = Sums{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)};
         }
+        all = merge_lanes<kMaxSplits>(all);
+      }
       if (TOP) {
         list = 0;
         if (warp < splits) list = ld_cluster_u64(map_rank(smem_u32(&s_best[lane]), static_cast<uint32_t>(warp)));
+        if (warp + NW < splits)
+          list = merge_best(list, ld_cluster_u64(map_rank(smem_u32(&s_best[31 - lane]), static_cast<uint32_t>(warp + NW))));
         list = join_lists<NW>(list, s_lists, p.n);
       }
     }
@@ -608,14 +617,19 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
     }
   }
   __syncwarp();
-  if (NW > 1 && splits > 1) cluster_sync();  // no CTA leaves while its part may still be read
+  if (SPLIT) cluster_sync();  // no CTA leaves while its part may still be read
 }
 
-template <bool F32, bool TOP, int NW, bool DEEP>
+template <bool F32, bool TOP, int NW, bool DEEP, bool SPLIT>
 cudaError_t launch(const LogprobParams& p, int T, int splits, const DeviceCtx& ctx, cudaStream_t st) {
   constexpr int kSmem = kRingBytes<F32, DEEP>;
-  cudaError_t e = prefer_max_smem_once<logprobs_kernel<F32, TOP, NW, DEEP>>(ctx.device, kSmem);
+  constexpr auto kern = logprobs_kernel<F32, TOP, NW, DEEP, SPLIT>;
+  cudaError_t e = prefer_max_smem_once<kern>(ctx.device, kSmem);
   if (e != cudaSuccess) return e;
+  if (splits > 8) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(NW == 1 ? (T + kLpWarps - 1) / kLpWarps : T * splits);
   cfg.blockDim = dim3(kLpThreads);
@@ -629,8 +643,8 @@ cudaError_t launch(const LogprobParams& p, int T, int splits, const DeviceCtx& c
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<F32, TOP, NW, DEEP>, p, T, splits);
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, T, splits);
 }
 
 template <bool F32, bool TOP>
@@ -638,19 +652,23 @@ cudaError_t launch_type(const LogprobParams& p, int T, const DeviceCtx& ctx, cud
   // A warp a row where the rows are short and many: 2,048 rows of 1,000 fp32 logits with
   // 5 alternatives take 6.9 us, 18.5 with a CTA each; 2,048 of 10,000: 21.8 and 27.4; 333
   // of 2,000: 8.5 and 6.1; 700 of 10,000: 13.5 and 11.3; 2,048 of 20,000: 43 and 37.
-  if (p.V <= 512 || (p.V <= 10000 && T >= 5 * ctx.num_sms)) return launch<F32, TOP, 1, false>(p, T, 1, ctx, st);
-  // A cluster a row where the rows leave SMs idle, down to 4,096 logits a CTA (8 rows of
-  // 131,072 fp32 logits with 20 alternatives: 8.4 us split by 8, 15.5 whole; 64 rows: 12.7
-  // by 4, 16.9 whole; 128 rows: 18.7 by 2, 16.9 whole).
+  if (p.V <= 512 || (p.V <= 10000 && T >= 5 * ctx.num_sms)) return launch<F32, TOP, 1, false, false>(p, T, 1, ctx, st);
+  // A cluster a row where the rows leave SMs idle, down to 2,048 logits a CTA (64 rows of
+  // 131,072 fp32 logits with 20 alternatives: 12.7 us split by 4, 16.9 whole; 128 rows: 18.7
+  // by 2, 16.9 whole; 8 rows of 20,000 bf16: 6.6 by 8, 7.1 by 4); 16 CTAs while each has an
+  // SM to itself (8 rows of 131,072: 8.1 and 8.2 by 8; 2 of 1,000,000: 13.0 and 17.0; 16
+  // rows of 131,072: 8.4 and 8.1).
   int splits = 1;
   if (2 * T <= ctx.num_sms)
-    while (splits < 8 && T * splits <= ctx.num_sms && p.V / (splits * 2) >= 4096) splits *= 2;
+    while (splits < 8 && T * splits <= ctx.num_sms && p.V / (splits * 2) >= 2048) splits *= 2;
+  if (splits == 8 && T * kMaxSplits <= ctx.num_sms && p.V / kMaxSplits >= 2048) splits = kMaxSplits;
+  if (splits > 1) return launch<F32, TOP, kLpWarps, false, true>(p, T, splits, ctx, st);
   // With an SM or half of one to itself a whole row's CTA needs more bytes on their way
   // (128 rows of 131,072 fp32 logits: 16.9 us, 26 with two stages; 512 rows, where the
   // larger ring leaves fewer CTAs an SM: 58 and 46).
   if constexpr (F32)
-    if (splits == 1 && T <= 2 * ctx.num_sms) return launch<F32, TOP, kLpWarps, true>(p, T, splits, ctx, st);
-  return launch<F32, TOP, kLpWarps, false>(p, T, splits, ctx, st);
+    if (T <= 2 * ctx.num_sms) return launch<F32, TOP, kLpWarps, true, false>(p, T, 1, ctx, st);
+  return launch<F32, TOP, kLpWarps, false, false>(p, T, 1, ctx, st);
 }
 
 }  // namespace
