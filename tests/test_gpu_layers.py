@@ -386,6 +386,55 @@ def test_lora_linear_graphs_may_share_a_workspace(T):
     _sync_ok()
 
 
+@pytest.mark.parametrize("T,N,K,R,n", [(8, 512, 2048, 16, 8), (64, 4096, 512, 32, 20), (400, 512, 1040, 64, 7), (1400, 700, 272, 24, 9)])
+def test_lora_linear_graph_follows_its_inputs(T, N, K, R, n):
+    """A replay takes the adapters, their factors, the rows' ids and the codes as they are then,
+    from batches without an adapter to ones where each row has another."""
+    dev = need_gpu()
+    g = _gen(dev, 41)
+    x, xs = _codes((T, K), g, dev, 1)
+    w, ws = _codes((N, K), g, dev, 128)
+    a, b, s = _adapters(n, N, K, R, g, dev)
+    ids = torch.full((T,), -1, dtype=torch.int32, device=dev)
+    y, want = torch.empty(T, N, device=dev), torch.empty(T, N, device=dev)
+    csa2.lora_linear(x, xs, w, ws, a, b, ids, y, adapter_scale=s, w_ready=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        csa2.lora_linear(x, xs, w, ws, a, b, ids, y, adapter_scale=s, w_ready=True)
+    for step in range(6):
+        ids.copy_([torch.full_like(ids, -1), torch.arange(T, device=dev, dtype=torch.int32) % n, _ids(T, n, 1, g, dev),
+                   torch.full_like(ids, n - 1), _ids(T, n, 5, g, dev), ids.flip(0)][step])
+        a.mul_(-1.5)
+        s.add_(0.25)
+        x2, _ = _codes((T, K), g, dev, 1)
+        x.copy_(x2)
+        graph.replay()
+        csa2.lora_linear(x, xs, w, ws, a, b, ids, want, adapter_scale=s)
+        _sync_ok()
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T", [5, 70, 1300])
+def test_lora_linear_many_adapters(T):
+    """A hundred thousand adapters, of which the rows use the first and the last ones."""
+    dev = need_gpu()
+    g = _gen(dev, 43)
+    K, N, R, n = 272, 128, 8, 100003
+    x, xs = _codes((T, K), g, dev, 1)
+    w, ws = _codes((N, K), g, dev, 128)
+    a, b, s = _adapters(n, N, K, R, g, dev)
+    ids = torch.randint(0, 9, (T,), generator=g, device=dev, dtype=torch.int32)
+    ids[::2] = n - 1 - ids[::2]
+    y = torch.empty(T, N, device=dev)
+    csa2.lora_linear(x, xs, w, ws, a, b, ids, y, adapter_scale=s)
+    _sync_ok()
+    used, at = torch.unique(ids, return_inverse=True)
+    u = used.long()
+    ref, tol = _lora_ref(x, xs, w, ws, a[u], b[u], at.int(), s[u], None, 0, 10000.0, 2)
+    _check_out(y, None, ref, tol, "fp32", T, N)
+
+
 def test_rows_further_apart_than_32_bits():
     """Row strides that put the last row past 2^32 bytes and 2^31 elements."""
     dev = need_gpu()
@@ -518,7 +567,8 @@ def test_logprobs_match_oracle(T, V, n, kind):
 @pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,V,n", [(3, 512, 9), (3, 513, 9), (759, 1500, 3), (760, 1500, 3), (760, 10000, 0), (760, 10001, 2),
                                    (76, 8192, 4), (77, 8192, 4), (304, 4000, 5), (305, 4000, 5), (153, 4000, 0), (5, 4095, 6),
-                                   (19, 65536, 6), (38, 65536, 32)])
+                                   (19, 65536, 6), (38, 65536, 32), (9, 32768, 7), (9, 32767, 7), (10, 32768, 7), (4, 2047, 3),
+                                   (4, 4097, 3), (1, 1 << 21, 32)])
 def test_logprobs_at_the_edges_of_their_kernels(T, V, n, kind):
     dev = need_gpu()
     g = _gen(dev, T + V)
