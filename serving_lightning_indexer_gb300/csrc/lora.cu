@@ -11,7 +11,7 @@
 // the other side that fp32's own roundings do).
 //
 // Two kernels, both bound by latency: launch, ids, operands, products, sums.  For few rows
-// a CTA takes 16 of them, one of their adapters and 8 of its ranks, its 16 or 32 warps the
+// a CTA takes 16 of them, one of their adapters and 8 of its ranks, its 8 to 32 warps the
 // blocks of 128 input dims in turn, added in warp order: 8 x 7,168 x 512 with 8 adapters
 // takes 8.4 us with its projection, 4.7 without adapters.  For many a CTA takes 128 rows,
 // 64 ranks and a share of the input dims, and goes through the tile's adapters with a in a
@@ -111,7 +111,7 @@ __device__ __forceinline__ void store_v(const InnerParams& p, long long row, int
   }
 }
 
-// W warps: 16, or 32 where there are more than 16 blocks of input dims.
+// W warps: 8, 16 or 32.
 template <int W>
 __global__ void __launch_bounds__(W * 32) lora_inner_kernel(const __grid_constant__ InnerParams p) {
   __shared__ float part[W][16][8];
@@ -553,12 +553,20 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
   const int tiles = (l.T + kTileRows - 1) / kTileRows, runs = (a.rank + kTileRanks - 1) / kTileRanks, blocks = (l.K + 127) / 128;
   // 8 ranks without a partner get 8 zeros beside them: products are of 16
   const dim3 grid((l.T + 15) / 16, (a.rank + 15) / 16 * 2, a.n_adapters < 16 ? a.n_adapters : 16);
-  // The small CTAs while they run in a wave or two (an SM holds two), by the most adapters
-  // that 16 rows can have: 333 x 1,360 x 1,001 with 5 of rank 24 take 11.8 us, 13.4 with the
-  // tiles; 64 x 2,048 x 32,768 with 16 of rank 64: 31.6 and 29.5.
-  if (static_cast<long long>(grid.x) * grid.y * grid.z <= 3LL * ctx.num_sms)
+  // The small CTAs while they, by the most adapters that 16 rows can have, and their blocks
+  // are few (the projection's time counted in): 333 x 1,360 x 1,001 with 5 of rank 24 take
+  // 11.4 us, 13.4 with the tiles; 64 x 4,096 x 8,192 with 16 of rank 80: 38 and 53; 200 x
+  // 2,048 x 4,096 with 16 of rank 64: 26.2 and 24.0; 96 x 7,168 x 512 with 16 of rank 48: 23.4
+  // and 21.0.
+  const long long small = static_cast<long long>(grid.x) * grid.y * grid.z;
+  if (small * (blocks + 8) <= 190LL * ctx.num_sms) {
+    // Up to 16 blocks, 8 warps where 16 would be more than an SM's two CTAs (333 x 1,360 x
+    // 1,001: 11.4 and 11.8 us; 256 rows of K = 1,024: 8.7 and 9.2); above, 32 (400 x 7,168 x
+    // 512 with 8 of rank 16: 26.4 us, 34.2 with 8).
+    if (blocks <= 16 && small > 2 * ctx.num_sms) return launch_pdl(lora_inner_kernel<8>, grid, dim3(256), 0, st, p);
     return blocks > 16 ? launch_pdl(lora_inner_kernel<32>, grid, dim3(1024), 0, st, p)
                        : launch_pdl(lora_inner_kernel<16>, grid, dim3(512), 0, st, p);
+  }
   // one CTA an SM: shares of the input dims, then of the adapters
   int splits = ctx.num_sms / (tiles * runs);
   splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
