@@ -9,9 +9,9 @@
 // few rows, bound by the weights' bytes (8 x 2,048 x 32,768: 12.7 us, 5.3 TB/s) or, where
 // they are few, by latency (8 x 7,168 x 512: 4.6 us).
 //
-// LORA: each adapter that a tile's rows use (lora.cu lists them) brings one to three more
-// blocks for every 64 ranks, bf16 products of the rows' inner products with the
-// adapter's b, summed like the others but only to the rows that have the adapter.  The
+// LORA: each adapter that a tile's rows use (lora.cu lists them) brings one more block for
+// every 64 ranks, or 32 where the inner products v are held in two or three bf16: bf16
+// products of the rows' v with the adapter's b, summed like the others but only to the rows that have the adapter.  The
 // projection's own blocks come first, and only what lora.cu wrote waits for it.  4,096 x
 // 2,048 x 32,768 with 4 adapters of rank 64: 268 us, 249 without adapters; 64 rows with 16
 // of rank 32: 25.3 us, 16.2 without, of which b's bytes are 5.
@@ -55,40 +55,55 @@ struct LoraParams {};
 template <>
 struct LoraParams<true> {
   // Inner products [planes T, pitch] and b [adapters N, rank], as boxes of a block's row by
-  // a tile's rows or columns: of the runs of 64 ranks, and of the last one if it is shorter.
+  // a tile's rows or columns: of the runs of `run` ranks, and of the last one if it is shorter.
   CUtensorMap map_v, map_b, map_v_last, map_b_last;
   const int* row_adapter;
   const int* lists;  // of tiles of 128 rows, kLoraListWords each; a tile of fewer makes its own
   int n_adapters, rank;
-  int pieces;  // blocks of an adapter: 64 ranks each, times planes of v
-  int planes;
+  int run;     // ranks of a block
+  int pieces;  // blocks of an adapter
+  int planes;  // of v
 };
 // Bytes of a row of v or b of some ranks in shared memory.  The least that hold them: a box
 // whose rows end far past the matrix's costs time (64 x 2,048 x 32,768 with 16 adapters of
 // rank 8: 43 us with 128, 26 with 32), though less than plain copies of the rows (50 us).
 __host__ __device__ __forceinline__ int lora_row_bytes(int ranks) { return ranks <= 16 ? 32 : ranks <= 32 ? 64 : 128; }
-// Block i of a tile's adapters: the adapter, where its ranks start, how many there are,
-// and where its plane of v starts.
+// Block i of a tile's adapters: the adapter, where its ranks start and how many there are.
+// In a stage b comes first, then the planes of v, whose products with it are one sum.
 struct LoraBlock {
-  int adapter, rank0, ranks, v_row;
-  __device__ __forceinline__ LoraBlock(const LoraParams<true>& lo, const int* list, int i, int T) {
+  int adapter, rank0, ranks, row;
+  __device__ __forceinline__ LoraBlock(const LoraParams<true>& lo, const int* list, int i) {
     const int j = i / lo.pieces, k = i - j * lo.pieces;
     adapter = list[4 + j];
-    rank0 = k / lo.planes * 64;
-    ranks = min(64, lo.rank - rank0);
-    v_row = k % lo.planes * T;
+    rank0 = k * lo.run;
+    ranks = min(lo.run, lo.rank - rank0);
+    row = lora_row_bytes(ranks);
   }
-  __device__ __forceinline__ int steps() const { return (ranks + 15) >> 4; }  // products of 16 ranks
-  __device__ __forceinline__ void expect(uint64_t* full, int v_rows, int b_rows) const {
-    mbar_arrive_expect_tx(full, (v_rows + b_rows) * lora_row_bytes(ranks));
-  }
-  __device__ __forceinline__ void copy_v(const LoraParams<true>& lo, uint8_t* dst, uint64_t* full, int t0, uint64_t policy) const {
-    tma_load_2d(dst, ranks < 64 ? &lo.map_v_last : &lo.map_v, rank0 * 2, v_row + t0, full, policy);
+  __device__ __forceinline__ void expect(const LoraParams<true>& lo, uint64_t* full, int v_rows, int b_rows) const {
+    mbar_arrive_expect_tx(full, (lo.planes * v_rows + b_rows) * row);
   }
   // Behind b's columns, and in the columns of 8 ranks without a partner, are zeros.
-  __device__ __forceinline__ void copy_b(const LoraParams<true>& lo, uint8_t* dst, uint64_t* full, int n0, int N,
+  __device__ __forceinline__ void copy_b(const LoraParams<true>& lo, uint8_t* stage, uint64_t* full, int n0, int N,
                                          uint64_t policy) const {
-    tma_load_2d(dst, ranks < 64 ? &lo.map_b_last : &lo.map_b, rank0 * 2, adapter * N + n0, full, policy);
+    tma_load_2d(stage, ranks < lo.run ? &lo.map_b_last : &lo.map_b, rank0 * 2, adapter * N + n0, full, policy);
+  }
+  __device__ __forceinline__ void copy_v(const LoraParams<true>& lo, uint8_t* stage, uint64_t* full, int t0, int T, int v_rows,
+                                         int b_rows, uint64_t policy) const {
+    for (int i = 0; i < lo.planes; ++i)
+      tma_load_2d(stage + (b_rows + i * v_rows) * row, ranks < lo.run ? &lo.map_v_last : &lo.map_v, rank0 * 2, i * T + t0, full,
+                  policy);
+  }
+  // The block's products; V_FIRST: v is the first operand.
+  template <bool V_FIRST>
+  __device__ __forceinline__ void products(const LoraParams<true>& lo, uint32_t d, const uint8_t* stage, int v_rows, int b_rows,
+                                           uint32_t idesc) const {
+    const uint64_t bd = smem_desc_rows(stage, row);
+    const int steps = (ranks + 15) >> 4;  // of 16 ranks
+    for (int i = 0; i < lo.planes; ++i) {
+      const uint64_t vd = smem_desc_rows(stage + (b_rows + i * v_rows) * row, row);
+      for (int k = 0; k < steps; ++k)
+        umma_bf16(d, (V_FIRST ? vd : bd) + 2 * k, (V_FIRST ? bd : vd) + 2 * k, idesc, i + k > 0 ? 1u : 0u);
+    }
   }
 };
 // The adapters among a tile's NT rows, each once, in the order of their first rows, and the
@@ -139,6 +154,7 @@ template <int BN, bool LORA>
 struct WideCfg {
   static constexpr int kStages = 4;
   static constexpr int kStageBytes = (kTileM + BN) * kBlockK;
+  static_assert((kLoraPlanes * kTileM + BN) * 64 <= kStageBytes, "a block of 32 ranks in all planes fits");
   static constexpr int kAccs = 512 / BN;          // TMEM ring: 512 columns
   static constexpr int kCols = BN / 2;            // columns of a tile an accumulation warp holds
   static constexpr int kOffOut = kStages * kStageBytes;  // 32 rows x 64 B of output per accumulation warp
@@ -248,7 +264,7 @@ struct TileAdapters {
     }
     return mine.adapters_too() ? count * lo.pieces : 0;
   }
-  __device__ __forceinline__ LoraBlock at(int i, int T) const { return LoraBlock(lo, list, i, T); }
+  __device__ __forceinline__ LoraBlock at(int i) const { return LoraBlock(lo, list, i); }
 };
 
 // The accumulation warps' part: sums each tile in registers and writes it.
@@ -525,13 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           adapters.look(tile);
           const int extra = adapters.blocks(tile);
           for (int i = 0; i < extra; ++i, ++it) {
-            const LoraBlock at = adapters.at(i, p.T);
+            const LoraBlock at = adapters.at(i);
             const int s = static_cast<int>(it % S);
             if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
             uint8_t* dst = smem + s * Cfg::kStageBytes;
-            at.expect(&full[s], kTileM, BN);
-            at.copy_v(lo, dst, &full[s], t0, keep);
-            at.copy_b(lo, dst + kTileM * kBlockK, &full[s], n0, p.N, keep);
+            at.expect(lo, &full[s], kTileM, BN);
+            at.copy_v(lo, dst, &full[s], t0, p.T, kTileM, BN, keep);
+            at.copy_b(lo, dst, &full[s], n0, p.N, keep);
           }
         }
       }
@@ -587,12 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           next -= blocks;
           const int extra = adapters.blocks(tile);
           for (; next < extra && ok; next += NA) {
-            const LoraBlock at = adapters.at(next, p.T);
-            const int steps = at.steps(), row = lora_row_bytes(at.ranks);
+            const LoraBlock at = adapters.at(next);
             ok = block([&](uint64_t, uint64_t) {
-              const uint64_t ad = smem_desc_rows(smem, row) + s * kStageDesc;
-              const uint64_t bd = smem_desc_rows(smem + kTileM * kBlockK, row) + s * kStageDesc;
-              for (int k = 0; k < steps; ++k) umma_bf16(d, ad + 2 * k, bd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
+              at.products<true>(lo, d, smem + s * Cfg::kStageBytes, kTileM, BN, idesc_b);
             });
           }
           next -= extra;
@@ -717,7 +730,9 @@ cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int 
   lo->row_adapter = a.row_adapter;
   lo->lists = to.lists;
   lo->planes = lora_planes(a.base.out_format);
-  lo->pieces = (a.rank + 63) / 64 * lo->planes;
+  // with b of 32 ranks all planes of v fit a stage
+  lo->run = lo->planes == 1 ? 64 : 32;
+  lo->pieces = (a.rank + lo->run - 1) / lo->run;
   const uint64_t row = 2 * static_cast<uint64_t>(a.rank);
   const uint64_t v_row = 2 * static_cast<uint64_t>(lora_pitch(a.rank));
   const uint64_t v_rows = lo->planes * static_cast<uint64_t>(a.base.T), b_rows = static_cast<uint64_t>(a.n_adapters) * a.base.N;
@@ -728,8 +743,8 @@ cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int 
     return encode_tmap_2d_u8(v, to.v, v_row, v_rows, v_row, bytes, rows, swizzle) == CUDA_SUCCESS &&
            encode_tmap_2d_u8(b, a.b, row, b_rows, row, bytes, columns, swizzle) == CUDA_SUCCESS;
   };
-  const int last = a.rank & 63;
-  if ((a.rank >= 64 && !encode(128, &lo->map_v, &lo->map_b)) ||
+  const int last = a.rank % lo->run;
+  if ((a.rank >= lo->run && !encode(2 * lo->run, &lo->map_v, &lo->map_b)) ||
       (last && !encode(lora_row_bytes(last), &lo->map_v_last, &lo->map_b_last))) {
     *why = "csa2_lora_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
@@ -789,6 +804,7 @@ template <int NT, bool LORA>
 struct NarrowCfg {
   static constexpr int kStages = 4;
   static constexpr int kStageBytes = (128 + NT) * kBlockK;
+  static_assert((kLoraPlanes * NT + 128) * 64 <= kStageBytes, "a block of 32 ranks in all planes fits");
   static constexpr int kAccs = 4;
   static constexpr int kCols = kAccs * NT < 32 ? 32 : kAccs * NT;
   static constexpr int kOffScales = kStages * kStageBytes;  // the parts [NT][128] reuse the stages
@@ -879,22 +895,22 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
         for (int i = 0; i < ahead; ++i, ++b) {
           const int s = b % S;
           if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
-          const LoraBlock at(lo, s_list, rank + i * splits, p.T);
-          at.expect(&full[s], NT, 128);
+          const LoraBlock at(lo, s_list, rank + i * splits);
+          at.expect(lo, &full[s], NT, 128);
           at.copy_b(lo, smem + s * Cfg::kStageBytes, &full[s], n0, p.N, pol_x);
         }
         if (b > blocks) pdl_wait();
         for (int i = 0; blocks + i < b; ++i) {
           const int s = (blocks + i) % S;
-          LoraBlock(lo, s_list, rank + i * splits, p.T).copy_v(lo, smem + s * Cfg::kStageBytes + 128 * kBlockK, &full[s], t0, pol_x);
+          LoraBlock(lo, s_list, rank + i * splits).copy_v(lo, smem + s * Cfg::kStageBytes, &full[s], t0, p.T, NT, 128, pol_x);
         }
         for (int i = ahead; ok && i < extra; ++i, ++b) {
           const int s = b % S;
           if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
-          const LoraBlock at(lo, s_list, rank + i * splits, p.T);
-          at.expect(&full[s], NT, 128);
+          const LoraBlock at(lo, s_list, rank + i * splits);
+          at.expect(lo, &full[s], NT, 128);
           at.copy_b(lo, smem + s * Cfg::kStageBytes, &full[s], n0, p.N, pol_x);
-          at.copy_v(lo, smem + s * Cfg::kStageBytes + 128 * kBlockK, &full[s], t0, pol_x);
+          at.copy_v(lo, smem + s * Cfg::kStageBytes, &full[s], t0, p.T, NT, 128, pol_x);
         }
       }
       if (!ok) {
@@ -930,12 +946,9 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
         ok = ok && mbar_wait(lready, 0u, s_abort);
         const int extra = ok ? shares_of(s_list[0] * lo.pieces, rank, splits) : 0;
         for (int i = 0; ok && i < extra; ++i) {
-          const LoraBlock at(lo, s_list, rank + i * splits, p.T);
-          const int steps = at.steps(), row = lora_row_bytes(at.ranks);
+          const LoraBlock at(lo, s_list, rank + i * splits);
           ok = block([&](uint32_t d, uint64_t, uint64_t) {
-            const uint64_t wd = smem_desc_rows(smem + (b % S) * Cfg::kStageBytes, row);
-            const uint64_t xd = smem_desc_rows(smem + (b % S) * Cfg::kStageBytes + 128 * kBlockK, row);
-            for (int k = 0; k < steps; ++k) umma_bf16(d, wd + 2 * k, xd + 2 * k, idesc_b, k > 0 ? 1u : 0u);
+            at.products<false>(lo, d, smem + (b % S) * Cfg::kStageBytes, NT, 128, idesc_b);
           });
         }
       }

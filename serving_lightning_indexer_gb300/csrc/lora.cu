@@ -213,19 +213,19 @@ __global__ void __launch_bounds__(W * 32) lora_inner_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- many rows
 // Products on tcgen05: with many adapters in a tile each of them is a product with all 128
-// rows, 16 times what the rows need, which its rate hides.  Each block of 128 input dims of the CTA's rows becomes bf16
+// rows, several times what the rows need.  Each block of 128 input dims of the CTA's rows becomes bf16
 // in a ring in shared memory; each adapter's block of a comes by tensor copies; each of
 // these pairs is a product of its own, which eight warps (a lane is a row, four warps
 // half the ranks) add, times the row's scale, to the sums of the rows that have the
 // adapter.  So a row's sums stay in registers throughout.
-constexpr int kTileRows = 128, kTileRanks = 64, kTileStages = 12, kTileXStages = 3, kTileRaw = 4, kTileAccs = 4;
+constexpr int kTileRows = 128, kTileRanks = 64, kTileStages = 4, kTileXStages = 3, kTileRaw = 4, kTileAccs = 4;
 constexpr int kSumWarps = 8, kConvertWarps = 8, kCopyWarp = kSumWarps + kConvertWarps, kIssueWarp = kCopyWarp + 1;
 constexpr int kTileWarps = kIssueWarp + 1;
 constexpr int kTileXBytes = kTileRows * 256;  // a block of x: two halves of 64 dims, rows of 128 bytes
 constexpr int kTileOffRaw = kTileXStages * kTileXBytes;  // blocks of codes, a lane's own words side by side; then the sums
 static_assert(kTileRows * kTileRanks * 4 <= kTileRaw * kTileRows * 128, "the sums fit where the codes were");
 constexpr int kTileOffA = kTileOffRaw + kTileRaw * kTileRows * 128;
-constexpr int kTileABytes = 3 * kTileRanks * 256;  // the ring of blocks of a: three of 64 ranks, twelve of 16
+constexpr int kTileABytes = 3 * kTileRanks * 256;  // the ring of blocks of a: three of 64 ranks, four of 48
 // Rows' scales of the blocks between the farthest copied one, kTileRaw - 1 ahead of the
 // converting warps, and the one whose sums are added, kTileXStages behind them.
 constexpr int kTileScales = 8, kTileOffScales = kTileOffA + kTileABytes;
@@ -234,7 +234,9 @@ constexpr int kTileSmem = 1024 + kTileOffScales + kTileScales * kTileRows * 4;
 
 // Grid: row tiles, shares of the input dims (a cluster), runs of 64 ranks times slots;
 // slot z takes the tile's adapters z, z + slots, ..  map_a: a as rows of K, boxes of 64
-// dims by `box` ranks (a run's, in sixteens).
+// dims by `box` ranks (a run's, in sixteens).  G adapters of 16 or 32 ranks share a
+// product, 64 columns wide, as its columns have nothing to do with each other (1,024 x
+// 7,168 x 512 with 16 adapters of rank 16, all in each tile: 83 us with one, 41 with four).
 __global__ void __launch_bounds__(kTileWarps * 32, 1)
     lora_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ InnerParams p, int slots, int box,
                      int stages) {
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
   float* part = reinterpret_cast<float*>(smem + kTileOffRaw);  // [rows][ranks]: a row's own adapter's sums
   uint8_t* x_ring = smem;
   uint8_t* a_ring = smem + kTileOffA;
-  const int a_bytes = box * 256;
+  const int G = box <= 32 ? kTileRanks / box : 1, a_bytes = G * box * 256;
   __shared__ __align__(16) int s_id[kTileRows], s_list[kTileRows + 4];
   __shared__ int s_place[kTileRows];  // a row's adapter's place in the list, or -1
   __shared__ int s_base[kTileWarps];
@@ -297,6 +299,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
     s_place[tid] = id >= 0 ? at : -1;
   }
   const int mine = n > slot ? (n - slot - 1) / slots + 1 : 0;  // adapters of this slot
+  const int groups = (mine + G - 1) / G;
   __syncthreads();                                             // s_place
   // a is asked for first; what else is read waits for the previous launch
   if (warp != kCopyWarp) {
@@ -312,13 +315,17 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
       int s = 0, sent = 0;
       uint32_t phase = 0;
       for (int b = 0; b < nb && ok; ++b)
-        for (int j = 0; j < mine; ++j, ++sent) {
+        for (int j = 0; j < groups; ++j, ++sent) {
           if (sent >= stages && !(ok = mbar_wait(&s_empty[s], phase ^ 1u, &s_abort))) break;
-          mbar_arrive_expect_tx(&s_full[s], a_bytes);
-          const int y = s_list[4 + slot + j * slots] * p.rank + r0;
+          const int members = min(G, mine - j * G);
+          mbar_arrive_expect_tx(&s_full[s], members * box * 256);
+          for (int g = 0; g < members; ++g) {
+            const int y = s_list[4 + slot + (j * G + g) * slots] * p.rank + r0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            tma_load_2d(a_ring + s * a_bytes + h * (a_bytes / 2), &map_a, ((b0 + b) * 128 + h * 64) * 2, y, &s_full[s], keep);
+            for (int h = 0; h < 2; ++h)
+              tma_load_2d(a_ring + s * a_bytes + h * (a_bytes / 2) + g * box * 128, &map_a, ((b0 + b) * 128 + h * 64) * 2, y,
+                          &s_full[s], keep);
+          }
           if (++s == stages) {
             s = 0;
             phase ^= 1u;
@@ -340,14 +347,14 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
   } else if (warp == kIssueWarp) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kTileRows, columns, 0, 0);
+      const uint32_t idesc = idesc_bf16_f32(kTileRows, G > 1 ? kTileRanks : columns, 0, 0);
       const uint64_t xd = smem_desc_sw128(x_ring), ad = smem_desc_sw128(a_ring);
       int s = 0;
       uint32_t phase = 0, at = 0;
       for (int b = 0; b < nb && ok; ++b) {
         const int xs = b % kTileXStages;
         if (!(ok = mbar_wait(&s_xfull[xs], static_cast<uint32_t>(b / kTileXStages) & 1u, &s_abort))) break;
-        for (int j = 0; j < mine; ++j, ++at) {
+        for (int j = 0; j < groups; ++j, ++at) {
           const int acc = static_cast<int>(at % kTileAccs);
           if (!(ok = mbar_wait(&s_full[s], phase, &s_abort))) break;
           if (at >= kTileAccs && !(ok = mbar_wait(&s_tempty[acc], (at / kTileAccs - 1) & 1u, &s_abort))) break;
@@ -437,25 +444,30 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
     const float* scales = reinterpret_cast<const float*>(smem + kTileOffScales) + row;
     const float factor = p.adapter_scale && place >= 0 ? __ldg(p.adapter_scale + s_id[row]) : 1.f;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 32;
-    const bool idle = half * 32 >= columns;
+    // The row's adapter's product, and where its ranks start among this warp's 32 columns:
+    // each warp has half of one adapter's, all of one's, or two's.
+    const int index = place >= 0 && place % slots == slot ? place / slots : -1, member = index % G;
+    const bool here = index >= 0 && (G == 1 ? half * 32 < columns : member * box >> 5 == half);
+    const int own_group = here ? index / G : -1;
+    const bool second = G == 4 && (member & 1);
     float y[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) y[k] = 0.f;
     int s = 0;
     uint32_t at = 0;
     for (int b = 0; b < nb && ok; ++b) {
-      for (int j = 0; j < mine; ++j, ++at) {
+      for (int j = 0; j < groups; ++j, ++at) {
         const int acc = static_cast<int>(at % kTileAccs);
-        const bool own = place == slot + j * slots;
+        const bool own = own_group == j;
         ok = __all_sync(0xffffffffu, mbar_wait(&s_tfull[acc], (at / kTileAccs) & 1u, &s_abort));
         if (!ok) break;
         tc_fence_after();
         if (warp == 0 && lane == 0) {  // the products have read the stages
           mbar_arrive(&s_empty[s]);
-          if (j + 1 == mine) mbar_arrive(&s_xempty[b % kTileXStages]);
+          if (j + 1 == groups) mbar_arrive(&s_xempty[b % kTileXStages]);
         }
         if (++s == stages) s = 0;
-        if (__any_sync(0xffffffffu, own) && !idle) {
+        if (__any_sync(0xffffffffu, own)) {
           uint32_t v[2][16];
           tmem_ld32x16_async(taddr + acc * kTileRanks, v[0]);
           tmem_ld32x16_async(taddr + acc * kTileRanks + 16, v[1]);
@@ -464,7 +476,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
           if (own) {
             const float scale = scales[(b % kTileScales) * kTileRows];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = fmaf(scale, __uint_as_float(v[k >> 4][k & 15]), y[k]);
+            for (int k = 0; k < 32; ++k)
+              y[k] = fmaf(scale, __uint_as_float(k < 16 && second ? v[1][k] : v[k >> 4][k & 15]), y[k]);
           }
         }
         tc_fence_before();
@@ -477,11 +490,11 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
       set_error(p.err, kErrTimeout);
     }
     // every block has been converted: its products are done
-    if (!idle) {  // the pieces of a row turned by its number: lanes do not collide
+    if (here) {  // the pieces of a row turned by its number: lanes do not collide
       float4* dst = reinterpret_cast<float4*>(part + row * kTileRanks);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        dst[(half * 8 + k) ^ (row & 15)] = make_float4(y[4 * k] * factor, y[4 * k + 1] * factor, y[4 * k + 2] * factor,
+        dst[((G == 1 ? half * 8 : 0) + k) ^ (row & 15)] = make_float4(y[4 * k] * factor, y[4 * k + 1] * factor, y[4 * k + 2] * factor,
                                                          y[4 * k + 3] * factor);
     }
   }
@@ -571,10 +584,14 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
   int splits = ctx.num_sms / (tiles * runs);
   splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
   if (splits > blocks) splits = blocks;
-  const int room = ctx.num_sms - ctas >= 16 ? ctx.num_sms - ctas : ctx.num_sms;
+  // The SMs that the projection's CTAs leave, if they are half of all (200 x 7,168 x 512 with
+  // 16 of rank 64: 29.0 us, 35.2 on all; 512 rows with 100 of rank 8, where they are not:
+  // 94 and 64).
+  const int room = 2 * ctas <= ctx.num_sms ? ctx.num_sms - ctas : ctx.num_sms;
+  const int box = a.rank > 48 ? kTileRanks : (a.rank + 15) & ~15, G = box <= 32 ? kTileRanks / box : 1;
   int slots = room / (tiles * runs * splits);
+  if (slots > (a.n_adapters + G - 1) / G) slots = (a.n_adapters + G - 1) / G;
   slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
-  if (slots > a.n_adapters) slots = a.n_adapters;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles, splits, runs * slots);
   cfg.blockDim = dim3(kTileWarps * 32);
@@ -591,14 +608,13 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
   cfg.numAttrs = splits > 1 ? 2 : 1;
   CUtensorMap map_a;
   const uint64_t row = 2 * static_cast<uint64_t>(l.K);
-  const int box = a.rank > 48 ? kTileRanks : (a.rank + 15) & ~15;
   if (encode_tmap_2d_u8(&map_a, a.a, row, static_cast<uint64_t>(a.n_adapters) * a.rank, row, 128, box) != CUDA_SUCCESS) {
     *why = "csa2_lora_linear: a tensor map could not be encoded";
     return cudaErrorInvalidValue;
   }
   cudaError_t e = prefer_max_smem_once<lora_tile_kernel>(ctx.device, kTileSmem);
   if (e != cudaSuccess) return e;
-  const int stages = kTileABytes / (box * 256) < kTileStages ? kTileABytes / (box * 256) : kTileStages;
+  const int stages = kTileABytes / ((box <= 32 ? kTileRanks : box) * 256);
   return cudaLaunchKernelEx(&cfg, lora_tile_kernel, map_a, p, slots, box, stages);
 }
 
