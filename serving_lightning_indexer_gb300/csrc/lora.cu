@@ -564,15 +564,32 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
                       a.rank, lora_pitch(a.rank), a.n_adapters, lora_planes(l.out_format), l.w_ready,
                       ctx.err};
   const int tiles = (l.T + kTileRows - 1) / kTileRows, runs = (a.rank + kTileRanks - 1) / kTileRanks, blocks = (l.K + 127) / 128;
-  // 8 ranks without a partner get 8 zeros beside them: products are of 16
-  const dim3 grid((l.T + 15) / 16, (a.rank + 15) / 16 * 2, a.n_adapters < 16 ? a.n_adapters : 16);
+  // The tiles' CTAs, one an SM: shares of the input dims, then of the adapters.  If the SMs
+  // that the projection's CTAs leave hold those of a slot, not more than they: the two
+  // launches run side by side (64 x 2,048 x 32,768 with 16 of rank 64: 29.7 us, 35.6 on all;
+  // 200 x 7,168 x 512: 28.7 and 35.2).
+  int splits = ctx.num_sms / (tiles * runs);
+  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  if (splits > blocks) splits = blocks;
+  const int left = ctx.num_sms - ctas, room = tiles * runs * splits <= left ? left : ctx.num_sms;
+  const int box = a.rank > 48 ? kTileRanks : (a.rank + 15) & ~15, G = box <= 32 ? kTileRanks / box : 1;
+  const int groups = ((a.n_adapters < kTileRows ? a.n_adapters : kTileRows) + G - 1) / G;  // of a tile, at most
+  int slots = room / (tiles * runs * splits);
+  if (slots > groups) slots = groups;
+  slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
   // The small CTAs while they, by the most adapters that 16 rows can have, and their blocks
   // are few (the projection's time counted in): 333 x 1,360 x 1,001 with 5 of rank 24 take
-  // 11.4 us, 13.4 with the tiles; 64 x 4,096 x 8,192 with 16 of rank 80: 38 and 53; 200 x
+  // 10.5 us, 13.2 with the tiles; 64 x 4,096 x 8,192 with 16 of rank 80: 38 and 53; 200 x
   // 2,048 x 4,096 with 16 of rank 64: 26.2 and 24.0; 96 x 7,168 x 512 with 16 of rank 48: 23.4
-  // and 21.0.
+  // and 21.0.  But not where the tiles' take no longer, at half a microsecond a product and
+  // 10 more, than the projection beside them (its weights at 4.2 TB/s): 128 x 2,048 x 32,768
+  // with 16 of rank 32 take 25.1 us with them and 29.0; 64 rows of rank 128: 50 and 40.
+  // 8 ranks without a partner get 8 zeros beside them: products are of 16.
+  const dim3 grid((l.T + 15) / 16, (a.rank + 15) / 16 * 2, a.n_adapters < 16 ? a.n_adapters : 16);
   const long long small = static_cast<long long>(grid.x) * grid.y * grid.z;
-  if (small * (blocks + 8) <= 190LL * ctx.num_sms) {
+  const int products = (blocks + splits - 1) / splits * ((groups + slots - 1) / slots);
+  const bool beside = tiles * runs * splits <= left && 20 + products <= (static_cast<long long>(l.N) * l.K) >> 21;
+  if (!beside && small * (blocks + 8) <= 190LL * ctx.num_sms) {
     // Up to 16 blocks, 8 warps where 16 would be more than an SM's two CTAs (333 x 1,360 x
     // 1,001: 11.4 and 11.8 us; 256 rows of K = 1,024: 8.7 and 9.2); above, 32 (400 x 7,168 x
     // 512 with 8 of rank 16: 26.4 us, 34.2 with 8).
@@ -580,18 +597,6 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
     return blocks > 16 ? launch_pdl(lora_inner_kernel<32>, grid, dim3(1024), 0, st, p)
                        : launch_pdl(lora_inner_kernel<16>, grid, dim3(512), 0, st, p);
   }
-  // one CTA an SM: shares of the input dims, then of the adapters
-  int splits = ctx.num_sms / (tiles * runs);
-  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
-  if (splits > blocks) splits = blocks;
-  // The SMs that the projection's CTAs leave, if they are half of all (200 x 7,168 x 512 with
-  // 16 of rank 64: 29.0 us, 35.2 on all; 512 rows with 100 of rank 8, where they are not:
-  // 94 and 64).
-  const int room = 2 * ctas <= ctx.num_sms ? ctx.num_sms - ctas : ctx.num_sms;
-  const int box = a.rank > 48 ? kTileRanks : (a.rank + 15) & ~15, G = box <= 32 ? kTileRanks / box : 1;
-  int slots = room / (tiles * runs * splits);
-  if (slots > (a.n_adapters + G - 1) / G) slots = (a.n_adapters + G - 1) / G;
-  slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles, splits, runs * slots);
   cfg.blockDim = dim3(kTileWarps * 32);
