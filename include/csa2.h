@@ -508,7 +508,8 @@ CSA2_API int csa2_batch_plan(const csa2_batch_plan_args* args, void* stream);
  *   r = x + residual, rounded to the residual's type (bf16 or fp32)
  *   y = r / sqrt(mean(r^2) + eps) * gamma       (of the rounded r)
  * residual_out receives r; codes and scale receive y by the rule of csa2_quant_fp8
- * with block_rows = 1 and gamma (the input of csa2_fp8_linear); y, if given, receives
+ * with block_rows = 1 and gamma (the input of csa2_fp8_linear), the codes those of the
+ * exact r * gamma * 448 / a rounded once to fp32, a the block's largest |r * gamma|; y, if given, receives
  * y in bf16 (the input of csa2_kv_project).  At least one of codes and y; scale goes
  * with codes.  residual_out may be residual itself (in place: the same pointer and
  * row stride); apart from that no output may overlap an input or another output,

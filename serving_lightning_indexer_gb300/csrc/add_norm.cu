@@ -2,9 +2,9 @@
 //   r = round(x + residual),  y = r / sqrt(mean(r^2) + eps) * gamma,  codes(y)
 //
 // Bound: HBM, each value read and written once: 7 B a value with a bf16 residual
-// (2 + 2 read, 2 + 1 written), 11 with an fp32 one.  4,096 x 7,168 bf16: 37 us, 5.6 TB/s
+// (2 + 2 read, 2 + 1 written), 11 with an fp32 one.  4,096 x 7,168 bf16: 40 us, 5.1 TB/s
 // (a plain copy: 6.8).  A decode step's few rows are launch and load latency: 8 x 7,168 in
-// 3.1 us.
+// 3.7 us.
 #include <cuda_bf16.h>
 
 #include "csa2_device.cuh"
@@ -36,6 +36,78 @@ __device__ __forceinline__ void pack16(const float (&y)[16], uint4 (&v)[2]) {
   for (int h = 0; h < 2; ++h)
     v[h] = make_uint4(pack_bf16(y[8 * h], y[8 * h + 1]), pack_bf16(y[8 * h + 2], y[8 * h + 3]),
                       pack_bf16(y[8 * h + 4], y[8 * h + 5]), pack_bf16(y[8 * h + 6], y[8 * h + 7]));
+}
+
+// Codes are of r * gamma * 448 / a, a the block's largest |r * gamma|, rounded once to fp32:
+// the norm's factor has no part in them.  In fp32 alone that is off by at most five roundings
+// (the product, a, 448 / a, what is less or more of it, and the last product).  Where values
+// six roundings to either side have one code, that is the code; where not (some 9 of a
+// million values), exact_codes decides.  With fp32's own roundings instead, 13 of 29.4 M codes
+// of 4,096 x 7,168 are on the other side of a border, and it takes 38.1 us, 40.1 so.
+constexpr float kNear = 3.5762786865234375e-7f;  // 6 x 2^-24
+
+// A magnitude in two parts; the larger of two, without a NaN.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair larger(Pair a, Pair b) {
+  const bool take = b.hi > a.hi || (b.hi == a.hi && b.lo > a.lo);
+  return Pair{take ? b.hi : a.hi, take ? b.lo : a.lo};
+}
+// The codes of a run from the stored r, the products and the largest of them in two parts
+// (2^-45 off).  By whole warps and seldom, so with few registers where many are taken
+// already (V above 1): unrolled, 4,096 x 7,168 takes 51 us in place of 40, and 1,003 x 2,064
+// 7.4 in place of 8.0.
+template <bool F32, int V>
+__device__ __forceinline__ void exact_codes(const uint4* r, const float* gamma, bool in, bool usual, uint32_t (&q)[4]) {
+  auto times = [&](int i, float (&hi)[4], float (&lo)[4]) {  // columns 4 i .. of the run
+    float x[4];
+    if constexpr (F32) {
+      const uint4 v = r[i];
+      x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+    } else {
+      const uint2 v = reinterpret_cast<const uint2*>(r)[i];
+      x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+      x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+    const float4 g = __ldg(reinterpret_cast<const float4*>(gamma) + i);
+    const float w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      hi[k] = x[k] * w[k];
+      lo[k] = fmaf(x[k], w[k], -hi[k]);
+    }
+  };
+  constexpr int kUnroll = V == 1 ? 4 : 1;
+  float hi[4], lo[4];
+  Pair a = {0.f, 0.f};
+#pragma unroll kUnroll
+  for (int i = 0; i < 4; ++i) {
+    if (!in) break;
+    times(i, hi, lo);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a = larger(a, Pair{fabsf(hi[k]), hi[k] < 0.f ? -lo[k] : lo[k]});
+  }
+  __syncwarp();
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1)
+    a = larger(a, Pair{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
+  if (!in || !usual) return;
+  // 448 / a as a factor, rounded down so that a zero keeps its sign, and what that lacks
+  float f = kE4m3Max / a.hi;
+  if (fmaf(-f, a.lo, fmaf(-f, a.hi, kE4m3Max)) < 0.f) f = __int_as_float(__float_as_int(f) - 1);
+  const float low = fmaf(-f, a.lo, fmaf(-f, a.hi, kE4m3Max)) * (f * (1.f / kE4m3Max));
+#pragma unroll kUnroll
+  for (int i = 0; i < 4; ++i) {
+    times(i, hi, lo);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) hi[k] = fmaf(hi[k], f, fmaf(lo[k], f, hi[k] * low));
+    const uint32_t v = e4m3x4(hi[0], hi[1], hi[2], hi[3]);
+    q[0] = i == 0 ? v : q[0];  // a rolled loop cannot index registers
+    q[1] = i == 1 ? v : q[1];
+    q[2] = i == 2 ? v : q[2];
+    q[3] = i == 3 ? v : q[3];
+  }
 }
 
 // A CTA takes a row and keeps it in registers between the sum of squares and the
@@ -120,7 +192,7 @@ __global__ void __launch_bounds__(256) add_norm_kernel(const __grid_constant__ A
   for (int r = 0; r < V; ++r) {
     const int c = (r * threads + tid) * 16;
     const bool in = c < p.K;
-    float y[16];
+    float y[16];  // r * gamma
     if constexpr (F32) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -135,27 +207,52 @@ __global__ void __launch_bounds__(256) add_norm_kernel(const __grid_constant__ A
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const float4 g = in ? __ldg(reinterpret_cast<const float4*>(p.gamma + c + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      y[i] = y[i] * inv * g.x;
-      y[i + 1] = y[i + 1] * inv * g.y;
-      y[i + 2] = y[i + 2] * inv * g.z;
-      y[i + 3] = y[i + 3] * inv * g.w;
-    }
-    if (!in) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = 0.f;  // 0 * inv is NaN where inv is infinite
+      y[i] *= g.x;
+      y[i + 1] *= g.y;
+      y[i + 2] *= g.z;
+      y[i + 3] *= g.w;
     }
     if (p.y && in) {
+      float n[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) n[i] = y[i] * inv;
       uint4 h[2];
-      pack16(y, h);
+      pack16(n, h);
       uint4* dst = reinterpret_cast<uint4*>(p.y + t * p.ld_y + c);
       dst[0] = h[0];
       dst[1] = h[1];
     }
     if (p.codes) {
-      float f;
-      const float s = e4m3_block(max8(amax16_rows(y)), &f);
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
+      top = max8(top);
+      const float a = top * inv;
+      const bool usual = !in || (top <= kLargest && a >= kAmaxFloor && a <= kLargest);  // the same in a block's lanes
+      float s = a / kE4m3Max;
+      uint32_t q[4], differ = 0;
+      if (usual) {
+        const float f = kE4m3Max / top, less = f * (1.f - kNear), more = f * (1.f + kNear);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          q[i] = e4m3x4(y[4 * i] * less, y[4 * i + 1] * less, y[4 * i + 2] * less, y[4 * i + 3] * less);
+          differ |= q[i] ^ e4m3x4(y[4 * i] * more, y[4 * i + 1] * more, y[4 * i + 2] * more, y[4 * i + 3] * more);
+        }
+      }
+      if (__builtin_expect(!__all_sync(0xffffffffu, usual), 0)) {  // a block's norm is zero or next to it, or not finite
+        float f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = in ? y[i] * inv : 0.f;  // 0 * inv is NaN where inv is infinite
+        const float scale = e4m3_block(max8(amax16(y)), &f);        // by all lanes
+        if (!usual) {
+          const uint4 w = codes16(y, f);
+          q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
+          s = scale;
+        }
+      }
+      if (__builtin_expect(__any_sync(0xffffffffu, differ != 0), 0)) exact_codes<F32, V>(out + c / 16 * kWords, p.gamma + c, in, usual, q);
       if (in) {
-        *reinterpret_cast<uint4*>(p.codes + t * p.ld_codes + c) = codes16(y, f);
+        *reinterpret_cast<uint4*>(p.codes + t * p.ld_codes + c) = make_uint4(q[0], q[1], q[2], q[3]);
         if ((tid & 7) == 0) p.scale[t * p.ld_scale + (c >> 7)] = s;
       }
     }

@@ -104,6 +104,29 @@ def test_add_norm_in_place_and_each_output_alone(T, K, kind):
         assert np.all(np.abs(s - np_(full[2])) <= 100 * U * s) and v.shape == (T, K)
 
 
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,K,unit", [(2000, 1040, False), (600, 7168, False), (300, 16384, False), (700, 528, True), (100, 7168, True)])
+def test_add_norm_codes_are_the_exact_quotients(T, K, unit, kind):
+    """Codes of r * gamma * 448 / a, a the block's largest |r * gamma|, rounded to fp32 and no
+    more before the code: every code is that of the quotient in 64 bits (2^-52 off), or of
+    what is 2^-40 less or more of it, where the kernel's two-part products are 2^-45 off.
+    With gamma of ones and bf16 r many lie on a border."""
+    dev, x, res, gamma = _norm_case(T, K, kind, T)
+    if unit:
+        gamma.fill_(1.0)
+    nb = -(-K // 128)
+    r, codes, scale = torch.empty_like(res), torch.empty(T, K, dtype=torch.uint8, device=dev), torch.empty(T, nb, device=dev)
+    csa2.add_norm_fp8(x, res, r, gamma, codes=codes, scale=scale)
+    _sync_ok()
+    v = torch.nn.functional.pad(r.double() * gamma.double(), (0, nb * 128 - K)).view(T, nb, 128)
+    q = (v * 448.0 / v.abs().amax(-1, keepdim=True)).view(T, -1)[:, :K]
+    less, want, more = ((q * (1.0 + d)).clamp(-448.0, 448.0).float().to(torch.float8_e4m3fn).float()
+                        for d in (-2.0 ** -40, 0.0, 2.0 ** -40))
+    got = codes.view(torch.float8_e4m3fn).float()
+    assert bool(((got == less) | (got == want) | (got == more)).all())
+    assert int((got != want).sum()) <= 2 and int((less != more).sum()) <= 2 + q.numel() * (2.0 ** -7 if unit else 2.0 ** -18)
+
+
 def test_add_norm_special_rows():
     dev = need_gpu()
     x = torch.zeros(6, 256, dtype=torch.bfloat16, device=dev)
