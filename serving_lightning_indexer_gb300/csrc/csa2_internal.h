@@ -184,7 +184,7 @@ struct LoraInner {
 constexpr int kLoraMaxRows = 1 << 20;
 constexpr int kLoraListWords = 132;
 constexpr int kLoraPlanes = 3;  // at most; the inner products' bf16 parts by the output's format
-inline int lora_planes(int out_format) { return out_format == CSA2_OUT_BF16 ? 1 : out_format == CSA2_OUT_F32 ? 2 : kLoraPlanes; }
+inline int lora_planes(int out_format) { return out_format == CSA2_OUT_BF16 ? 1 : kLoraPlanes; }
 inline int lora_pitch(int rank) { return (rank + 63) / 64 * 64; }  // rows of whole 128-byte words
 size_t lora_workspace_bytes(int T, int rank);
 LoraInner lora_inner_at(const csa2_lora_linear_args& a, void* ws, bool lists);

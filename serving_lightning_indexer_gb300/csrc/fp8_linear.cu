@@ -10,7 +10,7 @@
 // they are few, by latency (8 x 7,168 x 512: 4.6 us).
 //
 // LORA: each adapter that a tile's rows use (lora.cu lists them) brings one more block for
-// every 64 ranks, or 32 where the inner products v are held in two or three bf16: bf16
+// every 64 ranks, or 32 where the inner products v are held in three bf16: bf16
 // products of the rows' v with the adapter's b, summed like the others but only to the rows that have the adapter.  The
 // projection's own blocks come first, and only what lora.cu wrote waits for it.  4,096 x
 // 2,048 x 32,768 with 4 adapters of rank 64: 268 us, 249 without adapters; 64 rows with 16

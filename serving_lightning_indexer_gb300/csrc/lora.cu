@@ -5,10 +5,10 @@
 //
 // The codes are exact in bf16 and a is bf16, so a block's 128 products are summed by
 // the tensor core in fp32 and the block's scale is applied to the sum.  The result is
-// written as the bf16 nearest to it and, for fp32 output, the bf16 nearest to what that
-// leaves (2^-17 together); for e4m3 output a third (2^-25), as a code on the other side of
-// its border is 2^-3 off however near the border was (two leave three times the codes on
-// the other side that fp32's own roundings do).
+// written as the bf16 nearest to it and, but for bf16 output, the bf16 nearest to what that
+// leaves, and again (2^-25 together): two would leave fp32 output 2^-17 of v off, and e4m3
+// output, where a code on the other side of its border is 2^-3 off however near the border
+// was, three times the codes there that fp32's own roundings do.
 //
 // Two kernels, both bound by latency: launch, ids, operands, products, sums.  For few rows
 // a CTA takes 16 of them, one of their adapters and 8 of its ranks, its 8 to 32 warps the
@@ -36,7 +36,7 @@ struct InnerParams {
   int* lists;  // NULL: the projection's tiles are smaller and make their own
   long long ld_x, ld_xs;
   int T, K, rank, pitch, n_adapters;
-  int planes;  // 1, 2 or 3
+  int planes;  // 1 or 3
   int ready;   // a and row_adapter may be read before the previous launch completes
   uint32_t* err;
 };
