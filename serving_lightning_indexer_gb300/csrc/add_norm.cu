@@ -4,7 +4,7 @@
 // Bound: HBM, each value read and written once: 7 B a value with a bf16 residual
 // (2 + 2 read, 2 + 1 written), 11 with an fp32 one.  4,096 x 7,168 bf16: 40 us, 5.1 TB/s
 // (a plain copy: 6.8).  A decode step's few rows are launch and load latency: 8 x 7,168 in
-// 3.7 us.
+// 3.1 us.
 #include <cuda_bf16.h>
 
 #include "csa2_device.cuh"
@@ -117,10 +117,10 @@ __device__ __forceinline__ void exact_codes(const uint4* r, const float* gamma, 
 // stored, so that the result does not depend on whether a later launch reads the
 // residual again.  A thread writes only columns that it has read, which is what
 // allows residual_out to be residual.
-template <int V, bool F32>
-__global__ void __launch_bounds__(256) add_norm_kernel(const __grid_constant__ AddNormParams p) {
+template <int V, bool F32, int MOST>
+__global__ void __launch_bounds__(MOST) add_norm_kernel(const __grid_constant__ AddNormParams p) {
   constexpr int kWords = F32 ? 4 : 2;  // 16-byte words of a run of the residual
-  __shared__ float part[8];
+  __shared__ float part[MOST / 32];
   pdl_wait();
   pdl_trigger();
   const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(256) add_norm_kernel(const __grid_constant__ A
   }
 }
 
-template <int V>
+template <int V, int MOST>
 cudaError_t launch_v(const csa2_add_norm_fp8_args& a, const AddNormParams& p, cudaStream_t st) {
   // whole warps, no more than the row's runs need
   const int threads = ((a.K + 16 * V - 1) / (16 * V) + 31) / 32 * 32;
@@ -267,8 +267,8 @@ cudaError_t launch_v(const csa2_add_norm_fp8_args& a, const AddNormParams& p, cu
   // 512: 6.5 -> 5.1 us, 16,000 x 512: 16.6 -> 11.2 us, 600 x 512: 2.2 us either way).
   const int rows = threads == 32 ? 2 : 1;
   const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows)), block(threads, rows);
-  return a.residual_f32 ? launch_pdl(add_norm_kernel<V, true>, grid, block, 0, st, p)
-                        : launch_pdl(add_norm_kernel<V, false>, grid, block, 0, st, p);
+  return a.residual_f32 ? launch_pdl(add_norm_kernel<V, true, MOST>, grid, block, 0, st, p)
+                        : launch_pdl(add_norm_kernel<V, false, MOST>, grid, block, 0, st, p);
 }
 
 }  // namespace
@@ -277,9 +277,13 @@ cudaError_t launch_add_norm_fp8(const csa2_add_norm_fp8_args& a, cudaStream_t st
   const AddNormParams p{reinterpret_cast<const __nv_bfloat16*>(a.x), a.residual, a.residual_out, a.gamma, a.codes, a.scale,
                         reinterpret_cast<__nv_bfloat16*>(a.y), a.ld_x, a.ld_residual, a.ld_residual_out, a.ld_codes,
                         a.ld_scale, a.ld_y, a.T, a.K, a.eps};
-  if (a.K <= 4096) return launch_v<1>(a, p, st);
-  if (a.K <= 8192) return launch_v<2>(a, p, st);
-  return launch_v<4>(a, p, st);
+  // Runs a thread, and threads a CTA at most.  Up to two rows an SM want the shorter work a
+  // thread (8 x 7,168: 3.1 us with one run, 3.7 with two; 304 rows: 4.5 and 5.1), more rows
+  // the more CTAs an SM (456: 7.3 and 7.0; 4,096: 48.8 and 40.0); four runs hold registers for
+  // too few warps (2,048 x 16,384: 53.9 us, 48.0 with two).
+  if (a.K <= 4096) return launch_v<1, 256>(a, p, st);
+  if (a.K > 8192) return launch_v<2, 512>(a, p, st);
+  return a.T <= 304 ? launch_v<1, 512>(a, p, st) : launch_v<2, 256>(a, p, st);
 }
 
 }  // namespace csa2

@@ -13,7 +13,7 @@
 // Two kernels, both bound by latency: launch, ids, operands, products, sums.  For few rows
 // a CTA takes 16 of them, one of their adapters and 8 of its ranks, its 8 to 32 warps the
 // blocks of 128 input dims in turn, added in warp order: 8 x 7,168 x 512 with 8 adapters
-// takes 8.4 us with its projection, 4.7 without adapters.  For many a CTA takes 128 rows,
+// takes 8.3 us with its projection, 4.7 without adapters.  For many a CTA takes 128 rows,
 // 64 ranks and a share of the input dims, and goes through the tile's adapters with a in a
 // ring in shared memory; a cluster adds the shares in rank order: about 12 us of the 268 of
 // 4,096 x 2,048 x 32,768 at rank 64.
