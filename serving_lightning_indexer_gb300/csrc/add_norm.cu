@@ -44,6 +44,8 @@ __device__ __forceinline__ void pack16(const float (&y)[16], uint4 (&v)[2]) {
 // six roundings to either side have one code, that is the code; where not (some 9 of a
 // million values), exact_codes decides.  With fp32's own roundings instead, 13 of 29.4 M codes
 // of 4,096 x 7,168 are on the other side of a border, and it takes 38.1 us, 40.1 so.
+// Of blocks with a smaller or no finite a, of the norm itself.
+constexpr float kLeastTop = 8.271806125530277e-25f;  // 2^-80: its products' second parts are normal
 constexpr float kNear = 3.5762786865234375e-7f;  // 6 x 2^-24
 
 // A magnitude in two parts; the larger of two, without a NaN.
@@ -107,6 +109,33 @@ __device__ __forceinline__ void exact_codes(const uint4* r, const float* gamma, 
     q[1] = i == 1 ? v : q[1];
     q[2] = i == 2 ? v : q[2];
     q[3] = i == 3 ? v : q[3];
+  }
+}
+
+// A run of r from its words.
+template <bool F32>
+__device__ __forceinline__ void values(const uint4 (&v)[F32 ? 4 : 2], float (&y)[16]) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[4 * i] = __uint_as_float(v[i].x);
+      y[4 * i + 1] = __uint_as_float(v[i].y);
+      y[4 * i + 2] = __uint_as_float(v[i].z);
+      y[4 * i + 3] = __uint_as_float(v[i].w);
+    }
+  } else {
+    unpack16(v, y);
+  }
+}
+// y = y * by * gamma
+__device__ __forceinline__ void scaled(float (&y)[16], float by, const float* gamma) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 g = __ldg(reinterpret_cast<const float4*>(gamma + i));
+    y[i] = y[i] * by * g.x;
+    y[i + 1] = y[i + 1] * by * g.y;
+    y[i + 2] = y[i + 2] * by * g.z;
+    y[i + 3] = y[i + 3] * by * g.w;
   }
 }
 
@@ -193,17 +222,7 @@ __global__ void __launch_bounds__(MOST) add_norm_kernel(const __grid_constant__ 
     const int c = (r * threads + tid) * 16;
     const bool in = c < p.K;
     float y[16];  // r * gamma
-    if constexpr (F32) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[4 * i] = __uint_as_float(rv[r][i].x);
-        y[4 * i + 1] = __uint_as_float(rv[r][i].y);
-        y[4 * i + 2] = __uint_as_float(rv[r][i].z);
-        y[4 * i + 3] = __uint_as_float(rv[r][i].w);
-      }
-    } else {
-      unpack16(rv[r], y);
-    }
+    values<F32>(rv[r], y);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const float4 g = in ? __ldg(reinterpret_cast<const float4*>(p.gamma + c + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -212,49 +231,59 @@ __global__ void __launch_bounds__(MOST) add_norm_kernel(const __grid_constant__ 
       y[i + 2] *= g.z;
       y[i + 3] *= g.w;
     }
-    if (p.y && in) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
+    top = max8(top);
+    const float a = top * inv;
+    // the same in a block's lanes
+    const bool usual = !in || (top >= kLeastTop && top <= kLargest && a >= kAmaxFloor && a <= kLargest);
+    auto store_y = [&](float by) {
       float n[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) n[i] = y[i] * inv;
+      for (int i = 0; i < 16; ++i) n[i] = y[i] * by;
       uint4 h[2];
       pack16(n, h);
       uint4* dst = reinterpret_cast<uint4*>(p.y + t * p.ld_y + c);
       dst[0] = h[0];
       dst[1] = h[1];
+    };
+    if (p.y && in && usual) store_y(inv);
+    float s = a / kE4m3Max;
+    uint32_t q[4], differ = 0;
+    if (p.codes && usual) {
+      const float f = kE4m3Max / top, less = f * (1.f - kNear), more = f * (1.f + kNear);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q[i] = e4m3x4(y[4 * i] * less, y[4 * i + 1] * less, y[4 * i + 2] * less, y[4 * i + 3] * less);
+        differ |= q[i] ^ e4m3x4(y[4 * i] * more, y[4 * i + 1] * more, y[4 * i + 2] * more, y[4 * i + 3] * more);
+      }
     }
-    if (p.codes) {
-      float top = 0.f;
+    if (__builtin_expect(!__all_sync(0xffffffffu, usual), 0)) {
+      // a block's norm is zero or next to it, or it or r * gamma is not finite: from the stored r
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
-      top = max8(top);
-      const float a = top * inv;
-      const bool usual = !in || (top <= kLargest && a >= kAmaxFloor && a <= kLargest);  // the same in a block's lanes
-      float s = a / kE4m3Max;
-      uint32_t q[4], differ = 0;
-      if (usual) {
-        const float f = kE4m3Max / top, less = f * (1.f - kNear), more = f * (1.f + kNear);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          q[i] = e4m3x4(y[4 * i] * less, y[4 * i + 1] * less, y[4 * i + 2] * less, y[4 * i + 3] * less);
-          differ |= q[i] ^ e4m3x4(y[4 * i] * more, y[4 * i + 1] * more, y[4 * i + 2] * more, y[4 * i + 3] * more);
-        }
-      }
-      if (__builtin_expect(!__all_sync(0xffffffffu, usual), 0)) {  // a block's norm is zero or next to it, or not finite
-        float f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = in ? y[i] * inv : 0.f;  // 0 * inv is NaN where inv is infinite
-        const float scale = e4m3_block(max8(amax16(y)), &f);        // by all lanes
-        if (!usual) {
-          const uint4 w = codes16(y, f);
-          q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
-          s = scale;
-        }
-      }
-      if (__builtin_expect(__any_sync(0xffffffffu, differ != 0), 0)) exact_codes<F32, V>(out + c / 16 * kWords, p.gamma + c, in, usual, q);
+      for (int i = 0; i < 16; ++i) y[i] = 0.f;
       if (in) {
-        *reinterpret_cast<uint4*>(p.codes + t * p.ld_codes + c) = make_uint4(q[0], q[1], q[2], q[3]);
-        if ((tid & 7) == 0) p.scale[t * p.ld_scale + (c >> 7)] = s;
+        uint4 v[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) v[i] = out[c / 16 * kWords + i];
+        values<F32>(v, y);
+        scaled(y, inv, p.gamma + c);
       }
+      if (p.y && in && !usual) store_y(1.f);
+      __syncwarp();
+      float f;
+      const float scale = e4m3_block(max8(amax16(y)), &f);  // by all lanes
+      if (!usual) {
+        const uint4 w = codes16(y, f);
+        q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
+        s = scale;
+      }
+    }
+    if (__builtin_expect(__any_sync(0xffffffffu, differ != 0), 0)) exact_codes<F32, V>(out + c / 16 * kWords, p.gamma + c, in, usual, q);
+    if (p.codes && in) {
+      *reinterpret_cast<uint4*>(p.codes + t * p.ld_codes + c) = make_uint4(q[0], q[1], q[2], q[3]);
+      if ((tid & 7) == 0) p.scale[t * p.ld_scale + (c >> 7)] = s;
     }
   }
 }

@@ -149,6 +149,50 @@ def test_add_norm_special_rows():
     assert (r[5] == 2.0 ** 70).all() and not v[5].any() and (s[5] == 1).all()
 
 
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [256, 5120, 8208])
+def test_add_norm_products_below_fp32(K, kind):
+    """r * gamma next to fp32's smallest values, where the norm is not."""
+    dev, x, res, gamma = _norm_case(3, K, kind, 8)
+    x, res = x * 2.0 ** -50, res * 2.0 ** -50
+    gamma.mul_(2.0 ** -40)
+    x[1], res[1] = x[1] * 2.0 ** -10, res[1] * 2.0 ** -10
+    gamma[:128] *= 2.0 ** -10
+    r, codes = torch.empty_like(res), torch.empty(3, K, dtype=torch.uint8, device=dev)
+    scale, y = torch.empty(3, -(-K // 128), device=dev), torch.empty(3, K, dtype=torch.bfloat16, device=dev)
+    csa2.add_norm_fp8(x, res, r, gamma, codes=codes, scale=scale, y=y, eps=1e-37)
+    _sync_ok()
+    _check_norm(x, res, gamma, float(np.float32(1e-37)), r, codes, scale, y)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [256, 5120, 8208])
+def test_add_norm_products_past_fp32(K, kind):
+    """r * gamma leaves fp32 where the norm does not, and where the squares do (zeros)."""
+    dev, x, res, gamma = _norm_case(4, K, kind, 7)
+    x[0], x[1], x[2], x[3] = x[0] * 2.0 ** 30, x[1] * 2.0 ** -90, x[2] * 2.0 ** 100, x[3]
+    res[0], res[1], res[2] = res[0] * 2.0 ** 30, res[1] * 2.0 ** -90, res[2] * 2.0 ** 100
+    gamma.mul_(2.0 ** 100)
+    gamma[K // 2:] *= 2.0 ** -230
+    nb = -(-K // 128)
+    r, y = torch.empty_like(res), torch.empty(4, K, dtype=torch.bfloat16, device=dev)
+    codes, scale = torch.empty(4, K, dtype=torch.uint8, device=dev), torch.empty(4, nb, device=dev)
+    csa2.add_norm_fp8(x, res, r, gamma, codes=codes, scale=scale, y=y)
+    _sync_ok()
+    assert not codes[2].bitwise_and(0x7F).any() and not y[2].any() and (scale[2] == 1).all()
+    half = K // 2
+    for t in (0, 1, 3):     # gamma is 2^-130 in the second half: what is not told from zero there
+        _, want = o.add_norm_rows(f64(x[t:t + 1]), np_(res[t:t + 1].double()), f64(gamma), 1e-6, fp32=kind == torch.float32)
+        e = 44 * U
+        got = f64(y[t:t + 1])
+        assert np.all(np.abs(got - want)[:, :half] <= (2.0 ** -8 * (1 + e) + e) * np.abs(want)[:, :half])
+        assert np.all(np.abs(got - want)[:, half:] <= 2.0 ** -8 * np.abs(want)[:, half:] + 2.0 ** -133)
+        first = half // 128
+        s, m = o.e4m3_block_scales(want, 1)
+        assert np.all(np.abs(np_(scale[t:t + 1]) - s)[:, :first] <= (e + 2 * U) * s[:, :first])
+        _assert_codes(np_(codes[t:t + 1])[:, :first * 128], (want * o.expand_blocks(m, 1, 1, K))[:, :first * 128], 2 * e + 2 * U, "past")
+
+
 # ---------------------------------------------------------------- adapters
 def _adapters(n, N, K, R, g, dev):
     a = (torch.randn(n, R, K, generator=g, device=dev) / K ** 0.5).to(torch.bfloat16)
