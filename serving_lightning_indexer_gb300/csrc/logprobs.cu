@@ -21,6 +21,8 @@
 // cluster of CTAs a row splits (8 x 131,072 fp32: 3.6 us, 7.7 with 20 alternatives).
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "csa2_device.cuh"
 #include "csa2_internal.h"
 
@@ -629,9 +631,11 @@ cudaError_t launch(const LogprobParams& p, int T, int splits, const DeviceCtx& c
   constexpr auto kern = logprobs_kernel<F32, TOP, NW, DEEP, SPLIT>;
   cudaError_t e = prefer_max_smem_once<kern>(ctx.device, kSmem);
   if (e != cudaSuccess) return e;
-  if (splits > 8) {
+  static std::atomic<bool> above8[64];  // clusters of more CTAs have to be allowed, once a device
+  if (splits > 8 && !above8[ctx.device].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    above8[ctx.device].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(NW == 1 ? (T + kLpWarps - 1) / kLpWarps : T * splits);
