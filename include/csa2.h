@@ -539,9 +539,9 @@ CSA2_API int csa2_add_norm_fp8(const csa2_add_norm_fp8_args* args, void* stream)
  * before RoPE and the rounding to the output's type.  row_adapter[t] = -1: none (the
  * row's output is then that of csa2_fp8_linear); an id outside [-1, n_adapters)
  * counts as none and is recorded (CSA2_ERR_DEVICE_BOUNDS).  Rows of one adapter may
- * be anywhere; side by side they take the least time.  v is held as the bf16 nearest
- * to its fp32 sum for bf16 output, as the sum of three bf16 (2^-25 of it) for fp32 and
- * e4m3 output.  An infinity or NaN of one adapter stays in its
+ * be anywhere; side by side they take the least time.  v's fp32 sum is held as the sum
+ * of two bf16 (2^-17 of it) for bf16 output, of three (all of it) for fp32 and e4m3
+ * output.  An infinity or NaN of one adapter stays in its
  * own rows.
  * base: the arguments of csa2_fp8_linear, with its rules; T at most 2^20; w_ready = 1
  * says the same of a, b, adapter_scale and row_adapter as of w and w_scale.  rank is

@@ -183,8 +183,13 @@ struct LoraInner {
 };
 constexpr int kLoraMaxRows = 1 << 20;
 constexpr int kLoraListWords = 132;
-constexpr int kLoraPlanes = 3;  // at most; the inner products' bf16 parts by the output's format
-inline int lora_planes(int out_format) { return out_format == CSA2_OUT_BF16 ? 1 : kLoraPlanes; }
+// The bf16 parts that hold an inner product, by the output's format.  Two leave at most 2^-17 of
+// it, where bf16 output is rounded by up to 2^-8 (one would leave 2^-8 too: one output in 15 was
+// the other neighbour of its value, 1.72e-3 off the 64-bit one where fp32 sums are 1.66e-3).
+// Three hold all of it: fp32 output shows 2^-17, and e4m3 output a code on the other side of a
+// border, 2^-3 of its value.
+constexpr int kLoraPlanes = 3;  // at most
+constexpr int lora_planes(int out_format) { return out_format == CSA2_OUT_BF16 ? 2 : kLoraPlanes; }
 inline int lora_pitch(int rank) { return (rank + 63) / 64 * 64; }  // rows of whole 128-byte words
 size_t lora_workspace_bytes(int T, int rank);
 LoraInner lora_inner_at(const csa2_lora_linear_args& a, void* ws, bool lists);

@@ -10,11 +10,11 @@
 // they are few, by latency (8 x 7,168 x 512: 4.6 us).
 //
 // LORA: each adapter that a tile's rows use (lora.cu lists them) brings one more block for
-// every 64 ranks, or 32 where the inner products v are held in three bf16: bf16
-// products of the rows' v with the adapter's b, summed like the others but only to the rows that have the adapter.  The
+// every 64 or 32 ranks, whichever fit a stage: bf16 products of the parts of the rows' v with
+// the adapter's b, summed like the others but only to the rows that have the adapter.  The
 // projection's own blocks come first, and only what lora.cu wrote waits for it.  4,096 x
-// 2,048 x 32,768 with 4 adapters of rank 64: 268 us, 249 without adapters; 64 rows with 16
-// of rank 32: 24.5 us, 16.2 without, of which b's bytes are 5.
+// 2,048 x 32,768 with 4 adapters of rank 64: 287 us, 249 without adapters (an adapter takes two
+// blocks there); 64 rows with 16 of rank 32: 25.6 us, 16.2 without adapters, and b's bytes are 5 more.
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -63,13 +63,14 @@ struct LoraParams<true> {
   int run;     // ranks of a block
   int pieces;  // blocks of an adapter
   int planes;  // of v
+  int v_rows;  // of a plane of v in a stage
 };
 // Bytes of a row of v or b of some ranks in shared memory.  The least that hold them: a box
 // whose rows end far past the matrix's costs time (64 x 2,048 x 32,768 with 16 adapters of
 // rank 8: 43 us with 128, 26 with 32), though less than plain copies of the rows (50 us).
 __host__ __device__ __forceinline__ int lora_row_bytes(int ranks) { return ranks <= 16 ? 32 : ranks <= 32 ? 64 : 128; }
 // Block i of a tile's adapters: the adapter, where its ranks start and how many there are.
-// In a stage b comes first, then the planes of v, whose products with it are one sum.
+// In a stage the planes of v come first, whose products with b, behind them, are one sum.
 struct LoraBlock {
   int adapter, rank0, ranks, row;
   __device__ __forceinline__ LoraBlock(const LoraParams<true>& lo, const int* list, int i) {
@@ -79,28 +80,28 @@ struct LoraBlock {
     ranks = min(lo.run, lo.rank - rank0);
     row = lora_row_bytes(ranks);
   }
-  __device__ __forceinline__ void expect(const LoraParams<true>& lo, uint64_t* full, int v_rows, int b_rows) const {
-    mbar_arrive_expect_tx(full, (lo.planes * v_rows + b_rows) * row);
+  __device__ __forceinline__ void expect(const LoraParams<true>& lo, uint64_t* full, int b_rows) const {
+    mbar_arrive_expect_tx(full, (lo.planes * lo.v_rows + b_rows) * row);
   }
   // Behind b's columns, and in the columns of 8 ranks without a partner, are zeros.
   __device__ __forceinline__ void copy_b(const LoraParams<true>& lo, uint8_t* stage, uint64_t* full, int n0, int N,
                                          uint64_t policy) const {
-    tma_load_2d(stage, ranks < lo.run ? &lo.map_b_last : &lo.map_b, rank0 * 2, adapter * N + n0, full, policy);
+    tma_load_2d(stage + lo.planes * lo.v_rows * row, ranks < lo.run ? &lo.map_b_last : &lo.map_b, rank0 * 2, adapter * N + n0,
+                full, policy);
   }
-  __device__ __forceinline__ void copy_v(const LoraParams<true>& lo, uint8_t* stage, uint64_t* full, int t0, int T, int v_rows,
-                                         int b_rows, uint64_t policy) const {
+  __device__ __forceinline__ void copy_v(const LoraParams<true>& lo, uint8_t* stage, uint64_t* full, int t0, int T,
+                                         uint64_t policy) const {
     for (int i = 0; i < lo.planes; ++i)
-      tma_load_2d(stage + (b_rows + i * v_rows) * row, ranks < lo.run ? &lo.map_v_last : &lo.map_v, rank0 * 2, i * T + t0, full,
-                  policy);
+      tma_load_2d(stage + i * lo.v_rows * row, ranks < lo.run ? &lo.map_v_last : &lo.map_v, rank0 * 2, i * T + t0, full, policy);
   }
-  // The block's products; V_FIRST: v is the first operand.
+  // The block's products; V_FIRST: v is the first operand, of whose 128 rows those from v_rows on
+  // are whatever follows in the stage: rows that the output does not have.
   template <bool V_FIRST>
-  __device__ __forceinline__ void products(const LoraParams<true>& lo, uint32_t d, const uint8_t* stage, int v_rows, int b_rows,
-                                           uint32_t idesc) const {
-    const uint64_t bd = smem_desc_rows(stage, row);
+  __device__ __forceinline__ void products(const LoraParams<true>& lo, uint32_t d, const uint8_t* stage, uint32_t idesc) const {
+    const uint64_t bd = smem_desc_rows(stage + lo.planes * lo.v_rows * row, row);
     const int steps = (ranks + 15) >> 4;  // of 16 ranks
     for (int i = 0; i < lo.planes; ++i) {
-      const uint64_t vd = smem_desc_rows(stage + (b_rows + i * v_rows) * row, row);
+      const uint64_t vd = smem_desc_rows(stage + i * lo.v_rows * row, row);
       for (int k = 0; k < steps; ++k)
         umma_bf16(d, (V_FIRST ? vd : bd) + 2 * k, (V_FIRST ? bd : vd) + 2 * k, idesc, i + k > 0 ? 1u : 0u);
     }
@@ -154,8 +155,9 @@ template <int BN, bool LORA>
 struct WideCfg {
   static constexpr int kStages = 4;
   static constexpr int kStageBytes = (kTileM + BN) * kBlockK;
-  static_assert((kLoraPlanes * kTileM + BN) * 64 <= kStageBytes, "a block of 32 ranks in all planes fits");
   static constexpr int kAccs = 512 / BN;          // TMEM ring: 512 columns
+  // an issuer waits for every phase of the stages that it waits for at all
+  static_assert(kStages % kAccs == 0, "a stage's blocks are all of one accumulator");
   static constexpr int kCols = BN / 2;            // columns of a tile an accumulation warp holds
   static constexpr int kOffOut = kStages * kStageBytes;  // 32 rows x 64 B of output per accumulation warp
   static constexpr int kScaleSlots = 4;                  // ring of the scales of four blocks: 128 rows, 2 column halves
@@ -545,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = static_cast<int>(it % S);
             if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>((it / S) & 1) ^ 1u, s_abort))) break;
             uint8_t* dst = smem + s * Cfg::kStageBytes;
-            at.expect(lo, &full[s], kTileM, BN);
-            at.copy_v(lo, dst, &full[s], t0, p.T, kTileM, BN, keep);
+            at.expect(lo, &full[s], BN);
+            at.copy_v(lo, dst, &full[s], t0, p.T, keep);
             at.copy_b(lo, dst, &full[s], n0, p.N, keep);
           }
         }
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (; next < extra && ok; next += NA) {
             const LoraBlock at = adapters.at(next);
             ok = block([&](uint64_t, uint64_t) {
-              at.products<true>(lo, d, smem + s * Cfg::kStageBytes, kTileM, BN, idesc_b);
+              at.products<true>(lo, d, smem + s * Cfg::kStageBytes, idesc_b);
             });
           }
           next -= extra;
@@ -716,13 +718,13 @@ long long wide_tiles(const csa2_fp8_linear_args& a) {
 }
 
 // With adapters: their inner products, and the lists of tiles of 128 rows, are launched
-// first and described to the projection with tiles of `rows` rows and `columns` columns.
-// Nothing without.
-cudaError_t prepare_lora(const NoLora&, LoraParams<false>*, int, int, long long, const DeviceCtx&, cudaStream_t, const char**) {
+// first and described to the projection with tiles of `rows` rows and `columns` columns and
+// stages of `stage` bytes.  Nothing without.
+cudaError_t prepare_lora(const NoLora&, LoraParams<false>*, int, int, int, long long, const DeviceCtx&, cudaStream_t, const char**) {
   return cudaSuccess;
 }
-cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int columns, long long ctas, const DeviceCtx& ctx,
-                         cudaStream_t st, const char** why) {
+cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int columns, int stage, long long ctas,
+                         const DeviceCtx& ctx, cudaStream_t st, const char** why) {
   const csa2_lora_linear_args& a = *l.args;
   const LoraInner to = lora_inner_at(a, l.workspace, rows == kTileM);
   lo->n_adapters = a.n_adapters;
@@ -730,17 +732,20 @@ cudaError_t prepare_lora(const WithLora& l, LoraParams<true>* lo, int rows, int 
   lo->row_adapter = a.row_adapter;
   lo->lists = to.lists;
   lo->planes = lora_planes(a.base.out_format);
-  // with b of 32 ranks all planes of v fit a stage
-  lo->run = lo->planes == 1 ? 64 : 32;
+  // The ranks of a block are 64 where b and all planes of v fit a stage, else 32 (they do with 3 x
+  // 128 rows).  Up to 64 rows take as many of a tile of 128 (64 x 2,048 x 32,768 with 16 adapters of
+  // rank 64: 31.6 us, 45.6 with 128 and so 32 ranks; rank 32: 25.6 and 27.2).
+  lo->v_rows = a.base.T <= 64 && rows > 64 ? 64 : rows;
+  lo->run = (lo->planes * lo->v_rows + columns) * 128 <= stage ? 64 : 32;
   lo->pieces = (a.rank + lo->run - 1) / lo->run;
   const uint64_t row = 2 * static_cast<uint64_t>(a.rank);
   const uint64_t v_row = 2 * static_cast<uint64_t>(lora_pitch(a.rank));
-  const uint64_t v_rows = lo->planes * static_cast<uint64_t>(a.base.T), b_rows = static_cast<uint64_t>(a.n_adapters) * a.base.N;
+  const uint64_t v_all = lo->planes * static_cast<uint64_t>(a.base.T), b_rows = static_cast<uint64_t>(a.n_adapters) * a.base.N;
   auto encode = [&](int bytes, CUtensorMap* v, CUtensorMap* b) {
     const CUtensorMapSwizzle swizzle = bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
                                        : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                      : CU_TENSOR_MAP_SWIZZLE_128B;
-    return encode_tmap_2d_u8(v, to.v, v_row, v_rows, v_row, bytes, rows, swizzle) == CUDA_SUCCESS &&
+    return encode_tmap_2d_u8(v, to.v, v_row, v_all, v_row, bytes, lo->v_rows, swizzle) == CUDA_SUCCESS &&
            encode_tmap_2d_u8(b, a.b, row, b_rows, row, bytes, columns, swizzle) == CUDA_SUCCESS;
   };
   const int last = a.rank % lo->run;
@@ -767,7 +772,7 @@ cudaError_t launch_wide(const csa2_fp8_linear_args& a, const LinearParams& p, co
   cudaError_t e = prefer_max_smem_once<fp8_linear_wide_kernel<BN, OUT, SPLIT, L::kOn>>(ctx.device, WideCfg<BN, L::kOn>::kSmem);
   if (e != cudaSuccess) return e;
   LoraParams<L::kOn> lo{};
-  e = prepare_lora(lora, &lo, kTileM, BN, SPLIT ? 2 * wide_tiles<BN>(a) : wide_tiles<BN>(a), ctx, st, why);
+  e = prepare_lora(lora, &lo, kTileM, BN, WideCfg<BN, L::kOn>::kStageBytes, SPLIT ? 2 * wide_tiles<BN>(a) : wide_tiles<BN>(a), ctx, st, why);
   if (e != cudaSuccess) return e;
   const long long tiles = wide_tiles<BN>(a);
   cudaLaunchConfig_t cfg = {};
@@ -800,11 +805,13 @@ constexpr int kScaleSeg = 16;  // blocks whose scales are staged at a time (even
 // Of n blocks, those that a cluster's CTA `rank` takes: rank, rank + splits, ..
 __device__ __forceinline__ int shares_of(int n, int rank, int splits) { return n > rank ? (n - rank - 1) / splits + 1 : 0; }
 
-template <int NT, bool LORA>
+template <int NT, int OUT, bool LORA>
 struct NarrowCfg {
   static constexpr int kStages = 4;
-  static constexpr int kStageBytes = (128 + NT) * kBlockK;
-  static_assert((kLoraPlanes * NT + 128) * 64 <= kStageBytes, "a block of 32 ranks in all planes fits");
+  static constexpr int kBlockBytes = (128 + NT) * kBlockK;
+  // room for a block of 64 ranks in two planes (16 x 2,048 x 32,768 with 16 adapters of rank 64:
+  // 26.4 us, 32.1 with blocks of 32 ranks in stages of kBlockBytes; 32 rows: 32.7 and 41.2)
+  static constexpr int kStageBytes = LORA && lora_planes(OUT) == 2 ? (128 + 2 * NT) * 128 : kBlockBytes;
   static constexpr int kAccs = 4;
   static constexpr int kCols = kAccs * NT < 32 ? 32 : kAccs * NT;
   static constexpr int kOffScales = kStages * kStageBytes;  // the parts [NT][128] reuse the stages
@@ -819,7 +826,7 @@ template <int NT, int OUT, bool LORA>
 __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     fp8_linear_narrow_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                              const __grid_constant__ LinearParams p, const __grid_constant__ LoraParams<LORA> lo) {
-  using Cfg = NarrowCfg<NT, LORA>;
+  using Cfg = NarrowCfg<NT, OUT, LORA>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -855,7 +862,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
     prefetch_tmap(&map_w);
     if (LORA || p.w_ready) {  // the first weights do not wait for the previous launch
       for (int b = 0; b < min(S, blocks); ++b) {
-        mbar_arrive_expect_tx(&full[b], Cfg::kStageBytes);
+        mbar_arrive_expect_tx(&full[b], Cfg::kBlockBytes);
         tma_load_2d(smem + b * Cfg::kStageBytes, &map_w, (b0 + b) * kBlockK, n0, &full[b], pol_w);
       }
     }
@@ -883,7 +890,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
         if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
         uint8_t* dst = smem + s * Cfg::kStageBytes;
         if (b >= S || !(LORA || p.w_ready)) {
-          mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+          mbar_arrive_expect_tx(&full[s], Cfg::kBlockBytes);
           tma_load_2d(dst, &map_w, (b0 + b) * kBlockK, n0, &full[s], pol_w);
         }
         tma_load_2d(dst + 128 * kBlockK, &map_x, (b0 + b) * kBlockK, t0, &full[s], pol_x);
@@ -896,21 +903,21 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
           const int s = b % S;
           if (b >= S && !(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
           const LoraBlock at(lo, s_list, rank + i * splits);
-          at.expect(lo, &full[s], NT, 128);
+          at.expect(lo, &full[s], 128);
           at.copy_b(lo, smem + s * Cfg::kStageBytes, &full[s], n0, p.N, pol_x);
         }
         if (b > blocks) pdl_wait();
         for (int i = 0; blocks + i < b; ++i) {
           const int s = (blocks + i) % S;
-          LoraBlock(lo, s_list, rank + i * splits).copy_v(lo, smem + s * Cfg::kStageBytes, &full[s], t0, p.T, NT, 128, pol_x);
+          LoraBlock(lo, s_list, rank + i * splits).copy_v(lo, smem + s * Cfg::kStageBytes, &full[s], t0, p.T, pol_x);
         }
         for (int i = ahead; ok && i < extra; ++i, ++b) {
           const int s = b % S;
           if (!(ok = mbar_wait(&empty[s], static_cast<uint32_t>(b / S - 1) & 1u, s_abort))) break;
           const LoraBlock at(lo, s_list, rank + i * splits);
-          at.expect(lo, &full[s], NT, 128);
+          at.expect(lo, &full[s], 128);
           at.copy_b(lo, smem + s * Cfg::kStageBytes, &full[s], n0, p.N, pol_x);
-          at.copy_v(lo, smem + s * Cfg::kStageBytes, &full[s], t0, p.T, NT, 128, pol_x);
+          at.copy_v(lo, smem + s * Cfg::kStageBytes, &full[s], t0, p.T, pol_x);
         }
       }
       if (!ok) {
@@ -948,7 +955,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT == 64 ? 1 : 2)
         for (int i = 0; ok && i < extra; ++i) {
           const LoraBlock at(lo, s_list, rank + i * splits);
           ok = block([&](uint32_t d, uint64_t, uint64_t) {
-            at.products<false>(lo, d, smem + (b % S) * Cfg::kStageBytes, NT, 128, idesc_b);
+            at.products<false>(lo, d, smem + (b % S) * Cfg::kStageBytes, idesc_b);
           });
         }
       }
@@ -1192,7 +1199,7 @@ long long wide_time(const csa2_fp8_linear_args& a, const DeviceCtx& ctx) {
 template <int NT, int OUT, class L>
 cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, const L& lora, const DeviceCtx& ctx,
                           cudaStream_t st, const char** why, bool* taken) {
-  constexpr int kSmem = NarrowCfg<NT, L::kOn>::kSmem;
+  constexpr int kSmem = NarrowCfg<NT, OUT, L::kOn>::kSmem;
   auto kern = fp8_linear_narrow_kernel<NT, OUT, L::kOn>;
   const long long n_tiles = (static_cast<long long>(a.N) + 127) / 128;
   const int t_tiles = (a.T + NT - 1) / NT, blocks = (a.K + 127) / 128;
@@ -1236,7 +1243,7 @@ cudaError_t launch_narrow(const csa2_fp8_linear_args& a, const LinearParams& p, 
     return cudaErrorInvalidValue;
   }
   LoraParams<L::kOn> lo{};
-  e = prepare_lora(lora, &lo, NT, 128, tiles * splits, ctx, st, why);
+  e = prepare_lora(lora, &lo, NT, 128, NarrowCfg<NT, OUT, L::kOn>::kStageBytes, tiles * splits, ctx, st, why);
   if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, p, lo);
 }

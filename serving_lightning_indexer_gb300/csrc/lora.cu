@@ -5,17 +5,17 @@
 //
 // The codes are exact in bf16 and a is bf16, so a block's 128 products are summed by
 // the tensor core in fp32 and the block's scale is applied to the sum.  The result is
-// written as the bf16 nearest to it and, but for bf16 output, the bf16 nearest to what that
-// leaves, and again (2^-25 together): two would leave fp32 output 2^-17 of v off, and e4m3
-// output, where a code on the other side of its border is 2^-3 off however near the border
-// was, three times the codes there that fp32's own roundings do.
+// written as the bf16 nearest to it, the bf16 nearest to what that leaves (at most 2^-17 of it is
+// left, for bf16 output next to nothing) and, but for bf16 output, what that leaves: two would leave
+// fp32 output 2^-17 of v off, and e4m3 output, where a code on the other side of its border is
+// 2^-3 off however near the border was, three times the codes there that fp32's own roundings do.
 //
 // Two kernels, both bound by latency: launch, ids, operands, products, sums.  For few rows
 // a CTA takes 16 of them, one of their adapters and 8 of its ranks, its 8 to 32 warps the
 // blocks of 128 input dims in turn, added in warp order: 8 x 7,168 x 512 with 8 adapters
-// takes 8.3 us with its projection, 4.7 without adapters.  For many a CTA takes 128 rows,
+// takes 8.4 us with its projection, 4.7 without adapters.  For many a CTA takes 128 rows,
 // 64 ranks and a share of the input dims, and goes through the tile's adapters with a in a
-// ring in shared memory; a cluster adds the shares in rank order: about 12 us of the 268 of
+// ring in shared memory; a cluster adds the shares in rank order: about 12 us of the 287 of
 // 4,096 x 2,048 x 32,768 at rank 64.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,7 +36,7 @@ struct InnerParams {
   int* lists;  // NULL: the projection's tiles are smaller and make their own
   long long ld_x, ld_xs;
   int T, K, rank, pitch, n_adapters;
-  int planes;  // 1 or 3
+  int planes;  // 2 or 3
   int ready;   // a and row_adapter may be read before the previous launch completes
   uint32_t* err;
 };
