@@ -226,10 +226,13 @@ constexpr int kTileOffRaw = kTileXStages * kTileXBytes;  // blocks of codes, a l
 static_assert(kTileRows * kTileRanks * 4 <= kTileRaw * kTileRows * 128, "the sums fit where the codes were");
 constexpr int kTileOffA = kTileOffRaw + kTileRaw * kTileRows * 128;
 constexpr int kTileABytes = 3 * kTileRanks * 256;  // the ring of blocks of a: three of 64 ranks, four of 48
-// Rows' scales of the blocks between the farthest copied one, kTileRaw - 1 ahead of the
-// converting warps, and the one whose sums are added, kTileXStages behind them.
-constexpr int kTileScales = 8, kTileOffScales = kTileOffA + kTileABytes;
-static_assert(kTileRaw + kTileXStages <= kTileScales, "a scale stays until it is used");
+// Rows' scales, of the blocks between the farthest copied one and the first that a sum warp may
+// still have to read.  A converting warp asks for block b + kTileRaw - 1 when it has seen the
+// products of block b - 1 - kTileXStages complete; these were issued when every sum warp was
+// done with the product kTileAccs before them, so with one product a block the slowest warp may be
+// at block b - kTileXStages - kTileAccs: kTileRaw + kTileXStages + kTileAccs blocks in all.
+constexpr int kTileScales = 16, kTileOffScales = kTileOffA + kTileABytes;
+static_assert(kTileRaw + kTileXStages + kTileAccs <= kTileScales, "a scale stays until it is used");
 constexpr int kTileSmem = 1024 + kTileOffScales + kTileScales * kTileRows * 4;
 
 // Grid: row tiles, shares of the input dims (a cluster), runs of 64 ranks times slots;

@@ -22,7 +22,7 @@ from test_gpu_inputs import U, _gen, _sync_ok
 pytestmark = pytest.mark.gpu
 
 
-def _inputs(T, N, K, R, n, seed):
+def _inputs(T, N, K, R, n, seed, run=1):
     dev = need_gpu()
     g = _gen(dev, seed)
     nb = -(-K // 128)
@@ -37,7 +37,7 @@ def _inputs(T, N, K, R, n, seed):
     one = torch.arange(N, device=dev) % 2 == 0                                     # a single rank's product
     hot = torch.arange(N, device=dev)[:, None] // 2 % R == torch.arange(R, device=dev)
     b = torch.where(one[:, None] & ~hot, torch.zeros_like(b), b)
-    ids = torch.randint(-1, n, (T,), generator=g, device=dev, dtype=torch.int32)
+    ids = torch.randint(-1, n, (-(-T // run),), generator=g, device=dev, dtype=torch.int32).repeat_interleave(run)[:T].contiguous()
     return x, xs, w, ws, a, b, ids, 0.5 + torch.rand(n, generator=g, device=dev)
 
 
@@ -72,3 +72,22 @@ def test_lora_output_has_the_inner_products_bits(T, N, K, R, n, out):
     half = np.where(top > 0, np.exp2(np.floor(np.log2(np.where(top > 0, top, 1.0)))), 0.0) * torch.finfo(out).eps / 2
     err = np.abs(np_(y.double()) - want)
     assert np.all(err <= half + tol), (int((err > half + tol).sum()), float((err / (half + tol + 1e-300)).max()))
+
+
+@pytest.mark.parametrize("T,N,K,R,n,run", [
+    (4096, 512, 7168, 64, 4, 128), (4096, 512, 7168, 64, 9, 64), (4096, 512, 7168, 64, 30, 43), (4096, 256, 7168, 128, 4, 128),
+    (4096, 256, 7168, 128, 9, 60), (4096, 512, 7168, 16, 60, 16), (19000, 256, 2064, 64, 5, 128), (19000, 128, 2064, 32, 40, 50),
+    (200, 128, 32768, 64, 3, 50), (2432, 256, 16384, 48, 3, 300)])
+def test_lora_scales_of_long_shares(T, N, K, R, n, run):
+    """Nine blocks of input dims and more to a CTA of the many-rows kernel, with one adapter a tile,
+    two, three and more: a row's sums take the scales of their own blocks, again and again."""
+    x, xs, w, ws, a, b, ids, s = _inputs(T, N, K, R, n, T + N + R + run, run)
+    xs *= 2.0 ** (torch.arange(xs.shape[1], device=xs.device) % 7 - 3)
+    y, again = torch.empty(T, N, device=x.device), torch.empty(T, N, device=x.device)
+    csa2.lora_linear(x, xs, w, ws, a, b, ids, y, adapter_scale=s)
+    for _ in range(20):
+        csa2.lora_linear(x, xs, w, ws, a, b, ids, again, adapter_scale=s)
+        assert torch.equal(y, again)
+    _sync_ok()
+    want, mag, out_mag = _reference(x, xs, a, b, ids, s)
+    assert np.all(np.abs(np_(y.double()) - want) <= U * np.abs(want) + (-(-K // 128) + 10) * U * mag + (2 * R + 8) * U * out_mag)
