@@ -138,7 +138,7 @@ def load(build_if_missing: bool = False) -> C.CDLL:
     if not os.path.exists(path):
         if not build_if_missing:
             raise RuntimeError(f"libcsa2.so is not built ({path}); run __graft_entry__.build()")
-        _build.build()
+        _build.build_library()
     lib = C.CDLL(path)
     lib.csa2_status_string.restype = C.c_char_p
     lib.csa2_status_string.argtypes = [C.c_int]
@@ -513,6 +513,8 @@ def _load_call():
     load()
     if not os.path.exists(_build.CALL):
         raise RuntimeError(f"_csa2_call.so is not built ({_build.CALL}); run __graft_entry__.build()")
+    if _build.call_made_with() != _build.made_with():
+        raise RuntimeError(f"_csa2_call.so was built with {_build.call_made_with()}, this is {_build.made_with()}; run __graft_entry__.build()")
     loader = importlib.machinery.ExtensionFileLoader("_csa2_call", _build.CALL)
     _call = importlib.util.module_from_spec(importlib.util.spec_from_loader("_csa2_call", loader))
     loader.exec_module(_call)
