@@ -549,7 +549,8 @@ CSA2_API int csa2_add_norm_fp8(const csa2_add_norm_fp8_args* args, void* stream)
  * most 2^30.  An adapter of a smaller rank is padded with zeros.  Alignment: a, b 16 B;
  * row_adapter, adapter_scale 4 B; workspace 16 B: csa2_workspace_size(
  * CSA2_CALL_LORA_LINEAR, args, &bytes), read and written until the call's work is done,
- * so calls that may run at the same time need one each.  Results do not depend on
+ * so calls that may run at the same time need one each.  No output, nor the workspace,
+ * may overlap an input or another of them, which the call checks.  Results do not depend on
  * the launch's timing (no atomics); the order in which a row's parts are added, and so
  * its last bits, can depend on which adapters the rows around it have. */
 typedef struct {
@@ -577,7 +578,8 @@ CSA2_API int csa2_lora_linear(const csa2_lora_linear_args* args, void* workspace
  * the largest term apart, so that a likely token's log probability keeps its digits.
  * T * V is not limited; V at most 2^30, T at most 2^27, n_top at most 32.
  * Alignment: logits their own size (rows may start anywhere; 16-B aligned rows are
- * read fastest), the rest 4 B.  Outputs must not overlap the logits.  No workspace. */
+ * read fastest), the rest 4 B.  Outputs must not overlap the logits
+ * or each other, which the call checks.  No workspace. */
 typedef struct {
   const void* logits; int64_t ld_logits;       /* [T, V] bf16 or fp32, row stride ld_logits >= V */
   int32_t logits_f32;                          /* 0: bf16, 1: fp32 */

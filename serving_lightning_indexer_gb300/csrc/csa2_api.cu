@@ -75,18 +75,44 @@ bool g_ctx_ok[kMaxDevices];
 struct ByteRows {
   const void* at;
   long long n, rows, ld;
-  // Whether a run of this and a run of o have a byte in common: exact for equal
-  // strides or one run each, else whether the runs' spans meet.
+  // Whether a run of this and a run of o have a byte in common.
   bool meets(const ByteRows& o) const {
     if (!at || !o.at) return false;
     const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(o.at)) -
                         static_cast<long long>(reinterpret_cast<uintptr_t>(at));
     if (d >= (rows - 1) * ld + n || -d >= (o.rows - 1) * o.ld + o.n) return false;
-    if (ld != o.ld || rows == 1 || o.rows == 1) return true;
-    const long long r = ((d % ld) + ld) % ld, q = (d - r) / ld;  // o's first run starts at byte r of run q's stride
-    return (r < n && q < rows && -q < o.rows) || (r + o.n > ld && q + 1 < rows && -(q + 1) < o.rows);
+    if (rows > 1 && o.rows > 1 && ld == o.ld) {
+      const long long r = ((d % ld) + ld) % ld, q = (d - r) / ld;  // o's first run starts at byte r of run q's stride
+      return (r < n && q < rows && -q < o.rows) || (r + o.n > ld && q + 1 < rows && -(q + 1) < o.rows);
+    }
+    // run by run of the one with fewer, which only spans that meet come to
+    if (rows < o.rows) return o.meets(*this);
+    for (long long i = 0; i < o.rows; ++i) {
+      const long long e = d + i * o.ld;  // of this, the last run that starts before this one's end
+      const long long last = e + o.n <= 0 ? -1 : (e + o.n - 1) / ld;
+      if (last >= 0 && (last < rows ? last : rows - 1) * ld + n > e) return true;
+    }
+    return false;
   }
 };
+
+ByteRows one_run(const void* at, long long n) { return ByteRows{at, n, 1, n}; }
+// Rows of n elements, ld apart; strides that no memory has are cut where their sums stay in 64 bits.
+ByteRows runs(const void* at, long long n, long long rows, long long ld, int size) {
+  const long long most = (1LL << 60) / (rows * size);
+  return ByteRows{at, n * size, rows, (ld < most ? ld : most) * size};
+}
+
+// No output over an input or another output; a workspace counts as an output.
+int apart_check(const ByteRows* in, int n_in, const ByteRows* out, int n_out, const char* who) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (out[o].meets(in[i])) return fail(CSA2_ERR_UNSUPPORTED, "%s: an output overlaps an input", who);
+    for (int i = 0; i < o; ++i)
+      if (out[o].meets(out[i])) return fail(CSA2_ERR_UNSUPPORTED, "%s: two outputs overlap", who);
+  }
+  return CSA2_OK;
+}
 
 int rows_check(const csa2_rows& r, const char* who) {
   if (r.T < 1 || r.B < 1) return fail(CSA2_ERR_SHAPE, "%s: T=%d and B=%d must be >= 1", who, r.T, r.B);
@@ -677,6 +703,18 @@ int csa2_lora_linear(const csa2_lora_linear_args* a, void* ws, size_t ws_bytes, 
   if (!aligned16(ws)) return fail(CSA2_ERR_ALIGN, "csa2_lora_linear: workspace must be 16-B aligned");
   const size_t need = csa2::lora_workspace_bytes(a->base.T, a->rank);
   if (ws_bytes < need) return fail(CSA2_ERR_WORKSPACE, "csa2_lora_linear: workspace of %zu bytes, %zu needed", ws_bytes, need);
+  const csa2_fp8_linear_args& l = a->base;
+  const long long T = l.T, N = l.N, K = l.K, nb = (K + 127) / 128, n = a->n_adapters, rank = a->rank;
+  const int size = l.out_format == CSA2_OUT_F32 ? 4 : l.out_format == CSA2_OUT_BF16 ? 2 : 1;
+  const ByteRows in[] = {runs(l.x, K, T, l.ld_x, 1), runs(l.x_scale, nb, T, l.ld_x_scale, 4), runs(l.w, K, N, l.ld_w, 1),
+                         runs(l.w_scale, nb, (N + 127) / 128, l.ld_w_scale, 4), one_run(l.rope_head ? l.row_pos : nullptr, T * 4),
+                         one_run(a->row_adapter, T * 4), one_run(a->a, n * rank * K * 2), one_run(a->b, n * rank * N * 2),
+                         one_run(a->adapter_scale, n * 4)};
+  const ByteRows out[] = {runs(l.out, N, T, l.ld_out, size),
+                          runs(l.out_format == CSA2_OUT_FP8 ? l.out_scale : nullptr, N / 128, T, l.ld_out_scale, 4),
+                          one_run(ws, static_cast<long long>(need))};
+  rc = apart_check(in, 9, out, 3, "csa2_lora_linear");
+  if (rc) return rc;
   DeviceCtx ctx;
   cudaError_t e = csa2::device_ctx(&ctx);
   if (e != cudaSuccess) return cuda_fail(e, "csa2_lora_linear: device");
@@ -708,6 +746,14 @@ int csa2_logprobs(const csa2_logprobs_args* a, void* stream) {
   if (!aligned4(a->token) || !aligned4(a->logprob) || !aligned4(a->entropy) || !aligned4(a->lse) || !aligned4(a->top_id) ||
       !aligned4(a->top_logprob))
     return fail(CSA2_ERR_ALIGN, "csa2_logprobs: token and outputs must be 4-B aligned");
+  const long long T = a->T;
+  const int size = a->logits_f32 ? 4 : 2;
+  const ByteRows in[] = {runs(a->logits, a->V, T, a->ld_logits, size)};
+  const ByteRows out[] = {one_run(a->logprob, T * 4), one_run(a->entropy, T * 4), one_run(a->lse, T * 4),
+                          runs(a->n_top ? a->top_id : nullptr, a->n_top, T, a->ld_top, 4),
+                          runs(a->n_top ? a->top_logprob : nullptr, a->n_top, T, a->ld_top, 4)};
+  int rc = apart_check(in, 1, out, 5, "csa2_logprobs");
+  if (rc) return rc;
   DeviceCtx ctx;
   cudaError_t e = csa2::device_ctx(&ctx);
   if (e != cudaSuccess) return cuda_fail(e, "csa2_logprobs: device");
