@@ -93,7 +93,8 @@ __device__ __forceinline__ void write_list(const InnerParams& p, long long t0, i
 }
 
 // Writes v of a row and N ranks from `rank` on, in as many bf16 as there are planes.  An
-// infinite or NaN value is all in the first.
+// infinite or NaN value is all in the first; a finite one past bf16's range keeps bf16's largest
+// there, where rounding to nearest would make it an infinity.
 template <int N>
 __device__ __forceinline__ void store_v(const InnerParams& p, long long row, int rank, float (&v)[N]) {
   uint16_t* to = p.v + row * p.pitch + rank;
@@ -101,7 +102,8 @@ __device__ __forceinline__ void store_v(const InnerParams& p, long long row, int
     alignas(8) uint16_t h[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const __nv_bfloat16 b = __float2bfloat16_rn(v[k]);
+      __nv_bfloat16 b = __float2bfloat16_rn(v[k]);
+      if (__hisinf(b)) b = __float2bfloat16_rz(v[k]);  // of an infinity, itself
       const float rest = v[k] - __bfloat162float(b);
       v[k] = isfinite(rest) ? rest : 0.f;
       h[k] = *reinterpret_cast<const uint16_t*>(&b);

@@ -91,3 +91,29 @@ def test_lora_scales_of_long_shares(T, N, K, R, n, run):
     _sync_ok()
     want, mag, out_mag = _reference(x, xs, a, b, ids, s)
     assert np.all(np.abs(np_(y.double()) - want) <= U * np.abs(want) + (-(-K // 128) + 10) * U * mag + (2 * R + 8) * U * out_mag)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,N,K,R,n", [(8, 512, 384, 16, 4), (64, 20000, 256, 8, 5), (1300, 1000, 2064, 64, 6)])
+def test_lora_inner_products_next_to_the_largest_number(T, N, K, R, n, out):
+    """Between bf16's largest number and fp32's an inner product is finite, and so is the output
+    of a small b; an inner product that leaves fp32 is an infinity in its own rows."""
+    x, xs, w, ws, a, b, ids, s = _inputs(T, N, K, R, n, T + N + R)
+    x[:, 128:], xs[:, 0] = 0, 1.0                # one term: v = a's power of two times the factor
+    sign = torch.where(a > 0, 1.0, -1.0)
+    a = (sign * 2.0 ** 127).to(torch.bfloat16)
+    s = (2.0 - 2.0 ** -10 + 2.0 ** -16 * torch.arange(n, device=x.device)).float()      # 3.401e38 and above
+    b = b * 2.0 ** -20
+    ids[0], ids[1] = 0, n - 1
+    y = torch.empty(T, N, dtype=out, device=x.device)
+    csa2.lora_linear(x, xs, w, ws, a, b, ids, y, adapter_scale=s)
+    _sync_ok()
+    want, _, out_mag = _reference(x, xs, a, b, ids, s)
+    got = np_(y.double())
+    assert np.isfinite(got).all() and np.abs(want).max() > 2.0 ** 107
+    assert np.all(np.abs(got - want) <= torch.finfo(out).eps / 2 * np.abs(want) + (2.0 ** -17 + (2 * R + 8) * U) * out_mag)
+    s[0] = 4.0
+    again = torch.empty_like(y)
+    csa2.lora_linear(x, xs, w, ws, a, b, ids, again, adapter_scale=s)
+    _sync_ok()
+    assert not torch.isfinite(again[ids == 0][:, ::2]).any() and torch.equal(again[ids != 0], y[ids != 0])
