@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(MOST) add_norm_kernel(const __grid_constant__ 
     for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
     top = max8(top);
     const float a = top * inv;
-    // the same in a block's lanes
+    // The same in a block's lanes, but for those behind the last column, whose values are zeros
+    // and have no part in the block: where the block is not usual they go along and write nothing.
     const bool usual = !in || (top >= kLeastTop && top <= kLargest && a >= kAmaxFloor && a <= kLargest);
     auto store_y = [&](float by) {
       float n[16];
@@ -302,7 +303,7 @@ cudaError_t launch_v(const csa2_add_norm_fp8_args& a, const AddNormParams& p, cu
 
 }  // namespace
 
-cudaError_t launch_add_norm_fp8(const csa2_add_norm_fp8_args& a, cudaStream_t st) {
+cudaError_t launch_add_norm_fp8(const csa2_add_norm_fp8_args& a, const DeviceCtx& ctx, cudaStream_t st) {
   const AddNormParams p{reinterpret_cast<const __nv_bfloat16*>(a.x), a.residual, a.residual_out, a.gamma, a.codes, a.scale,
                         reinterpret_cast<__nv_bfloat16*>(a.y), a.ld_x, a.ld_residual, a.ld_residual_out, a.ld_codes,
                         a.ld_scale, a.ld_y, a.T, a.K, a.eps};
@@ -312,7 +313,7 @@ cudaError_t launch_add_norm_fp8(const csa2_add_norm_fp8_args& a, cudaStream_t st
   // too few warps (2,048 x 16,384: 53.9 us, 48.0 with two).
   if (a.K <= 4096) return launch_v<1, 256>(a, p, st);
   if (a.K > 8192) return launch_v<2, 512>(a, p, st);
-  return a.T <= 304 ? launch_v<1, 512>(a, p, st) : launch_v<2, 256>(a, p, st);
+  return a.T <= 2 * ctx.num_sms ? launch_v<1, 512>(a, p, st) : launch_v<2, 256>(a, p, st);
 }
 
 }  // namespace csa2

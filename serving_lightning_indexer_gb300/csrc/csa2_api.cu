@@ -690,7 +690,10 @@ int csa2_add_norm_fp8(const csa2_add_norm_fp8_args* a, void* stream) {
     for (int i = 0; i < o; ++i)
       if (out[o].meets(out[i])) return fail(CSA2_ERR_UNSUPPORTED, "csa2_add_norm_fp8: two outputs overlap");
   }
-  cudaError_t e = csa2::launch_add_norm_fp8(*a, static_cast<cudaStream_t>(stream));
+  DeviceCtx ctx;
+  cudaError_t e = csa2::device_ctx(&ctx);
+  if (e != cudaSuccess) return cuda_fail(e, "csa2_add_norm_fp8: device");
+  e = csa2::launch_add_norm_fp8(*a, ctx, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "csa2_add_norm_fp8: launch");
   return CSA2_OK;
 }

@@ -199,7 +199,7 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
 cudaError_t launch_lora_linear(const csa2_lora_linear_args& a, void* ws, const DeviceCtx& ctx, cudaStream_t st,
                                const char** why);
 // The residual's addition, RMSNorm and e4m3 codes.
-cudaError_t launch_add_norm_fp8(const csa2_add_norm_fp8_args& a, cudaStream_t st);
+cudaError_t launch_add_norm_fp8(const csa2_add_norm_fp8_args& a, const DeviceCtx& ctx, cudaStream_t st);
 // Log probabilities, entropy and top alternatives of rows of logits.
 cudaError_t launch_logprobs(const csa2_logprobs_args& a, const DeviceCtx& ctx, cudaStream_t st);
 // Rows, pages and slots of a batch from its sequences' lengths.
