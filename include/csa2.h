@@ -515,7 +515,10 @@ CSA2_API int csa2_batch_plan(const csa2_batch_plan_args* args, void* stream);
  * row stride); apart from that no output may overlap an input or another output,
  * which the call checks by the rows' places.  Rows t < T and columns k < K are
  * written and nothing else.  The row's sum of squares is held in fp32; where it
- * passes that range (from magnitudes of 2^57 on) y is zeros.  K is a multiple of 16,
+ * passes that range (from magnitudes of 2^57 on) y is zeros; with eps = 0 y loses digits
+ * where all of a row is below 2^-63, and is infinite or NaN below 2^-75.  In a block whose
+ * largest |r * gamma| is at least 2^-80 y is the fp32 product r * gamma over the root: one
+ * below 2^-126 keeps its absolute error, not its digits.  K is a multiple of 16,
  * at most 16384.  Alignment: x, residual, residual_out, codes, y, gamma 16 B; row
  * strides multiples of 16 B and below 2^29; scale 4 B.  No workspace. */
 typedef struct {
@@ -546,7 +549,9 @@ CSA2_API int csa2_add_norm_fp8(const csa2_add_norm_fp8_args* args, void* stream)
  * base: the arguments of csa2_fp8_linear, with its rules; T at most 2^20; w_ready = 1
  * says the same of a, b, adapter_scale and row_adapter as of w and w_scale.  rank is
  * a multiple of 8, at most 128; n_adapters >= 1, n_adapters * N and n_adapters * rank at
- * most 2^30.  An adapter of a smaller rank is padded with zeros.  Alignment: a, b 16 B;
+ * most 2^30.  An adapter of a smaller rank is padded with zeros (and costs what its rank
+ * is padded to); all of a call are in one a and one b, so a server that loads and drops
+ * adapters keeps them in fixed places there.  Alignment: a, b 16 B;
  * row_adapter, adapter_scale 4 B; workspace 16 B: csa2_workspace_size(
  * CSA2_CALL_LORA_LINEAR, args, &bytes), read and written until the call's work is done,
  * so calls that may run at the same time need one each.  No output, nor the workspace,

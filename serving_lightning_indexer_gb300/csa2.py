@@ -536,7 +536,8 @@ def lora_linear(x, x_scale, w, w_scale, a, b, row_adapter, out, adapter_scale=No
     """fp8_linear with the low-rank adapters of many requests beside it: a [n,rank,K] and
     b [n,N,rank] bf16, adapter_scale [n] fp32 (None: 1), row_adapter [T] int32, -1 for a row
     without one.  Row t of an adapter i gets adapter_scale[i] * (x[t] a[i]^T) b[i]^T added
-    before RoPE and rounding (csa2_lora_linear).  ws: a uint8 tensor of at least
+    before RoPE and rounding (csa2_lora_linear).  w_ready=True says of a, b, adapter_scale
+    and row_adapter too that nothing in flight writes them.  ws: a uint8 tensor of at least
     lora_workspace_size(T, rank) bytes that nothing else uses until the call's work is
     done; None takes one from torch's allocator, on the call's stream."""
     rc = (_call or _load_call()).lora_linear(x, x_scale, w, w_scale, a, b, row_adapter, out, adapter_scale, out_scale, row_pos,

@@ -13,8 +13,8 @@
 // every 64 or 32 ranks, whichever fit a stage: bf16 products of the parts of the rows' v with
 // the adapter's b, summed like the others but only to the rows that have the adapter.  The
 // projection's own blocks come first, and only what lora.cu wrote waits for it.  4,096 x
-// 2,048 x 32,768 with 4 adapters of rank 64: 287 us, 249 without adapters (an adapter takes two
-// blocks there); 64 rows with 16 of rank 32: 25.6 us, 16.2 without adapters, and b's bytes are 5 more.
+// 2,048 x 32,768 with 4 adapters of rank 64: 292 us, 236 without adapters (an adapter takes two
+// blocks there); 64 rows with 16 of rank 32: 25.7 us, 16.1 without adapters, and b's bytes are 5 more.
 #include <cuda_bf16.h>
 #include <string.h>
 

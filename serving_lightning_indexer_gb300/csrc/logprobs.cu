@@ -671,8 +671,10 @@ cudaError_t launch_type(const LogprobParams& p, int T, const DeviceCtx& ctx, cud
   if (splits == 8 && T * kMaxSplits <= ctx.num_sms && p.V / kMaxSplits >= 2048) splits = kMaxSplits;
   if (splits > 1) return launch<F32, TOP, kLpWarps, false, true>(p, T, splits, ctx, st);
   // With an SM or half of one to itself a whole row's CTA needs more bytes on their way
-  // (128 rows of 131,072 fp32 logits: 16.9 us, 26 with two stages; 512 rows, where the
-  // larger ring leaves fewer CTAs an SM: 58 and 46).
+  // (rows of 131,072 fp32 logits, 128 of them: 16.9 us, 26 with two stages), but the larger
+  // ring leaves fewer CTAs an SM (512: 58 and 46).  Between them the SMs' uneven shares of rows
+  // decide, with 5 alternatives: 250 rows 29.4 and 30.5, 304 35.9 and 32.5, 333 37.6 and 34.5,
+  // 400 41.1 and 46.8, 512 56.7 and 54.2.
   if constexpr (F32)
     if (T <= 2 * ctx.num_sms) return launch<F32, TOP, kLpWarps, true, false>(p, T, 1, ctx, st);
   return launch<F32, TOP, kLpWarps, false, false>(p, T, 1, ctx, st);

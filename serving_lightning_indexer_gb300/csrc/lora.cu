@@ -15,7 +15,7 @@
 // blocks of 128 input dims in turn, added in warp order: 8 x 7,168 x 512 with 8 adapters
 // takes 8.4 us with its projection, 4.7 without adapters.  For many a CTA takes 128 rows,
 // 64 ranks and a share of the input dims, and goes through the tile's adapters with a in a
-// ring in shared memory; a cluster adds the shares in rank order: about 12 us of the 287 of
+// ring in shared memory; a cluster adds the shares in rank order: about 12 us of the 292 of
 // 4,096 x 2,048 x 32,768 at rank 64.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -241,7 +241,7 @@ constexpr int kTileSmem = 1024 + kTileOffScales + kTileScales * kTileRows * 4;
 // slot z takes the tile's adapters z, z + slots, ..  map_a: a as rows of K, boxes of 64
 // dims by `box` ranks (a run's, in sixteens).  G adapters of 16 or 32 ranks share a
 // product, 64 columns wide, as its columns have nothing to do with each other (1,024 x
-// 7,168 x 512 with 16 adapters of rank 16, all in each tile: 83 us with one, 41 with four).
+// 7,168 x 512 with 16 adapters of rank 16, all in each tile: 83 us with one, 43 with four).
 __global__ void __launch_bounds__(kTileWarps * 32, 1)
     lora_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ InnerParams p, int slots, int box,
                      int stages) {
@@ -548,7 +548,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
 
 }  // namespace
 
-// The lists, kLoraListWords for each 128 rows, in 80 bytes for each 16.
+// The lists, kLoraListWords for each tile of 128 rows, in 80 bytes for each 16 rows (640 for 528):
+// tiles of fewer rows, whose lists are in shared memory, would have room for theirs too.
 static size_t lists_offset(int T, int rank) {
   return (2 * kLoraPlanes * static_cast<size_t>(T) * lora_pitch(rank) + 255) & ~static_cast<size_t>(255);
 }
@@ -571,8 +572,8 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
   const int tiles = (l.T + kTileRows - 1) / kTileRows, runs = (a.rank + kTileRanks - 1) / kTileRanks, blocks = (l.K + 127) / 128;
   // The tiles' CTAs, one an SM: shares of the input dims, then of the adapters.  If the SMs
   // that the projection's CTAs leave hold those of a slot, not more than they: the two
-  // launches run side by side (64 x 2,048 x 32,768 with 16 of rank 64: 29.7 us, 35.6 on all;
-  // 200 x 7,168 x 512: 28.7 and 35.2).
+  // launches run side by side (64 x 2,048 x 32,768 with 16 of rank 64: 32.1 us, 37.1 on all;
+  // 200 x 7,168 x 512: 30.2 and 36.5).
   int splits = ctx.num_sms / (tiles * runs);
   splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
   if (splits > blocks) splits = blocks;
@@ -584,11 +585,12 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
   slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
   // The small CTAs while they, by the most adapters that 16 rows can have, and their blocks
   // are few (the projection's time counted in): 333 x 1,360 x 1,001 with 5 of rank 24 take
-  // 10.5 us, 13.2 with the tiles; 64 x 4,096 x 8,192 with 16 of rank 80: 38 and 53; 200 x
-  // 2,048 x 4,096 with 16 of rank 64: 26.2 and 24.0; 96 x 7,168 x 512 with 16 of rank 48: 23.4
-  // and 21.0.  But not where the tiles' take no longer, at half a microsecond a product and
-  // 10 more, than the projection beside them (its weights at 4.2 TB/s): 128 x 2,048 x 32,768
-  // with 16 of rank 32 take 25.1 us with them and 29.0; 64 rows of rank 128: 50 and 40.
+  // 11.0 us, 13.2 with the tiles; 64 x 4,096 x 8,192 with 16 of rank 80: 40 and 57; 200 x
+  // 2,048 x 4,096 with 16 of rank 64: 34.6 and 32.4; 96 x 7,168 x 512 with 16 of rank 48: 25.3
+  // and 21.7 (but 200 rows with 16 of rank 16: 24.5 and 19.0).  But not where the tiles' take no
+  // longer, at half a microsecond a product and 10 more, than the projection beside them (its
+  // weights at 4.2 TB/s): 128 x 2,048 x 32,768 with 16 of rank 32 take 26.6 us with them and
+  // 30.0; 64 rows of rank 128: 54 and 43.
   // 8 ranks without a partner get 8 zeros beside them: products are of 16.
   const dim3 grid((l.T + 15) / 16, (a.rank + 15) / 16 * 2, a.n_adapters < 16 ? a.n_adapters : 16);
   const long long small = static_cast<long long>(grid.x) * grid.y * grid.z;
@@ -596,8 +598,8 @@ cudaError_t launch_lora_inner(const csa2_lora_linear_args& a, const LoraInner& t
   const bool beside = tiles * runs * splits <= left && 20 + products <= (static_cast<long long>(l.N) * l.K) >> 21;
   if (!beside && small * (blocks + 8) <= 190LL * ctx.num_sms) {
     // Up to 16 blocks, 8 warps where 16 would be more than an SM's two CTAs (333 x 1,360 x
-    // 1,001: 11.4 and 11.8 us; 256 rows of K = 1,024: 8.7 and 9.2); above, 32 (400 x 7,168 x
-    // 512 with 8 of rank 16: 26.4 us, 34.2 with 8).
+    // 1,001: 11.0 and 11.6 us); above, 32 (8 x 7,168 x 512 with 8 of rank 16: 8.5 us, 10.5 with 16,
+    // 14.1 with 8; 400 rows: 26.6, 24.4 and 34.4).
     if (blocks <= 16 && small > 2 * ctx.num_sms) return launch_pdl(lora_inner_kernel<8>, grid, dim3(256), 0, st, p);
     return blocks > 16 ? launch_pdl(lora_inner_kernel<32>, grid, dim3(1024), 0, st, p)
                        : launch_pdl(lora_inner_kernel<16>, grid, dim3(512), 0, st, p);
