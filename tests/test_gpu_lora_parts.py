@@ -59,6 +59,7 @@ def _reference(x, xs, a, b, ids, s):
     (1, 130, 16, 8, 1), (8, 512, 384, 16, 8), (8, 512, 384, 64, 8), (16, 1001, 272, 128, 5), (24, 640, 384, 64, 4), (32, 384, 144, 104, 9),
     (48, 256, 384, 40, 5), (64, 512, 2048, 72, 6),                                  # tiles of up to 64 rows
     (40, 20000, 256, 64, 16), (64, 20001, 272, 24, 7), (33, 19584, 144, 128, 3), (64, 19712, 384, 8, 12),   # up to 64 rows of 128
+    (40, 12700, 4096, 64, 3), (64, 12700, 4096, 40, 5),                             # the same, two CTAs a tile
     (65, 20000, 144, 64, 4), (500, 300, 272, 56, 60), (1300, 1000, 2064, 64, 6), (1300, 1001, 2064, 16, 30), (2700, 2001, 400, 72, 4)])
 def test_lora_output_has_the_inner_products_bits(T, N, K, R, n, out):
     x, xs, w, ws, a, b, ids, s = _inputs(T, N, K, R, n, T + N + R)
